@@ -230,6 +230,22 @@ int xt_rope_fwd(const void* x, void* y, const float* table, int B, int S, int H,
 int xt_rope_bwd(const void* d, void* dx, const float* table, int B, int S, int H, int hd,
                 int64_t ld, int dt, int acc, void* stream);
 
+/* RoPE over several axes: positions are given per token and per axis (time, height and width of a
+ * patch; one axis: positions that restart with each document of a packed row).  pos is int32
+ * [n_axes][T] (1 to 4 axes), sections a HOST array of n_axes pair counts adding up to hd/2: the
+ * pairs i = 0 .. hd/2 − 1 belong to the axes in order.  θ = pos[axis(i)][t]·f_i with
+ * f_i = base^(−2i/hd) (per_axis = 0), or base^(−k/sections[a]) for pair k of axis a (per_axis = 1);
+ * the rotation and its backward are xt_rope_fwd's.  Angles are reduced exactly (integer arithmetic
+ * modulo a turn), so any int32 position is as accurate as position 0.  Token t, head h lives at
+ * x + t·ld_x + h·hd (y + t·ld_y + h·hd); x and y may be one buffer with one stride (in place), except
+ * with acc = 1.  hd even and at most 256 (else XT_ERR_INVALID_ARG / XT_ERR_UNSUPPORTED). */
+int xt_rope_axes_fwd(const void* x, int64_t ld_x, void* y, int64_t ld_y, const int32_t* pos, int n_axes,
+                     const int32_t* sections, int per_axis, double base, int64_t T, int H, int hd, int dt,
+                     void* stream);
+int xt_rope_axes_bwd(const void* d, int64_t ld_d, void* dx, int64_t ld_dx, const int32_t* pos, int n_axes,
+                     const int32_t* sections, int per_axis, double base, int64_t T, int H, int hd, int dt, int acc,
+                     void* stream);
+
 /* ---------------------------------------------------------------------------------
  * Row-wise safe softmax ([AE] op table row softmax and § Softmax 反向推导):
  * y = exp(x − max)/Σ exp(x − max); dx = y∘(d − Σ_c d∘y).
@@ -513,6 +529,32 @@ int xt_adamw_workspace_size(int n, const int64_t* numel, size_t* bytes);
 int xt_adamw_step(const xt_adamw_config* cfg, int n, float* const* param, const float* const* grad, float* const* m,
                   float* const* v, void* const* shadow, int shadow_dtype, const int64_t* numel, float* norm_out,
                   void* ws, size_t ws_bytes, void* stream);
+
+/* The same step with both moments held in 8 bits (2 bytes and 2/64 of state per weight instead of 8).
+ * 256 consecutive elements of a tensor share one float32 scale for each moment (xt_adamw8_scales(numel)
+ * = ceil(numel / 256) of them per tensor): m = m_scale·c·|c| with c the int8 code, √v = r_scale·c² with c
+ * the uint8 code.  A step decodes m and v, forms
+ *   g' = f·g,  m' = β₁ m + (1−β₁) g',  v' = β₂ v + ((1−β₂) g')·g',
+ * each operation rounded to float32 by itself (f: grad_scale·c of xt_adamw_step, c from the norm taken in
+ * 64-bit accuracy), updates θ from m' and v' as xt_adamw_step does, and codes them again:
+ *   m_scale = max|m'|/127², c = sign(m')·rint(√(|m'|/m_scale)), r_scale = √(max v')/255²,
+ *   c = rint(√(√v'/r_scale)), but at least 1 where v' > 0,
+ * so the codes are defined to the last bit.  State of zeros (codes and scales) is the state before the first
+ * step.  A block with a gradient that is not finite ends with scales that decode to NaN (its θ is NaN too).
+ * Arguments as for xt_adamw_step, with m_code, r_code, m_scale and r_scale HOST arrays of device pointers.
+ * The workspace (xt_adamw8_workspace_size, 8-byte aligned) is needed when clipping or norm_out is
+ * requested; its contents on entry do not matter.  Deterministic.
+ * xt_adamw8_decode writes the float32 moments that the codes stand for (m, v: HOST arrays whose entries,
+ * or which themselves, may be NULL). */
+int xt_adamw8_scales(int64_t numel, int64_t* count);
+int xt_adamw8_workspace_size(int n, const int64_t* numel, size_t* bytes);
+int xt_adamw8_step(const xt_adamw_config* cfg, int n, float* const* param, const float* const* grad,
+                   int8_t* const* m_code, uint8_t* const* r_code, float* const* m_scale, float* const* r_scale,
+                   void* const* shadow, int shadow_dtype, const int64_t* numel, float* norm_out, void* ws,
+                   size_t ws_bytes, void* stream);
+int xt_adamw8_decode(int n, const int8_t* const* m_code, const uint8_t* const* r_code, const float* const* m_scale,
+                     const float* const* r_scale, float* const* m, float* const* v, const int64_t* numel,
+                     void* stream);
 
 /* ---------------------------------------------------------------------------------
  * Native block stack ([BP] § Framåtgåendet; [DO] § dropout 接在哪（wiring）):

@@ -1,0 +1,82 @@
+"""Arguments that the operators of packed-document training refuse, on the host: every refusal comes before
+anything touches a device."""
+import ctypes as C
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def xt():
+    from transformer_fwd_bwd_gb300 import build
+    build.build()
+    from transformer_fwd_bwd_gb300 import xt as m
+    m.lib()
+    return m
+
+
+def rope(xt, x=16, ld_x=64, y=32, ld_y=64, pos=16, axes=2, sections=(8, 24), per_axis=0, base=1e4, T=4, H=1, hd=64, dt=0,
+         acc=None):
+    sec = (C.c_int32 * max(1, len(sections)))(*sections) if sections is not None else None
+    args = [x, ld_x, y, ld_y, pos, axes, sec, per_axis, C.c_double(base), T, H, hd, dt]
+    if acc is None:
+        return xt.lib().xt_rope_axes_fwd(*args, None)
+    return xt.lib().xt_rope_axes_bwd(*args, acc, None)
+
+
+def test_rope_axes_refusals(xt):
+    bad = xt.XT_ERR_INVALID_ARG
+    assert rope(xt, dt=2) == bad
+    assert rope(xt, hd=63) == bad
+    assert rope(xt, hd=258, ld_x=258, ld_y=258, sections=(64, 65)) == xt.XT_ERR_UNSUPPORTED
+    assert rope(xt, axes=0) == bad and rope(xt, axes=5, sections=(8, 8, 8, 4, 4)) == bad
+    assert rope(xt, sections=(8, 23)) == bad and b"add up" in xt.lib().xt_last_error()
+    assert rope(xt, sections=(-8, 40)) == bad
+    assert rope(xt, sections=None) == bad
+    assert rope(xt, base=0.0) == bad and rope(xt, base=float("nan")) == bad
+    assert rope(xt, per_axis=2) == bad
+    assert rope(xt, ld_x=63) == bad and rope(xt, ld_y=63) == bad
+    assert rope(xt, T=-1) == bad and rope(xt, H=0) == bad
+    assert rope(xt, x=None) == bad and rope(xt, y=None) == bad and rope(xt, pos=None) == bad
+    assert rope(xt, x=16, y=16, ld_x=64, ld_y=128) == bad
+    assert rope(xt, acc=2) == bad and rope(xt, acc=1, x=16, y=16) == bad
+    assert rope(xt, T=0, x=None, y=None, pos=None) == xt.XT_OK
+    with pytest.raises(ValueError):   # positions of another shape
+        xt.xt_rope_axes_fwd(torch.zeros(4, 64), torch.zeros(4, 64), torch.zeros(1, 4, dtype=torch.int32), [8, 24], 1, 64)
+    with pytest.raises(ValueError):   # not on a GPU
+        xt.xt_rope_axes_fwd(torch.zeros(4, 64), torch.zeros(4, 64), torch.zeros(2, 4, dtype=torch.int32), [8, 24], 1, 64)
+
+
+def adamw8(xt, n=1, numel=(1000,), ws=8, ws_bytes=1 << 20, shadow_dtype=0, null=None, **kw):
+    cfg = xt.adamw_config(**{**dict(lr=1e-3, max_grad_norm=1.0), **kw})
+    N = (C.c_int64 * max(1, len(numel)))(*numel)
+    lists = [(C.c_void_p * max(1, len(numel)))(*([16] * len(numel))) for _ in range(7)]
+    if null is not None:
+        lists[null][0] = None
+    return xt.lib().xt_adamw8_step(C.byref(cfg), n, *lists[:6], lists[6], shadow_dtype, N, None, ws, ws_bytes, None)
+
+
+def test_adamw8_refusals(xt):
+    bad = xt.XT_ERR_INVALID_ARG
+    L = xt.lib()
+    assert L.xt_adamw8_step(None, 0, *[None] * 7, 0, None, None, None, 0, None) == bad
+    assert adamw8(xt, n=-1) == bad
+    assert adamw8(xt, numel=(-5,)) == bad
+    assert adamw8(xt, step=0) == bad
+    assert adamw8(xt, beta1=1.0) == bad and adamw8(xt, beta2=-0.1) == bad
+    assert adamw8(xt, eps=0.0) == bad and adamw8(xt, lr=-1.0) == bad and adamw8(xt, weight_decay=-1.0) == bad
+    assert adamw8(xt, shadow_dtype=3) == bad
+    for i in range(6):
+        assert adamw8(xt, null=i) == bad
+    assert adamw8(xt, ws=None) == bad and adamw8(xt, ws_bytes=4) == bad
+    assert adamw8(xt, ws=12) == xt.XT_ERR_ALIGNMENT
+    assert adamw8(xt, n=0, numel=()) == xt.XT_OK
+    n = C.c_int64(0)
+    assert [L.xt_adamw8_scales(k, C.byref(n)) or n.value for k in (0, 1, 256, 257)] == [0, 1, 1, 2]
+    assert L.xt_adamw8_scales(-1, C.byref(n)) == bad
+    assert L.xt_adamw8_workspace_size(1, None, C.byref(C.c_size_t())) == bad
+    assert L.xt_adamw8_decode(1, None, None, None, None, None, None, (C.c_int64 * 1)(4), None) == bad
+    with pytest.raises(ValueError):   # lists of different lengths
+        xt.xt_adamw8_step(xt.adamw_config(1e-3), [], [torch.zeros(1)], [], [], [], [])
+    with pytest.raises(ValueError):   # not on a GPU
+        xt.xt_adamw8_step(xt.adamw_config(1e-3), [torch.zeros(1)], [torch.zeros(1)], [], [], [], [])

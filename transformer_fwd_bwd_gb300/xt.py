@@ -107,6 +107,8 @@ _SIGS = {
     "xt_rope_table": [_VP, _I, _I, _D, _I, _VP],
     "xt_rope_fwd": [_VP, _VP, _VP, _I, _I, _I, _I, _I64, _I, _VP],
     "xt_rope_bwd": [_VP, _VP, _VP, _I, _I, _I, _I, _I64, _I, _I, _VP],
+    "xt_rope_axes_fwd": [_VP, _I64, _VP, _I64, _VP, _I, _VP, _I, _D, _I64, _I, _I, _I, _VP],
+    "xt_rope_axes_bwd": [_VP, _I64, _VP, _I64, _VP, _I, _VP, _I, _D, _I64, _I, _I, _I, _I, _VP],
     "xt_softmax_fwd": [_VP, _VP, _I64, _I64, _I, _I64, _I, _VP],
     "xt_dropout_add_norm_fwd": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _F, _U64, _I, _I, _F, _I, _VP],
     "xt_norm_bwd_dropout": [_I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I, _I, _VP, _I, _I, _F,
@@ -144,6 +146,11 @@ _SIGS = {
     "xt_adamw_step": [C.POINTER(AdamWConfig), _I, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
                       C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), _I,
                       C.POINTER(C.c_int64), _VP, _VP, C.c_size_t, _VP],
+    "xt_adamw8_scales": [_I64, C.POINTER(C.c_int64)],
+    "xt_adamw8_workspace_size": [_I, C.POINTER(C.c_int64), _SZP],
+    "xt_adamw8_step": [C.POINTER(AdamWConfig), _I, _PP, _PP, _PP, _PP, _PP, _PP, _PP, _I, C.POINTER(C.c_int64), _VP,
+                       _VP, C.c_size_t, _VP],
+    "xt_adamw8_decode": [_I, _PP, _PP, _PP, _PP, _PP, _PP, C.POINTER(C.c_int64), _VP],
     "xt_matmul_fwd": [C.POINTER(MatmulDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
     "xt_matmul_gelu_fwd": [C.POINTER(MatmulDesc), _VP, _VP, _VP, _VP, _VP, C.c_size_t, _VP],
     "xt_matmul_gelu_bwd": [C.POINTER(MatmulDesc), _VP, _VP, _VP, _VP, _VP, C.c_size_t, _VP],
@@ -470,6 +477,30 @@ def xt_rope_bwd(d, dx, table, B, S, H, hd, ld, acc=0, s=None):
     call("xt_rope_bwd", ptr(d, False), ptr(dx, False), ptr(table), B, S, H, hd, ld, dt(d), acc, stream(s))
 
 
+def _rope_axes(name, x, y, pos, sections, H, hd, base, per_axis, acc, s):
+    if x.dtype != y.dtype or x.dim() != 2 or y.shape[0] != x.shape[0]:
+        raise ValueError("x and y are [T, >= H*hd] tensors of one dtype")
+    if x.shape[1] < H * hd or y.shape[1] < H * hd or (x.numel() and (x.stride(1) != 1 or y.stride(1) != 1)):
+        raise ValueError("x and y need unit column stride and H*hd columns")
+    if pos.dtype != torch.int32 or tuple(pos.shape) != (len(sections), x.shape[0]):
+        raise ValueError("pos must be int32 [len(sections), T]")
+    T = x.shape[0]
+    sec = (C.c_int32 * max(1, len(sections)))(*sections)
+    ld = lambda t: t.stride(0) if T > 1 else max(t.stride(0), H * hd)  # noqa: E731
+    call(name, ptr(x, False), ld(x), ptr(y, False), ld(y), ptr(pos), len(sections), sec, int(per_axis), float(base), T,
+         H, hd, dt(x), *acc, stream(s))
+
+
+def xt_rope_axes_fwd(x, y, pos, sections, H, hd, base=10000.0, per_axis=0, s=None):
+    """Rotates the first H·hd columns of x [T, ≥ H·hd] into y; pos int32 [axes, T]; sections: pairs of each
+    axis, adding up to hd/2."""
+    _rope_axes("xt_rope_axes_fwd", x, y, pos, sections, H, hd, base, per_axis, (), s)
+
+
+def xt_rope_axes_bwd(d, dx, pos, sections, H, hd, base=10000.0, per_axis=0, acc=0, s=None):
+    _rope_axes("xt_rope_axes_bwd", d, dx, pos, sections, H, hd, base, per_axis, (int(acc),), s)
+
+
 def xt_softmax_fwd(x, y, causal=0, q_len=0, s=None):
     cols = x.shape[-1]
     rows = x.numel() // cols
@@ -633,6 +664,89 @@ def xt_adamw_step(cfg, params, grads, m, v, shadows=None, norm_out=None, ws=None
         ws = adamw_workspace(numel, params[0].device)
     call("xt_adamw_step", C.byref(cfg), n, P, G, M, V, SH, sdt, N, ptr(norm_out), ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
+
+
+def adamw8_scales(numel: int) -> int:
+    """Scales (float32, for each moment) of a tensor of numel elements."""
+    n = C.c_int64(0)
+    call("xt_adamw8_scales", int(numel), C.byref(n))
+    return int(n.value)
+
+
+def adamw8_state(params):
+    """Zero state of the 8-bit step for a list of tensors: (m codes, r codes, m scales, r scales)."""
+    def new(p, dtype, n):
+        return torch.zeros(n, dtype=dtype, device=p.device)
+    return ([new(p, torch.int8, p.numel()) for p in params], [new(p, torch.uint8, p.numel()) for p in params],
+            [new(p, torch.float32, adamw8_scales(p.numel())) for p in params],
+            [new(p, torch.float32, adamw8_scales(p.numel())) for p in params])
+
+
+def adamw8_workspace(numels, device="cuda"):
+    arr = (C.c_int64 * max(1, len(numels)))(*numels)
+    return workspace(ws_bytes("xt_adamw8_workspace_size", len(numels), arr), device)
+
+
+def _ptrs(tensors):
+    return (C.c_void_p * max(1, len(tensors)))(*[t.data_ptr() if t is not None else None for t in tensors])
+
+
+def _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale):
+    if not (len(m_code) == len(r_code) == len(m_scale) == len(r_scale) == n):
+        raise ValueError("the lists must have the same length")
+    for lst, dtype in ((m_code, torch.int8), (r_code, torch.uint8), (m_scale, torch.float32), (r_scale, torch.float32)):
+        scales = dtype == torch.float32
+        for t, k in zip(lst, numel):
+            if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError("codes are contiguous int8 (m) and uint8 (r), scales float32 CUDA tensors")
+            if t.numel() != (adamw8_scales(k) if scales else k):
+                raise ValueError("code and scale sizes must match the tensors")
+
+
+def xt_adamw8_step(cfg, params, grads, m_code, r_code, m_scale, r_scale, shadows=None, norm_out=None, ws=None, s=None):
+    """One AdamW step with the moments in 8 bits over lists of float32 tensors (see adamw8_state; params and
+    the state are updated in place); shadows, norm_out as for xt_adamw_step."""
+    n = len(params)
+    if len(grads) != n:
+        raise ValueError("params and grads must have the same length")
+    for t in list(params) + list(grads):
+        if t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError("params and grads must be contiguous float32 CUDA tensors")
+    numel = [t.numel() for t in params]
+    if [t.numel() for t in grads] != numel:
+        raise ValueError("tensor sizes differ")
+    _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale)
+    sh, sdt = None, XT_F32
+    if shadows is not None:
+        dts = {t.dtype for t in shadows if t is not None}
+        if len(dts) > 1 or len(shadows) != n:
+            raise ValueError("shadows must share one dtype, one entry for each tensor")
+        for t, k in zip(shadows, numel):
+            if t is not None and (t.numel() != k or not t.is_contiguous()):
+                raise ValueError("shadow shapes must match params")
+        sdt = next((dt(t) for t in shadows if t is not None), XT_F32)
+        sh = _ptrs(shadows)
+    N = (C.c_int64 * max(1, n))(*numel)
+    if ws is None and n and (cfg.max_grad_norm > 0 or norm_out is not None):
+        ws = adamw8_workspace(numel, params[0].device)
+    call("xt_adamw8_step", C.byref(cfg), n, _ptrs(params), _ptrs(grads), _ptrs(m_code), _ptrs(r_code), _ptrs(m_scale),
+         _ptrs(r_scale), sh, sdt, N, ptr(norm_out), ptr(ws), ws.numel() if ws is not None else 0, stream(s))
+
+
+def xt_adamw8_decode(m_code, r_code, m_scale, r_scale, m=None, v=None, s=None):
+    """The float32 moments that the codes stand for, into lists m and v (either may be None)."""
+    numel = [t.numel() for t in m_code]
+    n = len(numel)
+    _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale)
+    for lst in (m, v):
+        if lst is None:
+            continue
+        if len(lst) != n or any(t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != k
+                                for t, k in zip(lst, numel)):
+            raise ValueError("m and v must be contiguous float32 tensors of the codes' sizes")
+    N = (C.c_int64 * max(1, n))(*numel)
+    call("xt_adamw8_decode", n, _ptrs(m_code), _ptrs(r_code), _ptrs(m_scale), _ptrs(r_scale),
+         _ptrs(m) if m is not None else None, _ptrs(v) if v is not None else None, N, stream(s))
 
 
 def xt_quantize_fp8(x, out, dequant, ws=None, s=None):
