@@ -62,6 +62,7 @@ typedef enum { XT_F32 = 0, XT_BF16 = 1 } xt_dtype;
 /* device error flag bits */
 #define XT_DEVERR_INDEX 1u   /* a token id or target outside [0, V) */
 #define XT_DEVERR_TIMEOUT 2u /* a bounded mbarrier wait in a GEMM gave up */
+#define XT_DEVERR_PLAN 4u    /* masked attention was given a plan that was not made for its T */
 
 const char* xt_last_error(void);
 const char* xt_version(void);
@@ -288,6 +289,58 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
                      const void* o_lo, const void* d_o, int64_t ld_o, const float* lse, void* dq, void* dk,
                      void* dv, int64_t ld_dqkv, void* ws, size_t ws_bytes, int B, int S, int H, int hd,
                      int causal, int dt, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Masked attention over packed documents, forward and backward: for training on rows that hold several
+ * texts or images.  T tokens; query head h reads key / value head h / (H / Hkv) (Hkv divides H):
+ *   a_ij = scale·q_i·k_j,  c = cap·tanh(a/cap) (cap > 0; else a),  s = c − slopes[h]·|i − j| (slopes != NULL),
+ *   P = softmax of s_i over the keys that i sees,  O = P V,  lse_i = log Σ exp s_ij;
+ *   D_i = dO_i·O_i,  dS = P∘(dO Vᵀ − D)∘(1 − tanh²),  dQ = scale·dS K,  dK = scale·dSᵀ Q,  dV = Pᵀ dO
+ *   (dK and dV are sums over the query heads that share them; slopes are constants).
+ * What i sees is the plan's: keys of its own document's valid tokens, with causal = 1 only those at or
+ * before i and those of the document's prefix.  A token outside every document's valid part sees nothing and
+ * is not seen: O = 0, lse = −∞, gradients 0; its rows of q, k, v, o and d_o may hold anything.  NaN or ∞ in a
+ * token reaches only the rows that see it.
+ *
+ * xt_attention_plan makes the plan of a batch, which every layer's forward and backward then use:
+ *   doc_off  int32 [n_docs + 1], ascending token offsets; document d spans [doc_off[d], doc_off[d+1]).  NULL:
+ *            n_docs spans of T / n_docs tokens (T a multiple of n_docs).
+ *   doc_len  int32 [n_docs], tokens of the span that count (the rest is padding); NULL: all.
+ *   prefix   int32 [n_docs], leading tokens that every token of the document sees (causal = 1; more than the
+ *            document has means all); NULL: none.
+ * plan: xt_attention_plan_size(T) bytes, 16-byte aligned, a function of these arrays' values when the call
+ * runs.  Offsets that fall or leave [0, T], lengths outside the span and negative prefixes set
+ * XT_DEVERR_INDEX; no access depends on them.  A plan made for another T sets XT_DEVERR_PLAN and the
+ * attention call writes nothing.
+ *
+ * Layout: token t of q is row t (ld_q elements apart), its head h columns [h·hd, h·hd + hd); k, v likewise
+ * with Hkv heads, o, o_lo, d_o and dq as q, dk and dv as k.  lse: float32 [H][T].  o_lo (may be NULL; o's
+ * layout) receives O − bf16(O), and passed to the backward is part of the O that D is formed from, as for
+ * xt_attention_fwd.  scale = 0 means 1/√hd.  Gradients are overwritten.  The backward's workspace holds D.
+ * Supported: dtype = XT_BF16, hd 64 or 128, row strides multiples of 8 elements, all pointers 16-byte
+ * aligned, T < 2³⁰ (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
+ * device-side waits are bounded (XT_DEVERR_TIMEOUT).
+ * ------------------------------------------------------------------------------- */
+typedef struct xt_attention_desc {
+  int64_t T;
+  int32_t H, Hkv, hd, dtype;
+  float scale;         /* 0: 1/sqrt(hd) */
+  float cap;           /* 0: scores are not capped */
+  const float* slopes; /* device, [H], or NULL: no distance bias */
+} xt_attention_desc;
+
+int xt_attention_plan_size(int64_t T, size_t* bytes);
+int xt_attention_plan(int64_t T, int n_docs, const int32_t* doc_off, const int32_t* doc_len, const int32_t* prefix,
+                      int causal, void* plan, size_t plan_bytes, void* stream);
+int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
+                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* o, void* o_lo,
+                            int64_t ld_o, float* lse, void* stream);
+int xt_attention_masked_bwd_workspace_size(const xt_attention_desc* desc, size_t* bytes);
+int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
+                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* o,
+                            const void* o_lo, int64_t ld_o, const void* d_o, int64_t ld_do, const float* lse, void* dq,
+                            int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, void* ws, size_t ws_bytes,
+                            void* stream);
 
 /* ---------------------------------------------------------------------------------
  * Cross-entropy, mean over rows ([AE] op table row cross_entropy, § Cross-entropy 反向推导):

@@ -80,3 +80,55 @@ def test_adamw8_refusals(xt):
         xt.xt_adamw8_step(xt.adamw_config(1e-3), [], [torch.zeros(1)], [], [], [], [])
     with pytest.raises(ValueError):   # not on a GPU
         xt.xt_adamw8_step(xt.adamw_config(1e-3), [torch.zeros(1)], [torch.zeros(1)], [], [], [], [])
+
+
+def masked(xt, T=256, H=2, Hkv=1, hd=64, dtype=1, scale=0.0, cap=0.0, plan=16, plan_bytes=1 << 20, q=16, ld_q=128,
+           ld_k=64, o=16, o_lo=None, lse=16, bwd=False, ws=16, ws_bytes=1 << 20, dk=16, ld_dk=64):
+    d = xt.AttentionDesc(T, H, Hkv, hd, dtype, scale, cap, None)
+    L = xt.lib()
+    if bwd:
+        return L.xt_attention_masked_bwd(C.byref(d), plan, plan_bytes, q, ld_q, 16, ld_k, 16, ld_k, o, o_lo, 128, 16, 128,
+                                         lse, 16, 128, dk, ld_dk, 16, 64, ws, ws_bytes, None)
+    return L.xt_attention_masked_fwd(C.byref(d), plan, plan_bytes, q, ld_q, 16, ld_k, 16, ld_k, o, o_lo, 128, lse, None)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_masked_attention_refusals(xt, bwd):
+    bad, uns, ali = xt.XT_ERR_INVALID_ARG, xt.XT_ERR_UNSUPPORTED, xt.XT_ERR_ALIGNMENT
+    go = lambda **kw: masked(xt, bwd=bwd, **kw)  # noqa: E731
+    assert go(T=-1) == bad and go(T=1 << 30) == bad
+    assert go(H=0) == bad and go(H=3, Hkv=2) == bad and go(Hkv=0) == bad
+    assert go(dtype=0) == uns
+    assert go(hd=32) == uns and go(hd=96) == uns
+    assert go(scale=-1.0) == bad and go(scale=float("nan")) == bad
+    assert go(cap=-1.0) == bad and go(cap=float("inf")) == bad
+    assert go(plan=None) == bad and go(plan=8) == ali and go(plan_bytes=100) == bad
+    assert go(q=None) == bad and go(q=24) == ali and go(ld_q=120) == bad and go(ld_q=132) == ali
+    assert go(ld_k=56) == bad and go(o=None) == bad and go(o_lo=8) == ali and go(lse=None) == bad
+    assert go(T=0, plan=None, lse=None, q=None, o=None) == xt.XT_OK
+    if bwd:
+        assert go(ws=None) == bad and go(ws=8) == ali and go(ws_bytes=100) == bad
+        assert go(dk=None) == bad and go(ld_dk=60) == bad and go(ld_dk=68) == ali
+
+
+def test_attention_plan_refusals(xt):
+    bad = xt.XT_ERR_INVALID_ARG
+    L = xt.lib()
+    n = C.c_size_t(0)
+    assert L.xt_attention_plan_size(-1, C.byref(n)) == bad and L.xt_attention_plan_size(1 << 30, C.byref(n)) == bad
+    assert L.xt_attention_plan_size(1000, C.byref(n)) == xt.XT_OK
+    go = lambda T=1000, docs=4, off=None, causal=1, plan=16, size=n.value: L.xt_attention_plan(  # noqa: E731
+        T, docs, off, None, None, causal, plan, size, None)
+    assert go(T=-1) == bad and go(T=1 << 30) == bad and go(docs=-1) == bad
+    assert go(docs=3) == bad and go(docs=0) == bad     # equal spans need a divisor
+    assert go(causal=2) == bad and go(plan=None) == bad and go(size=n.value - 1) == bad
+    assert go(plan=8) == xt.XT_ERR_ALIGNMENT
+    assert go(T=0, docs=0, size=64) == xt.XT_OK
+    with pytest.raises(ValueError):   # one length per document
+        xt.xt_attention_plan(torch.zeros(4), 8, 2, doc_len=torch.zeros(3, dtype=torch.int32))
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    for bad_args in (dict(o=z(4, 64)), dict(k=z(4, 64).float()), dict(v=z(5, 64)), dict(lse=torch.zeros(2, 3)),
+                     dict(slopes=torch.zeros(3)), dict(q=z(128, 4).t())):
+        a = dict(q=z(4, 128), k=z(4, 64), v=z(4, 64), o=z(4, 128), lse=torch.zeros(2, 4), slopes=None) | bad_args
+        with pytest.raises(ValueError):
+            xt.xt_attention_masked_fwd(a["q"], a["k"], a["v"], a["o"], a["lse"], z(64), 2, 1, 64, slopes=a["slopes"])

@@ -1,0 +1,187 @@
+// Entry points of masked attention: argument checks, tensor maps, launches (the kernels: attention_masked.cuh).
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "attention_masked.cuh"
+
+namespace xt {
+namespace attnm {
+
+int prepare_kernel(const void* kernel, int smem, int regs) {
+  static std::mutex mu;
+  static std::set<std::pair<const void*, int>> done;  // (kernel, device): the attribute is the device's
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(XT_ERR_CUDA, "masked attention: no current device");
+  std::lock_guard<std::mutex> lk(mu);
+  if (done.count({kernel, dev})) return XT_OK;
+  cudaFuncAttributes fa{};
+  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail(XT_ERR_CUDA, "masked attention: kernel attributes: %s", cudaGetErrorString(e));
+  if (regs && fa.numRegs != regs)
+    return fail(XT_ERR_UNSUPPORTED, "masked attention: kernel built with %d registers, not %d", fa.numRegs, regs);
+  done.insert({kernel, dev});
+  return XT_OK;
+}
+
+namespace {
+
+// [T, heads, hd] view of rows of ld elements, boxes of 128 tokens × 64 elements of one head, 128-byte swizzle.
+int token_map(CUtensorMap* tm, const void* base, int64_t ld, int64_t T, int heads, int hd) {
+  auto enc = encode_fn();
+  if (!enc) return fail(XT_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[4] = {cuuint64_t(hd), cuuint64_t(heads), cuuint64_t(T), 1};
+  cuuint64_t strides[3] = {cuuint64_t(hd * 2), cuuint64_t(ld * 2), cuuint64_t(T * ld * 2)};
+  cuuint32_t box[4] = {64, 1, BT, 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(XT_ERR_CUDA, "masked attention: cuTensorMapEncodeTiled failed (%d)", int(r));
+  return XT_OK;
+}
+
+struct Strided {
+  const void* p;
+  int64_t ld;
+  int heads;
+};
+
+int check(const char* fn, const xt_attention_desc* d, const void* plan, size_t plan_bytes, const void* lse,
+          std::initializer_list<Strided> xs) {
+  XT_REQUIRE(d != nullptr, "%s: desc is NULL", fn);
+  XT_REQUIRE(d->T >= 0 && d->T < (int64_t(1) << 30), "%s: T must be in [0, 2^30)", fn);
+  XT_REQUIRE(d->H > 0 && d->Hkv > 0 && d->H % d->Hkv == 0, "%s: H must be a positive multiple of Hkv", fn);
+  if (d->dtype != XT_BF16) return fail(XT_ERR_UNSUPPORTED, "%s: only bf16 is supported", fn);
+  if (d->hd != 64 && d->hd != 128) return fail(XT_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", fn);
+  XT_REQUIRE(std::isfinite(d->scale) && d->scale >= 0.f, "%s: scale must be finite and not negative", fn);
+  XT_REQUIRE(std::isfinite(d->cap) && d->cap >= 0.f, "%s: cap must be finite and not negative", fn);
+  const attn_plan::Layout l(d->T);
+  if (l.tiles * d->H >= (int64_t(1) << 30)) return fail(XT_ERR_UNSUPPORTED, "%s: too many tokens times heads", fn);
+  if (d->T == 0) return XT_OK;
+  XT_REQUIRE(plan && lse, "%s: NULL pointer", fn);
+  if (!aligned16(plan)) return fail(XT_ERR_ALIGNMENT, "%s: the plan must be 16-byte aligned", fn);
+  XT_REQUIRE(plan_bytes >= size_t(l.total) * 4, "%s: plan too small (%zu < %zu)", fn, plan_bytes, size_t(l.total) * 4);
+  for (const Strided& x : xs) {
+    XT_REQUIRE(x.p, "%s: NULL pointer", fn);
+    XT_REQUIRE(x.ld >= int64_t(x.heads) * d->hd, "%s: row stride smaller than the heads' columns", fn);
+    if (x.ld % 8) return fail(XT_ERR_ALIGNMENT, "%s: row strides must be multiples of 8", fn);
+    if (!aligned16(x.p)) return fail(XT_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned", fn);
+  }
+  return XT_OK;
+}
+
+attnm::Params params(const xt_attention_desc* d, const void* plan) {
+  Params p{};
+  p.plan = attn_plan::view(plan, d->T);
+  p.H = d->H;
+  p.Hkv = d->Hkv;
+  p.group = d->H / d->Hkv;
+  const double scale = d->scale > 0.f ? double(d->scale) : 1.0 / std::sqrt(double(d->hd)), log2e = 1.4426950408889634;
+  p.scale = float(scale);
+  p.sc = float(scale * log2e);
+  if (d->cap > 0.f) {
+    p.capk = float(2.0 * log2e * scale / double(d->cap));
+    p.cap2 = float(double(d->cap) * log2e);
+  }
+  p.slopes = d->slopes;
+  p.flag = errflag();
+  p.wait_ns = wait_limit_ns();
+  return p;
+}
+
+}  // namespace
+}  // namespace attnm
+}  // namespace xt
+
+using namespace xt;
+using namespace xt::attnm;
+
+extern "C" {
+
+int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
+                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* o, void* o_lo,
+                            int64_t ld_o, float* lse, void* stream) {
+  const char* fn = "xt_attention_masked_fwd";
+  const int H = desc ? desc->H : 0, Hkv = desc ? desc->Hkv : 0;
+  XT_TRY(check(fn, desc, plan, plan_bytes, lse, {{q, ld_q, H}, {k, ld_k, Hkv}, {v, ld_v, Hkv}, {o, ld_o, H}}));
+  if (desc->T == 0) return XT_OK;
+  if (!aligned16(o_lo)) return fail(XT_ERR_ALIGNMENT, "%s: o_lo must be 16-byte aligned", fn);
+  attnm::Params p = attnm::params(desc, plan);
+  p.q = static_cast<const bf16*>(q);
+  p.k = static_cast<const bf16*>(k);
+  p.v = static_cast<const bf16*>(v);
+  p.ldq = ld_q;
+  p.ldk = ld_k;
+  p.ldv = ld_v;
+  p.o = static_cast<bf16*>(o);
+  p.o_lo = static_cast<bf16*>(o_lo);
+  p.ldo = ld_o;
+  p.lse = lse;
+  CUtensorMap tq, tk, tv;
+  XT_TRY(token_map(&tq, q, ld_q, desc->T, H, desc->hd));
+  XT_TRY(token_map(&tk, k, ld_k, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tv, v, ld_v, desc->T, Hkv, desc->hd));
+  const bool cap = desc->cap > 0.f, bias = desc->slopes != nullptr;
+  return desc->hd == 64 ? launch_fwd<64>(cap, bias, tq, tk, tv, p, as_stream(stream))
+                        : launch_fwd<128>(cap, bias, tq, tk, tv, p, as_stream(stream));
+}
+
+int xt_attention_masked_bwd_workspace_size(const xt_attention_desc* desc, size_t* bytes) {
+  XT_REQUIRE(desc && bytes && desc->T >= 0 && desc->H > 0, "xt_attention_masked_bwd_workspace_size: bad arguments");
+  *bytes = (size_t(desc->T) * size_t(desc->H) * 4 + 255) & ~size_t(255);
+  return XT_OK;
+}
+
+int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
+                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* o,
+                            const void* o_lo, int64_t ld_o, const void* d_o, int64_t ld_do, const float* lse, void* dq,
+                            int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const char* fn = "xt_attention_masked_bwd";
+  const int H = desc ? desc->H : 0, Hkv = desc ? desc->Hkv : 0;
+  XT_TRY(check(fn, desc, plan, plan_bytes, lse,
+               {{q, ld_q, H}, {k, ld_k, Hkv}, {v, ld_v, Hkv}, {o, ld_o, H}, {d_o, ld_do, H}, {dq, ld_dq, H},
+                {dk, ld_dk, Hkv}, {dv, ld_dv, Hkv}}));
+  if (desc->T == 0) return XT_OK;
+  if (!aligned16(o_lo)) return fail(XT_ERR_ALIGNMENT, "%s: o_lo must be 16-byte aligned", fn);
+  size_t need = 0;
+  XT_TRY(xt_attention_masked_bwd_workspace_size(desc, &need));
+  XT_REQUIRE(ws && ws_bytes >= need, "%s: workspace too small (%zu < %zu)", fn, ws_bytes, need);
+  if (!aligned16(ws)) return fail(XT_ERR_ALIGNMENT, "%s: the workspace must be 16-byte aligned", fn);
+  attnm::Params p = attnm::params(desc, plan);
+  p.q = static_cast<const bf16*>(q);
+  p.k = static_cast<const bf16*>(k);
+  p.v = static_cast<const bf16*>(v);
+  p.ldq = ld_q;
+  p.ldk = ld_k;
+  p.ldv = ld_v;
+  p.o = const_cast<bf16*>(static_cast<const bf16*>(o));
+  p.o_lo = const_cast<bf16*>(static_cast<const bf16*>(o_lo));
+  p.ldo = ld_o;
+  p.d_o = static_cast<const bf16*>(d_o);
+  p.lddo = ld_do;
+  p.lse = const_cast<float*>(lse);
+  p.D = static_cast<float*>(ws);
+  p.dq = static_cast<bf16*>(dq);
+  p.dk = static_cast<bf16*>(dk);
+  p.dv = static_cast<bf16*>(dv);
+  p.lddq = ld_dq;
+  p.lddk = ld_dk;
+  p.lddv = ld_dv;
+  CUtensorMap tq, tk, tv, tdo;
+  XT_TRY(token_map(&tq, q, ld_q, desc->T, H, desc->hd));
+  XT_TRY(token_map(&tk, k, ld_k, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tv, v, ld_v, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tdo, d_o, ld_do, desc->T, H, desc->hd));
+  const bool cap = desc->cap > 0.f, bias = desc->slopes != nullptr;
+  cudaStream_t s = as_stream(stream);
+  if (desc->hd == 64) {
+    XT_TRY((launch_bwd<64, false>(cap, bias, tq, tk, tv, tdo, p, s)));
+    return launch_bwd<64, true>(cap, bias, tq, tk, tv, tdo, p, s);
+  }
+  XT_TRY((launch_bwd<128, false>(cap, bias, tq, tk, tv, tdo, p, s)));
+  return launch_bwd<128, true>(cap, bias, tq, tk, tv, tdo, p, s);
+}
+
+}  // extern "C"

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libxt.so")
 
 XT_OK, XT_ERR_INVALID_ARG, XT_ERR_UNSUPPORTED, XT_ERR_ALIGNMENT, XT_ERR_CUDA, XT_ERR_TIMEOUT = range(6)
 XT_F32, XT_BF16 = 0, 1
-XT_DEVERR_INDEX, XT_DEVERR_TIMEOUT = 1, 2
+XT_DEVERR_INDEX, XT_DEVERR_TIMEOUT, XT_DEVERR_PLAN = 1, 2, 4
 XT_NORM_RMS, XT_NORM_LN = 0, 1
 XT_MLP_SWIGLU, XT_MLP_GELU = 0, 1
 XT_ATTN_AUTO, XT_ATTN_COMPOSED, XT_ATTN_FUSED = 0, 1, 2
@@ -45,6 +45,11 @@ class AdamWConfig(C.Structure):
     _fields_ = [("lr", C.c_float), ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float),
                 ("weight_decay", C.c_float), ("max_grad_norm", C.c_float), ("grad_scale", C.c_float),
                 ("step", C.c_int32)]
+
+
+class AttentionDesc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("H", C.c_int32), ("Hkv", C.c_int32), ("hd", C.c_int32), ("dtype", C.c_int32),
+                ("scale", C.c_float), ("cap", C.c_float), ("slopes", C.c_void_p)]
 
 
 class BlockConfig(C.Structure):
@@ -118,6 +123,13 @@ _SIGS = {
     "xt_attention_bwd_workspace_size": [_I, _I, _I, _SZP],
     "xt_attention_bwd": [_VP, _VP, _VP, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP, C.c_size_t,
                          _I, _I, _I, _I, _I, _I, _VP],
+    "xt_attention_plan_size": [_I64, _SZP],
+    "xt_attention_plan": [_I64, _I, _VP, _VP, _VP, _I, _VP, C.c_size_t, _VP],
+    "xt_attention_masked_fwd": [C.POINTER(AttentionDesc), _VP, C.c_size_t, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP,
+                                _I64, _VP, _VP],
+    "xt_attention_masked_bwd_workspace_size": [C.POINTER(AttentionDesc), _SZP],
+    "xt_attention_masked_bwd": [C.POINTER(AttentionDesc), _VP, C.c_size_t, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP,
+                                _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, C.c_size_t, _VP],
     "xt_cross_entropy_workspace_size": [_I64, _SZP],
     "xt_cross_entropy_fwd": [_VP, _VP, _VP, _VP, _I64, _I64, _I, _VP, _VP],
     "xt_cross_entropy_fwd_bwd": [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I, _VP, _VP],
@@ -526,6 +538,80 @@ def xt_attention_bwd(q, k, v, o, d_o, lse, dq, dk, dv, B, S, H, hd, causal=1, o_
     call("xt_attention_bwd", ptr(q, False), ptr(k, False), ptr(v, False), q.stride(0), ptr(o, False),
          ptr(o_lo, False), ptr(d_o, False), o.stride(0), ptr(lse), ptr(dq, False), ptr(dk, False), ptr(dv, False),
          dq.stride(0), ptr(ws), ws.numel(), B, S, H, hd, causal, dt(q), stream(s))
+
+
+def attention_plan_buffer(T, device="cuda"):
+    """A buffer for the plan of T tokens (xt_attention_plan fills it)."""
+    return torch.empty(ws_bytes("xt_attention_plan_size", int(T)), dtype=torch.uint8, device=device)
+
+
+def _ints(t, n, name):
+    if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+        raise ValueError(f"{name} must be int32 with {n} entries")
+    return ptr(t)
+
+
+def xt_attention_plan(plan, T, n_docs, doc_off=None, doc_len=None, prefix=None, causal=1, s=None):
+    """The plan of a batch of T tokens in n_docs documents: doc_off int32 [n_docs + 1] (None: equal spans),
+    doc_len and prefix int32 [n_docs] or None."""
+    call("xt_attention_plan", int(T), int(n_docs), _ints(doc_off, n_docs + 1, "doc_off"), _ints(doc_len, n_docs, "doc_len"),
+         _ints(prefix, n_docs, "prefix"), int(causal), ptr(plan), plan.numel() * plan.element_size(), stream(s))
+
+
+def _attention_desc(T, H, Hkv, hd, dtype, scale, cap, slopes):
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != H):
+        raise ValueError("slopes must be float32 with one entry per query head")
+    return AttentionDesc(int(T), H, Hkv, hd, dtype, float(scale or 0.0), float(cap), ptr(slopes))
+
+
+def attention_masked_workspace(T, H, Hkv, hd, device="cuda"):
+    """The backward's workspace."""
+    d = _attention_desc(T, H, Hkv, hd, XT_BF16, None, 0.0, None)
+    return torch.empty(ws_bytes("xt_attention_masked_bwd_workspace_size", C.byref(d)), dtype=torch.uint8, device=device)
+
+
+def _token_rows(T, hd, dtype, *pairs):
+    """(pointer, row stride) of each [T, heads·hd] tensor, flattened."""
+    out = []
+    for t, heads in pairs:
+        if t.dim() != 2 or t.shape[0] != T or t.shape[1] != heads * hd or t.dtype != dtype:
+            raise ValueError(f"expected a [{T}, {heads * hd}] tensor of {dtype}")
+        st0, st1 = t.stride()
+        if st1 != 1:
+            raise ValueError("unit column stride is needed")
+        out += [ptr(t, False), st0 if T > 1 else max(st0, -(-heads * hd // 8) * 8)]
+    return out
+
+
+def xt_attention_masked_fwd(q, k, v, o, lse, plan, H, Hkv, hd, scale=None, cap=0.0, slopes=None, o_lo=None, s=None):
+    """q, o [T, H·hd], k, v [T, Hkv·hd] bf16 views with unit column stride, lse float32 [H, T]; plan: from
+    xt_attention_plan; cap: tanh cap of the scores (0: none); slopes: float32 [H] or None."""
+    T = q.shape[0]
+    if o_lo is not None and (o_lo.shape != o.shape or o_lo.stride() != o.stride() or o_lo.dtype != o.dtype):
+        raise ValueError("o_lo must have o's layout")
+    if lse.dtype != torch.float32 or lse.numel() != H * T:
+        raise ValueError("lse must be float32 [H, T]")
+    d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
+    q_, k_, v_, o_ = (_token_rows(T, hd, q.dtype, x) for x in ((q, H), (k, Hkv), (v, Hkv), (o, H)))
+    call("xt_attention_masked_fwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, o_[0],
+         ptr(o_lo, False), o_[1], ptr(lse), stream(s))
+
+
+def xt_attention_masked_bwd(q, k, v, o, d_o, lse, dq, dk, dv, plan, H, Hkv, hd, scale=None, cap=0.0, slopes=None,
+                            o_lo=None, ws=None, s=None):
+    """Gradients of xt_attention_masked_fwd (its o, lse and o_lo); dq, dk, dv in the layouts of q, k, v."""
+    T = q.shape[0]
+    if o_lo is not None and (o_lo.shape != o.shape or o_lo.stride() != o.stride() or o_lo.dtype != o.dtype):
+        raise ValueError("o_lo must have o's layout")
+    if lse.dtype != torch.float32 or lse.numel() != H * T:
+        raise ValueError("lse must be float32 [H, T]")
+    d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
+    if ws is None:
+        ws = attention_masked_workspace(T, H, Hkv, hd, q.device)
+    q_, k_, v_, o_, do_, dq_, dk_, dv_ = (_token_rows(T, hd, q.dtype, x) for x in (
+        (q, H), (k, Hkv), (v, Hkv), (o, H), (d_o, H), (dq, H), (dk, Hkv), (dv, Hkv)))
+    call("xt_attention_masked_bwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, o_[0],
+         ptr(o_lo, False), o_[1], *do_, ptr(lse), *dq_, *dk_, *dv_, ptr(ws), ws.numel() * ws.element_size(), stream(s))
 
 
 def xt_softmax_bwd(d, y, dx, causal=0, q_len=0, acc=0, s=None):
