@@ -19,6 +19,8 @@
 // done over from its visible columns alone (redo_row): the check costs an addition per output element.
 #pragma once
 
+#include <type_traits>
+
 #include "attention_plan.cuh"
 #include "gemm.cuh"
 #include "internal.cuh"
@@ -73,6 +75,32 @@ __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  return f32x2_pack(__uint_as_float(lo), __uint_as_float(hi));
+}
+// 32 lanes × 16 consecutive columns into registers, and back.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -130,6 +158,20 @@ struct Mma {
   }
 };
 
+// r[c] −= slope₂·|d0 + c|.
+template <int N>
+__device__ __forceinline__ void add_bias(uint32_t (&r)[N], float slope2, int d0, int side) {
+  if (side != 0) {
+    const float st = side > 0 ? slope2 : -slope2, b0 = st * float(d0);
+#pragma unroll
+    for (int c = 0; c < N; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + fmaf(float(c), st, b0));
+  } else {
+    const float d = float(d0);
+#pragma unroll
+    for (int c = 0; c < N; ++c) r[c] = __float_as_uint(fmaf(-slope2, fabsf(d + float(c)), __uint_as_float(r[c])));
+  }
+}
+
 // Scores of one row, r[c] = q·k of column base + c, to s·log₂e (CAP or BIAS; without both the caller
 // scales).  d0: column 0 minus the row, in tokens; side: +1 / −1 where every column of the tile lies before
 // / behind the row (the distance is then linear in c), 0 else.
@@ -146,18 +188,7 @@ __device__ __forceinline__ void to_log2(uint32_t (&r)[N], const Params& p, float
 #pragma unroll
     for (int c = 0; c < N; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * p.sc);
   }
-  if constexpr (BIAS) {
-    if (side != 0) {
-      const float st = side > 0 ? slope2 : -slope2, b0 = st * float(d0);
-#pragma unroll
-      for (int c = 0; c < N; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + fmaf(float(c), st, b0));
-    } else {
-      const float d = float(d0);
-#pragma unroll
-      for (int c = 0; c < N; ++c)
-        r[c] = __float_as_uint(fmaf(-slope2, fabsf(d + float(c)), __uint_as_float(r[c])));
-    }
-  }
+  if constexpr (BIAS) add_bias(r, slope2, d0, side);
 }
 
 // ------------------------------------------------------------------------------ the careful path
@@ -520,14 +551,14 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         if (j > rg.x && __any_sync(0xffffffffu, need)) {
           if (C::OWN_P) tc_fence_after();
           const float a = need ? exp2f((m - m_new) * unit) : 1.f;
-#pragma unroll
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + uint32_t(c * 32), o);
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 16) {  // few registers: the row's scores stay in theirs
+            uint32_t o[16];
+            tmem_ld16(tO + uint32_t(c), o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-            tmem_st32(tO + uint32_t(c * 32), o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            tmem_st16(tO + uint32_t(c), o);
           }
         }
         if (need) {
@@ -538,16 +569,19 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         const uint64_t sc2 = f32x2_pack(unit, unit), ms2 = f32x2_pack(-ms, -ms);
         uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          float x0, x1;
-          f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2), x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          ls[(c >> 1) & 3] = f32x2_add(ls[(c >> 1) & 3], f32x2_pack(x0, x1));
-          s[c >> 1] = pack_bf16(x0, x1);
-          if (c == 62) tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(s));
+        for (int c = 0; c < 128; c += 32) {  // 32 columns at a time: 16 registers of P
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            f32x2_unpack(f32x2_fma(pair(s[c + e], s[c + e + 1]), sc2, ms2), x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            ls[(e >> 1) & 3] = f32x2_add(ls[(e >> 1) & 3], f32x2_pack(x0, x1));
+            pk[e >> 1] = pack_bf16(x0, x1);
+          }
+          tmem_st16(tP + uint32_t(c / 2), pk);
         }
-        tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         float la, lb;
         f32x2_unpack(f32x2_add(f32x2_add(ls[0], ls[1]), f32x2_add(ls[2], ls[3])), la, lb);
         l += la + lb;
@@ -639,7 +673,8 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // before this tile's second products wherever its buffer allows (two S buffers, or KEY at hd 128 one), so
 // the tensor core works while the rows are at their exponentials.  The query pass also forms D (its rows'
 // dO·O) and leaves it in the workspace for the key pass, which follows it: no kernel of its own for D.
-constexpr int kThreadsBwd = 320;
+constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 MMA, 2 and 3 idle, 4–11 rows
+constexpr uint32_t kBwdRegsCtl = 72, kBwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
 
 template <int HD, bool KEY>
 struct BwdCfg {
@@ -732,8 +767,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
   const CUtensorMap *tmA1 = KEY ? &tmK : &tmQ, *tmA2 = KEY ? &tmV : &tmDO;
   const CUtensorMap *tmR1 = KEY ? &tmQ : &tmK, *tmR2 = KEY ? &tmDO : &tmV;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_dec<kBwdRegsCtl>();
+    if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- TMA producer
       uint32_t na = 0, n = 0;
       bool ok = true;
@@ -768,9 +804,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         drained &= mbar_wait(smem_u32(&r_full[g % C::RING]), (g / C::RING) & 1);
       }
       if (!drained) give_up();
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------------- MMA issuer
       uint32_t na = 0, g = 0;
       bool ok = true;
@@ -825,7 +859,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
     }
   } else {
     // ---------------------------------------------------------------- rows
-    const int qw = warp & 3, half = (warp - 2) >> 2, col0 = 64 * half;
+    regs_inc<kBwdRegsRows>();
+    const int qw = warp & 3, half = (warp - 4) >> 2, col0 = 64 * half;
     const int rr = qw * 32 + lane;
     const uint32_t lane_off = uint32_t(qw * 32) << 16;
     const uint32_t tDP = tbase + C::DP + lane_off + uint32_t(col0);
@@ -878,14 +913,14 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         if (half == 0 && real) p.D[int64_t(it.h0) * T + row] = Dr;
       }
       int h = it.h0, t = it.rg.x;
-      // KEY: this thread's entry of a column tile's lse·log₂e (half 0) or D (half 1), read one tile ahead
+      // KEY: this thread's entry of a column tile's −lse·log₂e (half 0) or −D (half 1), read one tile ahead
       auto vec_entry = [&](int hh, int tt) -> float {
         const int q = tt * BT + rr;
         if (half == 0) {
-          const float x = q < T ? p.lse[int64_t(hh) * T + q] * kLog2e : INFINITY;
-          return x == -INFINITY ? INFINITY : x;
+          const float x = q < T ? p.lse[int64_t(hh) * T + q] * -kLog2e : -INFINITY;
+          return x == INFINITY ? -INFINITY : x;
         }
-        return q < T ? p.D[int64_t(hh) * T + q] : 0.f;
+        return q < T ? -p.D[int64_t(hh) * T + q] : 0.f;
       };
       float vnext = 0.f;
       if (KEY && it.n > 0) vnext = vec_entry(h, t);
@@ -909,50 +944,56 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
-        if constexpr (BIAS && !CAP)
-          to_log2<64, CAP, BIAS>(s, p, slope2, t * BT + col0 - row, t < it.tile ? 1 : t > it.tile ? -1 : 0);
         const float unit = (CAP || BIAS) ? 1.f : p.sc;
+        const int side = t < it.tile ? 1 : t > it.tile ? -1 : 0;
+        float slack[CAP ? 64 : 1];  // 1 − tanh²
+        if constexpr (CAP) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {  // as to_log2, keeping u = 1/(1 + e^{2a/cap}): 1 − tanh² = 4u(1 − u)
+            const float u = rcp(1.f + ex2(__uint_as_float(s[c]) * p.capk));
+            s[c] = __float_as_uint(fmaf(-2.f * p.cap2, u, p.cap2));
+            slack[c] = 4.f * u * (1.f - u);
+          }
+          if constexpr (BIAS) add_bias(s, slope2, t * BT + col0 - row, side);
+        } else if constexpr (BIAS) {
+          to_log2<64, CAP, BIAS>(s, p, slope2, t * BT + col0 - row, side);
+        }
         const bool edge = t < it.rg.z || t >= it.rg.w;
         const int lo = iv.x - t * BT - col0, hi = iv.y - t * BT - col0;
-        const float dist0 = float(t * BT + col0 - row);
-        uint32_t pk[32];
+        if (edge) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float u[2];
-          if constexpr (CAP) {  // as to_log2, keeping 1/(1 + e^{2a/cap}) for the slope 1 − tanh²
+          for (int c = 0; c < 64; ++c)
+            if (c < lo || c >= hi) {
+              s[c] = __float_as_uint(-INFINITY);
+              if constexpr (CAP) slack[c] = 0.f;
+            }
+        }
+        const uint64_t unit2 = f32x2_pack(unit, unit), nl2 = f32x2_pack(-lse2, -lse2);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              u[e] = rcp(1.f + ex2(__uint_as_float(s[c + e]) * p.capk));
-              float x = fmaf(-2.f * p.cap2, u[e], p.cap2);
-              if constexpr (BIAS) x = fmaf(-slope2, fabsf(dist0 + float(c + e)), x);
-              s[c + e] = __float_as_uint(x);
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = c; e < c + 32; e += 4) {
+            float4 nl;
+            if constexpr (KEY) nl = *reinterpret_cast<const float4*>(lv + col0 + e);
+            float x[4];
+            f32x2_unpack(f32x2_fma(pair(s[e], s[e + 1]), unit2, KEY ? f32x2_pack(nl.x, nl.y) : nl2), x[0], x[1]);
+            f32x2_unpack(f32x2_fma(pair(s[e + 2], s[e + 3]), unit2, KEY ? f32x2_pack(nl.z, nl.w) : nl2), x[2], x[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
+            if constexpr (KEY) {
+              pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
+              pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (CAP) x[k] *= slack[e + k];
+              s[e + k] = __float_as_uint(x[k]);
             }
           }
-          const float l0 = KEY ? lv[col0 + c] : lse2, l1 = KEY ? lv[col0 + c + 1] : lse2;
-          float x0, x1;
-          f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                 f32x2_pack(unit, unit), f32x2_pack(-l0, -l1)),
-                       x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          if (edge) {
-            if (c < lo || c >= hi) x0 = 0.f;
-            if (c + 1 < lo || c + 1 >= hi) x1 = 0.f;
-          }
-          if constexpr (KEY) pk[c >> 1] = pack_bf16(x0, x1);
-          if constexpr (CAP) {
-            x0 *= 4.f * u[0] * (1.f - u[0]);
-            x1 *= 4.f * u[1] * (1.f - u[1]);
-            if (edge) {  // a masked column's tanh may be NaN
-              if (c < lo || c >= hi) x0 = 0.f;
-              if (c + 1 < lo || c + 1 >= hi) x1 = 0.f;
-            }
-          }
-          s[c] = __float_as_uint(x0);
-          s[c + 1] = __float_as_uint(x1);
+          if constexpr (KEY) tmem_st16(tS + uint32_t(c / 2), pk);
         }
         if constexpr (KEY) {
-          tmem_st32(tS, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -964,17 +1005,33 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(d));
         tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
         tmem_ld_wait();
+        const uint64_t nd2 = f32x2_pack(-Dr, -Dr);
+        auto form_ds = [&](auto masked) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float x0 = __uint_as_float(s[c]) * (__uint_as_float(d[c]) - (KEY ? lv[128 + col0 + c] : Dr));
-          float x1 = __uint_as_float(s[c + 1]) * (__uint_as_float(d[c + 1]) - (KEY ? lv[128 + col0 + c + 1] : Dr));
-          if (edge) {  // a masked column's dP may be NaN
-            if (c < lo || c >= hi) x0 = 0.f;
-            if (c + 1 < lo || c + 1 >= hi) x1 = 0.f;
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = c; e < c + 32; e += 4) {
+              float4 nd;
+              if constexpr (KEY) nd = *reinterpret_cast<const float4*>(lv + 128 + col0 + e);
+              float x[4];
+              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e], d[e + 1]), KEY ? f32x2_pack(nd.x, nd.y) : nd2),
+                                     pair(s[e], s[e + 1])), x[0], x[1]);
+              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e + 2], d[e + 3]), KEY ? f32x2_pack(nd.z, nd.w) : nd2),
+                                     pair(s[e + 2], s[e + 3])), x[2], x[3]);
+              if constexpr (decltype(masked)::value) {  // a masked column's dP or D may be NaN
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (e + k < lo || e + k >= hi) x[k] = 0.f;
+              }
+              pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
+              pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
+            }
+            tmem_st16(tDP + uint32_t(c / 2), pk);
           }
-          pk[c >> 1] = pack_bf16(x0, x1);
-        }
-        tmem_st32(tDP, pk);
+        };
+        if (edge) form_ds(std::true_type{});
+        else form_ds(std::false_type{});
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -1088,7 +1145,7 @@ int launch_bwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk
   static int bwd_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo, \
                      const Params& p, cudaStream_t s) {                                                          \
     auto k = attnm_bwd_kernel<HD, KEY, CAP, BIAS>;                                                               \
-    XT_TRY(prepare_kernel(reinterpret_cast<const void*>(k), BwdCfg<HD, KEY>::BYTES, 0));                         \
+    XT_TRY(prepare_kernel(reinterpret_cast<const void*>(k), BwdCfg<HD, KEY>::BYTES, 168));                         \
     const int64_t items = int64_t(p.plan.tiles) * (KEY ? p.Hkv : p.H);                                           \
     launch(k, unsigned(items < num_sms() ? items : num_sms()), kThreadsBwd, BwdCfg<HD, KEY>::BYTES, s, tq, tk,   \
            tv, tdo, p);                                                                                          \
