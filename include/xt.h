@@ -316,7 +316,8 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  * Layout: token t of q is row t (ld_q elements apart), its head h columns [h·hd, h·hd + hd); k, v likewise
  * with Hkv heads, o, o_lo, d_o and dq as q, dk and dv as k.  lse: float32 [H][T].  o_lo (may be NULL; o's
  * layout) receives O − bf16(O), and passed to the backward is part of the O that D is formed from, as for
- * xt_attention_fwd.  scale = 0 means 1/√hd.  Gradients are overwritten.  The backward's workspace holds D.
+ * xt_attention_fwd.  scale = 0 means 1/√hd.  Gradients are overwritten.  The backward's workspace holds D (and partial sums where few shared
+ * key heads are split over more of the GPU).
  * Supported: dtype = XT_BF16, hd 64 or 128, row strides multiples of 8 elements, all pointers 16-byte
  * aligned, T < 2³⁰ (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
  * device-side waits are bounded (XT_DEVERR_TIMEOUT).

@@ -27,6 +27,28 @@ int prepare_kernel(const void* kernel, int smem, int regs) {
 
 namespace {
 
+// dK and dV of a split key pass: the splits' sums added in order, scaled and rounded.
+__global__ void __launch_bounds__(256) attnm_join_kernel(const __grid_constant__ attnm::Params p, int width) {
+  pdl_begin();
+  const int64_t n = p.plan.T * width, per = n / 4;
+  for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < 2 * per; v += int64_t(gridDim.x) * 256) {
+    const bool is_v = v >= per;
+    const int64_t e = (is_v ? v - per : v) * 4, t = e / width;
+    const float* src = (is_v ? p.part_v : p.part_k) + e;
+    float4 a = *reinterpret_cast<const float4*>(src);
+    for (int s = 1; s < p.split; ++s) {
+      const float4 b = *reinterpret_cast<const float4*>(src + s * n);
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    const float mul = is_v ? 1.f : p.scale;
+    bf16* out = (is_v ? p.dv + t * p.lddv : p.dk + t * p.lddk) + (e - t * width);
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(a.x * mul, a.y * mul), pack_bf16(a.z * mul, a.w * mul));
+  }
+}
+
 // [T, heads, hd] view of rows of ld elements, boxes of 128 tokens × 64 elements of one head, 128-byte swizzle.
 int token_map(CUtensorMap* tm, const void* base, int64_t ld, int64_t T, int heads, int hd) {
   auto enc = encode_fn();
@@ -69,6 +91,26 @@ int check(const char* fn, const xt_attention_desc* d, const void* plan, size_t p
     if (!aligned16(x.p)) return fail(XT_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned", fn);
   }
   return XT_OK;
+}
+
+// Items of the key pass per key tile and head: shared key heads leave few of them, each over the whole group
+// of query heads.  Where they are fewer than four per SM of a GB300 the group is cut into up to its heads, the
+// parts' float32 sums being joined by a second kernel (4 x 1023 tokens, 16 query and 4 key heads of 128:
+// MEASURED).  A constant SM count keeps the workspace's size a function of the problem alone.
+int key_split(const xt_attention_desc* d) {
+  constexpr int64_t kWanted = 4 * 152;
+  const int64_t items = attn_plan::Layout(d->T).tiles * d->Hkv;
+  const int group = d->H / d->Hkv;
+  int split = 1;
+  while (split < group && items * split < kWanted) split = split * 2 < group ? split * 2 : group;
+  const int share = (group + split - 1) / split;
+  return (group + share - 1) / share;
+}
+size_t d_bytes(const xt_attention_desc* d) {  // nl and nd, rows of whole tiles
+  return 2 * size_t(attn_plan::Layout(d->T).tiles) * BT * size_t(d->H) * 4;
+}
+size_t part_bytes(const xt_attention_desc* d, int split) {
+  return (size_t(split) * size_t(d->T) * size_t(d->Hkv) * size_t(d->hd) * 4 + 255) & ~size_t(255);
 }
 
 attnm::Params params(const xt_attention_desc* d, const void* plan) {
@@ -128,8 +170,11 @@ int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, siz
 }
 
 int xt_attention_masked_bwd_workspace_size(const xt_attention_desc* desc, size_t* bytes) {
-  XT_REQUIRE(desc && bytes && desc->T >= 0 && desc->H > 0, "xt_attention_masked_bwd_workspace_size: bad arguments");
-  *bytes = (size_t(desc->T) * size_t(desc->H) * 4 + 255) & ~size_t(255);
+  XT_REQUIRE(desc && bytes && desc->T >= 0 && desc->T < (int64_t(1) << 30) && desc->H > 0 && desc->Hkv > 0 &&
+                 desc->H % desc->Hkv == 0 && desc->hd > 0,
+             "xt_attention_masked_bwd_workspace_size: bad arguments");
+  const int split = key_split(desc);
+  *bytes = d_bytes(desc) + (split > 1 ? 2 * part_bytes(desc, split) : 0);
   return XT_OK;
 }
 
@@ -162,7 +207,8 @@ int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, siz
   p.d_o = static_cast<const bf16*>(d_o);
   p.lddo = ld_do;
   p.lse = const_cast<float*>(lse);
-  p.D = static_cast<float*>(ws);
+  p.nl = static_cast<float*>(ws);
+  p.nd = p.nl + int64_t(p.plan.tiles) * BT * H;
   p.dq = static_cast<bf16*>(dq);
   p.dk = static_cast<bf16*>(dk);
   p.dv = static_cast<bf16*>(dv);
@@ -176,12 +222,24 @@ int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, siz
   XT_TRY(token_map(&tdo, d_o, ld_do, desc->T, H, desc->hd));
   const bool cap = desc->cap > 0.f, bias = desc->slopes != nullptr;
   cudaStream_t s = as_stream(stream);
+  p.split = key_split(desc);
+  p.share = (p.group + p.split - 1) / p.split;
+  if (p.split > 1) {
+    p.part_k = reinterpret_cast<float*>(static_cast<char*>(ws) + d_bytes(desc));
+    p.part_v = reinterpret_cast<float*>(reinterpret_cast<char*>(p.part_k) + part_bytes(desc, p.split));
+  }
   if (desc->hd == 64) {
     XT_TRY((launch_bwd<64, false>(cap, bias, tq, tk, tv, tdo, p, s)));
-    return launch_bwd<64, true>(cap, bias, tq, tk, tv, tdo, p, s);
+    XT_TRY((launch_bwd<64, true>(cap, bias, tq, tk, tv, tdo, p, s)));
+  } else {
+    XT_TRY((launch_bwd<128, false>(cap, bias, tq, tk, tv, tdo, p, s)));
+    XT_TRY((launch_bwd<128, true>(cap, bias, tq, tk, tv, tdo, p, s)));
   }
-  XT_TRY((launch_bwd<128, false>(cap, bias, tq, tk, tv, tdo, p, s)));
-  return launch_bwd<128, true>(cap, bias, tq, tk, tv, tdo, p, s);
+  if (p.split == 1) return XT_OK;
+  const int width = Hkv * desc->hd;
+  const int64_t blocks = ceil_div(desc->T * width / 2, 256), most = int64_t(num_sms()) * 8;
+  launch(attnm_join_kernel, unsigned(blocks < most ? blocks : most), 256, 0, s, p, width);
+  return check_launch("xt_attention_masked_bwd (join)");
 }
 
 }  // extern "C"

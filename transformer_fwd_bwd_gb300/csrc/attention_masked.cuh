@@ -15,8 +15,15 @@
 //
 // Rows whose mask leaves nothing get O = 0, lse = −∞ and zero gradients.  A masked element's P is 0 by
 // selection, so whatever its score is (NaN, ∞) stays out of the row; but the products add 0·V for masked
-// keys of a tile, which a NaN or ∞ in V turns into NaN.  A row whose result is not finite is therefore
-// done over from its visible columns alone (redo_row): the check costs an addition per output element.
+// keys of a tile, which a NaN or ∞ in V turns into NaN.  A row whose result is not finite, and which has
+// such a column among its masked ones, is therefore done over from its visible columns alone (repair): the
+// check costs a fused multiply-add per output element.
+//
+// Work items (a head and a tile or pair of tiles, the longest first) are the blocks of the grid, one per SM
+// at a time; a running block takes over the next item instead of ending (clusterlaunchcontrol: the hardware
+// cancels the launch of a waiting block and hands out its index), which keeps its tensor memory, barriers and
+// loads in flight across items and balances them by their real times.  The producer warp takes the next item
+// when its last load of this one is issued and leaves its description in shared memory for the other warps.
 #pragma once
 
 #include <type_traits>
@@ -39,6 +46,7 @@ constexpr float kRescale = 8.f;  // log2 growth of the running max that forces a
 struct Params {
   attn_plan::View plan;
   int H, Hkv, group;      // query heads, key / value heads, H / Hkv
+  int split, share;       // key pass: items per key head and tile, query heads of each (but the last)
   float sc;               // scale·log₂e
   float scale;
   float capk, cap2;       // 2·log₂e·scale/cap, cap·log₂e (CAP)
@@ -49,9 +57,10 @@ struct Params {
   const bf16 *d_o;
   int64_t ldo, lddo;
   float *lse;             // [H][T]
-  float *D;               // [H][T]
+  float *nl, *nd;         // workspace, [H][tiles·128]: −lse·log₂e (−∞ where nothing is seen) and −D
   bf16 *dq, *dk, *dv;
   int64_t lddq, lddk, lddv;
+  float *part_k, *part_v; // split > 1: float32 sums [split][T][Hkv·hd] of dK (before scale) and dV
   uint32_t* flag;
   uint64_t wait_ns;
 };
@@ -119,8 +128,11 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  return mbar_wait_spin(bar, parity, limit_ns);
+}
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, limit_ns));
+  return __all_sync(0xffffffffu, spin(bar, parity, limit_ns));
 }
 
 template <uint32_t N>
@@ -135,21 +147,24 @@ __device__ __forceinline__ void regs_inc() {
 // The products of 128-row tiles held in shared memory as HD/64 swizzled chunks of TILE bytes.
 template <int HD>
 struct Mma {
-  static constexpr uint32_t kIdescS = instr_desc_bf16(128, 128, false, false);
-  static constexpr uint32_t kIdescO = instr_desc_bf16(128, HD, false, true);
-  // D = A Bᵀ over the head dimension (both K-major)
+  // D [128 × N] = A Bᵀ over the head dimension (both K-major), N rows of B from b on
+  template <int N = BT>
   static __device__ __forceinline__ void nt(uint32_t d, uint32_t a, uint32_t b) {
+    constexpr uint32_t kIdesc = instr_desc_bf16(128, N, false, false);
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
       const uint32_t off = uint32_t((kk >> 2) * TILE + (kk & 3) * 32);
-      tc_mma<kBf16>(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+      tc_mma<kBf16>(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
     }
   }
-  // D (+)= A B over 128 tokens: A bf16 in tensor memory (k-step kk at a + (kk/4)·skip + 8·(kk%4)), B MN-major
-  static __device__ __forceinline__ void tn(uint32_t d, uint32_t a, uint32_t skip, uint32_t b, bool first) {
+  // D [128 × HD] (+)= A B over N tokens: A bf16 in tensor memory, 64 tokens (32 columns) every `step` columns,
+  // B's N rows from b on, MN-major
+  template <int N = BT>
+  static __device__ __forceinline__ void tn(uint32_t d, uint32_t a, uint32_t step, uint32_t b, bool first) {
+    constexpr uint32_t kIdesc = instr_desc_bf16(128, HD, false, true);
 #pragma unroll
-    for (int kk = 0; kk < BT / 16; ++kk)
-      tc_mma_ts(d, a + uint32_t(kk >> 2) * skip + uint32_t(kk & 3) * 8, smem_desc(b + kk * 2048, TILE, 1024), kIdescO,
+    for (int kk = 0; kk < N / 16; ++kk)
+      tc_mma_ts(d, a + uint32_t(kk >> 2) * step + uint32_t(kk & 3) * 8, smem_desc(b + kk * 2048, TILE, 1024), kIdesc,
                 (!first || kk > 0) ? 1u : 0u);
   }
   static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int head, int tile) {
@@ -224,9 +239,10 @@ __device__ __forceinline__ float pair_score(const Params& p, float dot, float sl
 // one, then every lane adds the columns to its HD/32 elements.
 //   FWD:  out = Σ_j p_j v_j,               row = query, m2: the running max
 //   else: out = Σ dS_ij·(other row), out2 = Σ P_ij·dO_i (KEY), of the row `row` of head h
+// False as soon as a sum is not finite: the row sees such a value itself, and its result stands.
 template <int HD, bool KEY, bool FWD, bool CAP, bool BIAS>
-__device__ __noinline__ void redo_row(const Params& p, int h, int kh, int row, int lo, int hi, float m2, float D,
-                                      float* out, float* out2) {
+__device__ __forceinline__ bool redo_row(const Params& p, int h, int kh, int row, int lo, int hi, float m2, float D,
+                                         float* out, float* out2) {
   constexpr int W = HD / 32;
   const int lane = threadIdx.x & 31;
   const float slope2 = BIAS ? p.slopes[h] * kLog2e : 0.f;
@@ -234,6 +250,7 @@ __device__ __noinline__ void redo_row(const Params& p, int h, int kh, int row, i
   const bf16* k = p.k + int64_t(kh) * HD;
   const bf16* v = p.v + int64_t(kh) * HD;
   const bf16* g = FWD ? nullptr : p.d_o + int64_t(h) * HD;
+#pragma unroll 1
   for (int j0 = lo; j0 < hi; j0 += 32) {
     const int j = j0 + lane;
     float pj = 0.f, dsj = 0.f;
@@ -244,12 +261,14 @@ __device__ __noinline__ void redo_row(const Params& p, int h, int kh, int row, i
           pair_score<CAP, BIAS>(p, dot_rows<HD>(q + i * p.ldq, k + c * p.ldk), slope2, int(i - c), slack);
       float mm = m2, dd = D;
       if constexpr (KEY) {
-        mm = p.lse[int64_t(h) * p.plan.T + i] * kLog2e;
-        dd = p.D[int64_t(h) * p.plan.T + i];
+        mm = -p.nl[int64_t(h) * p.plan.tiles * BT + i];
+        dd = -p.nd[int64_t(h) * p.plan.tiles * BT + i];
       }
       pj = ex2(s - mm);
       if constexpr (!FWD) dsj = pj * slack * (dot_rows<HD>(g + i * p.lddo, v + c * p.ldv) - dd);
     }
+    float bad = 0.f;
+#pragma unroll 1
     for (int u = 0; u < 32 && j0 + u < hi; ++u) {
       const int64_t j2 = j0 + u;
       const float pu = __shfl_sync(0xffffffffu, pj, u), du = __shfl_sync(0xffffffffu, dsj, u);
@@ -262,18 +281,219 @@ __device__ __noinline__ void redo_row(const Params& p, int h, int kh, int row, i
         for (int e = 0; e < W; ++e) out2[e] = fmaf(pu, to_f(y[lane * W + e]), out2[e]);
       }
     }
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      bad = fmaf(out[e], 0.f, bad);
+      if constexpr (KEY && !FWD) bad = fmaf(out2[e], 0.f, bad);
+    }
+    if (__any_sync(0xffffffffu, bad != 0.f)) return false;
   }
+  return true;
+}
+
+template <int HD>
+__device__ __forceinline__ bool row_finite(const bf16* x) {
+  float bad = 0.f;
+  for (int c = 0; c < HD; c += 8) {
+    float v[8];
+    Vec<bf16>::load(x + c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bad = fmaf(v[e], 0.f, bad);
+  }
+  return bad == 0.f;
+}
+
+// Rows of this warp (`rows`: lanes whose result is not finite) that a masked column's NaN or ∞ reached through
+// the second products, over the columns [c0, c1) of the tiles the item met.  The first and the last column
+// that hold one are found once; a row is done over if it masks one of them.  A lane writes the HD/32 elements
+// it summed if they are of the warp's part (part_n parts of HD/part_n columns).
+template <int HD, bool KEY, bool FWD, bool CAP, bool BIAS>
+__device__ __noinline__ void repair(const Params& p, int h0, int heads, int kh, int row, int2 iv, uint32_t rows,
+                                    int c0, int c1, float m2, float D, float inv, int part, int part_n, int split) {
+  constexpr int W = HD / 32;
+  const int lane = threadIdx.x & 31;
+  c1 = min(c1, int(p.plan.T));
+  auto clean = [&](int c) {
+    if constexpr (FWD) return row_finite<HD>(p.v + int64_t(c) * p.ldv + int64_t(kh) * HD);
+    else if constexpr (!KEY) return row_finite<HD>(p.k + int64_t(c) * p.ldk + int64_t(kh) * HD);
+    else for (int h = h0; h < h0 + heads; ++h)
+      if (!row_finite<HD>(p.q + int64_t(c) * p.ldq + int64_t(h) * HD) ||
+          !row_finite<HD>(p.d_o + int64_t(c) * p.lddo + int64_t(h) * HD)) return false;
+    return true;
+  };
+  int first = 0x7fffffff, last = -1;
+#pragma unroll 1
+  for (int b = c0; b < c1 && first == 0x7fffffff; b += 32) {
+    const uint32_t m = __ballot_sync(0xffffffffu, b + lane < c1 && !clean(b + lane));
+    if (m) first = b + __ffs(m) - 1;
+  }
+  if (first == 0x7fffffff) return;
+#pragma unroll 1
+  for (int e = c1; e > c0 && last < 0; e -= 32) {
+    const int c = e - 32 + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, c >= c0 && !clean(c));
+    if (m) last = e - 1 - __clz(m);
+  }
+  rows &= __ballot_sync(0xffffffffu, first < iv.x || last >= iv.y);
+#pragma unroll 1
+  while (rows) {
+    const int src = __ffs(rows) - 1;
+    rows &= rows - 1;
+    const int rw = __shfl_sync(0xffffffffu, row, src), lo = __shfl_sync(0xffffffffu, iv.x, src),
+              hi = __shfl_sync(0xffffffffu, iv.y, src);
+    const float mm = __shfl_sync(0xffffffffu, m2, src), dd = __shfl_sync(0xffffffffu, D, src),
+                mul = __shfl_sync(0xffffffffu, inv, src);
+    float a1[W] = {}, a2[W] = {};
+    bool ok = true;
+#pragma unroll 1
+    for (int h = h0; h < h0 + heads && ok; ++h)
+      ok = redo_row<HD, KEY, FWD, CAP, BIAS>(p, h, kh, rw, lo, hi, mm, dd, a1, a2);
+    __syncwarp();
+    if (!ok || lane / (32 / part_n) != part) continue;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int64_t c = int64_t(KEY ? kh : h0) * HD + lane * W + e;
+      if constexpr (FWD) {
+        const float x = a1[e] * mul;
+        const bf16 hi_x = __float2bfloat16_rn(x);
+        p.o[int64_t(rw) * p.ldo + c] = hi_x;
+        if (p.o_lo) p.o_lo[int64_t(rw) * p.ldo + c] = __float2bfloat16_rn(x - __bfloat162float(hi_x));
+      } else if constexpr (!KEY) {
+        p.dq[int64_t(rw) * p.lddq + c] = __float2bfloat16_rn(a1[e] * p.scale);
+      } else if (p.split > 1) {
+        const int64_t at = (int64_t(split) * p.plan.T + rw) * (int64_t(p.Hkv) * HD) + c;
+        p.part_k[at] = a1[e];
+        p.part_v[at] = a2[e];
+      } else {
+        p.dk[int64_t(rw) * p.lddk + c] = __float2bfloat16_rn(a1[e] * p.scale);
+        p.dv[int64_t(rw) * p.lddv + c] = __float2bfloat16_rn(a2[e]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ work items
+
+// Asks for the index of a block of this grid that has not started; 16 bytes land at dst.
+__device__ __forceinline__ void take_block(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// The index, or −1 where none was left (no further request may follow then).
+__device__ __forceinline__ int taken_block(uint32_t src) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+      : "=r"(x)
+      : "r"(src)
+      : "memory");
+  return x;
+}
+
+// A contiguous copy into shared memory that completes on an mbarrier (16-byte units).
+__device__ __forceinline__ void copy_in(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// A work item as the producer leaves it for the other warps.
+struct alignas(16) Item {
+  int h;             // query head, or (key pass) key head; −1: no more
+  int tile;          // first tile of the pair; the row tile
+  int a, b;          // column tiles of the pair's union; (key pass) first query head, heads
+  int4 r0, r1;       // ranges (r1: the pair's second tile, or (split) in x)
+};
+struct Queue {
+  Item item[2];
+  uint4 reply;
+  uint64_t full[2], empty[2], got;
+};
+
+template <bool KEY, bool PAIR>
+__device__ __forceinline__ Item describe(const Params& p, int i) {
+  Item it;
+  const int per = KEY ? p.Hkv * p.split : p.H;
+  const int n = i / per, h = i - n * per;
+  if constexpr (PAIR) {
+    const int4 x = __ldg(p.plan.pairs + 3 * n);
+    it.tile = x.x;
+    it.a = x.y;
+    it.b = x.z;
+    it.r0 = __ldg(p.plan.pairs + 3 * n + 1);
+    it.r1 = __ldg(p.plan.pairs + 3 * n + 2);
+    it.h = h;
+  } else {
+    const int4* rec = (KEY ? p.plan.ks : p.plan.qs) + 2 * n;
+    it.tile = __ldg(rec).x;
+    it.r0 = __ldg(rec + 1);
+    const int sp = KEY ? h / p.Hkv : 0;
+    it.h = KEY ? h - sp * p.Hkv : h;
+    it.a = KEY ? it.h * p.group + sp * p.share : h;
+    it.b = KEY ? min(p.share, p.group - sp * p.share) : 1;
+    it.r1 = make_int4(sp, 0, 0, 0);
+  }
+  return it;
+}
+
+// The producer's side of the queue.
+struct Source {
+  Queue* q;
+  uint32_t n = 0;  // items published
+  __device__ __forceinline__ bool publish(const Item& it, uint64_t limit) {
+    const uint32_t s = n & 1;
+    if (!spin(smem_u32(&q->empty[s]), ((n >> 1) & 1) ^ 1, limit)) return false;
+    q->item[s] = it;
+    mbar_arrive(smem_u32(&q->full[s]));
+    ++n;
+    return true;
+  }
+  // The next block's index; a request always ends before the block does.
+  __device__ __forceinline__ int take() {
+    const uint32_t bar = smem_u32(&q->got);
+    fence_proxy_async_smem();  // the last reply has been read
+    mbar_expect_tx(bar, 16);
+    take_block(smem_u32(&q->reply), bar);
+    if (!mbar_wait(bar, (n - 1) & 1)) return -1;
+    return taken_block(smem_u32(&q->reply));
+  }
+};
+// Everybody else's: item n, false when the wait ran out.  All lanes of a warp, or one thread (WARP false).
+template <bool WARP>
+__device__ __forceinline__ bool next_item(Queue* q, uint32_t n, Item& it, uint64_t limit) {
+  const uint32_t s = n & 1;
+  bool ok = spin(smem_u32(&q->full[s]), (n >> 1) & 1, limit);
+  if (WARP) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return false;
+  it = q->item[s];
+  if (WARP) __syncwarp();
+  if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&q->empty[s]));
+  return true;
+}
+__device__ __forceinline__ void queue_init(Queue* q, int readers) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(smem_u32(&q->full[i]), 1);
+    mbar_init(smem_u32(&q->empty[i]), readers);
+  }
+  mbar_init(smem_u32(&q->got), 1);
 }
 
 // ------------------------------------------------------------------------------ forward
 //
-// One persistent CTA per SM.  A work item is a head and a pair of 128-query tiles, one tile per stream;
-// the two streams share the K and V tiles (a tile that only one of them meets is released by the other).
-// Warps: 0 TMA, 1 and 2 the streams' MMA issuers (1 owns TMEM), 3 idle, 4–7 and 8–11 the streams'
-// softmax rows, one query row per thread.  While one stream's rows are at their exponentials the tensor
-// core works for the other.
-// TMEM per stream: S [0, 128) | P | O.  hd 64 has room for P of its own ([128, 160) … 64 columns), so S of
-// the next tile is computed as soon as the rows have read this one; with hd 128 P lies over S.
+// A work item is a head and a pair of 128-query tiles, one tile per stream; the two streams share the K and V
+// tiles (a tile that only one of them meets is released for the other).  Warps: 0 TMA, 1 (and 2) MMA issuers
+// (1 owns TMEM), 4–7 and 8–11 the streams' softmax rows, one query row per thread.
+// TMEM per stream, 256 columns: S [0, 128) | P | O.  With hd 64 P has 64 columns of its own, S of the next tile
+// is computed as soon as the rows have read this one, and each stream has an issuer.  With hd 128 P lies over
+// S, so a stream's rows wait while P V and the next S are computed: one thread issues both streams' products
+// in turn (P V and S of stream 0, then of stream 1), which sets the streams half a period apart — one is
+// at its exponentials while the other's products run.
 constexpr int kThreadsFwd = 384;
 constexpr uint32_t kFwdRegsCtl = 72, kFwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
 
@@ -282,69 +502,56 @@ struct FwdCfg {
   static constexpr int QT = HD / 64 * TILE;         // bytes of a 128-row tile
   static constexpr int RING = HD == 64 ? 4 : 2;     // K (and V) tiles in flight
   static constexpr bool OWN_P = HD == 64;
+  static constexpr int ISSUERS = OWN_P ? 2 : 1;
   static constexpr int Q = 0;
   static constexpr int K = Q + 2 * QT;
   static constexpr int V = K + RING * QT;
   static constexpr int BARS = V + RING * QT;
-  static constexpr int BYTES = 1024 + BARS + 512;
+  static constexpr int BYTES = 1024 + BARS + 1024;
 };
 
-struct FwdItem {
-  int h, kh, t0;        // head, key head, first tile of the pair
-  int4 r0, r1;          // the tiles' key ranges
-  int a, b;             // key tiles that either meets
+template <int HD>
+struct FwdBars {
+  Queue queue;
+  uint64_t k_full[FwdCfg<HD>::RING], k_empty[FwdCfg<HD>::RING], v_full[FwdCfg<HD>::RING], v_empty[FwdCfg<HD>::RING];
+  struct Stream {
+    uint64_t q_full, q_empty, s_full, s_free, p_full, pv_done;
+  } st[2];
+  uint64_t mma_done[2];
+  uint32_t tmem, abort;
 };
-
-__device__ __forceinline__ int4 range_of(const int4* r, int tile, int tiles) {
-  return tile < tiles ? __ldg(r + tile) : make_int4(0, 0, 0, 0);
-}
-__device__ __forceinline__ FwdItem fwd_item(const Params& p, int i) {
-  FwdItem it;
-  const int n = i / p.H;
-  it.h = i - n * p.H;
-  it.kh = it.h / p.group;
-  it.t0 = 2 * __ldg(p.plan.pair_order + n);
-  it.r0 = range_of(p.plan.qrange, it.t0, p.plan.tiles);
-  it.r1 = range_of(p.plan.qrange, it.t0 + 1, p.plan.tiles);
-  const bool e0 = it.r0.y <= it.r0.x, e1 = it.r1.y <= it.r1.x;
-  it.a = e0 ? it.r1.x : e1 ? it.r0.x : min(it.r0.x, it.r1.x);
-  it.b = e0 ? it.r1.y : e1 ? it.r0.y : max(it.r0.y, it.r1.y);
-  return it;
-}
-// Work item of round r for this CTA (rounds alternate direction over the CTAs; the items come longest first).
-__device__ __forceinline__ int snake(int r) {
-  const int G = int(gridDim.x), c = int(blockIdx.x);
-  return r * G + ((r & 1) ? G - 1 - c : c);
-}
 
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreadsFwd, 1)
     attnm_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   using C = FwdCfg<HD>;
-  constexpr uint32_t TCOLS = 512;
+  constexpr uint32_t TCOLS = 512, RING = C::RING;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
-  uint64_t* k_full = bars;                // [RING]
-  uint64_t* k_empty = k_full + C::RING;   // one arrival per stream
-  uint64_t* v_full = k_empty + C::RING;
-  uint64_t* v_empty = v_full + C::RING;
-  uint64_t* stream_bars = v_empty + C::RING;  // per stream: q_full, q_empty, s_full, s_free, p_full, pv_done, mma_done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stream_bars + 14);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  FwdBars<HD>& B = *reinterpret_cast<FwdBars<HD>*>(smem + C::BARS);
+  static_assert(sizeof(FwdBars<HD>) <= 1024, "barrier space");
+  volatile uint32_t* abort_flag = &B.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::RING; ++i) {
-      mbar_init(smem_u32(&k_full[i]), 1);
-      mbar_init(smem_u32(&k_empty[i]), 2);
-      mbar_init(smem_u32(&v_full[i]), 1);
-      mbar_init(smem_u32(&v_empty[i]), 2);
+    queue_init(&B.queue, 8 + C::ISSUERS);
+    for (uint32_t i = 0; i < RING; ++i) {
+      mbar_init(smem_u32(&B.k_full[i]), 1);
+      mbar_init(smem_u32(&B.k_empty[i]), C::ISSUERS);
+      mbar_init(smem_u32(&B.v_full[i]), 1);
+      mbar_init(smem_u32(&B.v_empty[i]), C::ISSUERS);
     }
-    for (int st = 0; st < 2; ++st)
-      for (int i = 0; i < 7; ++i) mbar_init(smem_u32(&stream_bars[7 * st + i]), (i == 3 || i == 4) ? 4 : 1);
-    *abort_flag = 0;
+    for (int st = 0; st < 2; ++st) {
+      mbar_init(smem_u32(&B.st[st].q_full), 1);
+      mbar_init(smem_u32(&B.st[st].q_empty), 1);
+      mbar_init(smem_u32(&B.st[st].s_full), 1);
+      mbar_init(smem_u32(&B.st[st].s_free), 4);
+      mbar_init(smem_u32(&B.st[st].p_full), 4);
+      mbar_init(smem_u32(&B.st[st].pv_done), 1);
+      mbar_init(smem_u32(&B.mma_done[st]), 1);
+    }
+    B.abort = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -353,147 +560,200 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
     prefetch_tmap(&tmV);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), TCOLS);
+    tmem_alloc(smem_u32(&B.tmem), TCOLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = B.tmem;
   pdl_begin();
   auto give_up = [&]() {
     *abort_flag = 1;
     flag_error(p.flag, XT_DEVERR_TIMEOUT);
   };
-  const bool ok_plan = attn_plan::valid(p.plan);
-  if (!ok_plan && blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.flag, XT_DEVERR_PLAN);
-  const int items = ok_plan ? (p.plan.tiles + 1) / 2 * p.H : 0;
 
   const int wg = warp >> 2;
   if (wg == 0) {
     regs_dec<kFwdRegsCtl>();
     if (warp == 0 && lane == 0) {
-      // -------------------------------------------------------------- TMA producer
-      uint32_t nq = 0, n = 0;  // items, K / V tiles so far
+      // -------------------------------------------------------------- TMA producer, work items
+      uint32_t n = 0, nq[2] = {0, 0};  // K / V tiles and Q tiles so far
       bool ok = true;
+      Source src{&B.queue};
+      Item it;
+      it.h = -1;
+      if (attn_plan::valid(p.plan)) it = describe<false, true>(p, int(blockIdx.x));
+      else if (blockIdx.x == 0) flag_error(p.flag, XT_DEVERR_PLAN);
 #pragma unroll 1
-      for (int r = 0; r * int(gridDim.x) < items && ok && !*abort_flag; ++r) {
-        const int i = snake(r);
-        if (i >= items) continue;
-        const FwdItem it = fwd_item(p, i);
+      for (;;) {
+        if (!src.publish(it, p.wait_ns)) { ok = false; break; }
+        if (it.h < 0) break;
+        const int kh = it.h / p.group;
 #pragma unroll 1
         for (int st = 0; st < 2 && ok; ++st) {
-          uint64_t* b = stream_bars + 7 * st;
-          if (!mbar_wait(smem_u32(&b[1]), (nq & 1) ^ 1, p.wait_ns)) { ok = false; break; }
-          mbar_expect_tx(smem_u32(&b[0]), C::QT);
-          Mma<HD>::load(sb + C::Q + st * C::QT, &tmQ, smem_u32(&b[0]), it.h, it.t0 + st);
+          auto& b = B.st[st];
+          if (!mbar_wait(smem_u32(&b.q_empty), (nq[st] & 1) ^ 1, p.wait_ns)) { ok = false; break; }
+          mbar_expect_tx(smem_u32(&b.q_full), C::QT);
+          Mma<HD>::load(sb + C::Q + st * C::QT, &tmQ, smem_u32(&b.q_full), it.h, it.tile + st);
+          ++nq[st];
         }
-        if (!ok) break;
-        ++nq;
 #pragma unroll 1
-        for (int j = it.a; j < it.b; ++j, ++n) {
-          const uint32_t s = n % C::RING, ph = ((n / C::RING) & 1) ^ 1;
-          if (*abort_flag || !mbar_wait(smem_u32(&k_empty[s]), ph, p.wait_ns)) { ok = false; break; }
-          mbar_expect_tx(smem_u32(&k_full[s]), C::QT);
-          Mma<HD>::load(sb + C::K + s * C::QT, &tmK, smem_u32(&k_full[s]), it.kh, j);
-          if (!mbar_wait(smem_u32(&v_empty[s]), ph, p.wait_ns)) {  // K of this tile is in flight: drained below
+        for (int j = it.a; j < it.b && ok; ++j, ++n) {
+          const uint32_t s = n % RING, ph = ((n / RING) & 1) ^ 1;
+          if (*abort_flag || !mbar_wait(smem_u32(&B.k_empty[s]), ph, p.wait_ns)) { ok = false; break; }
+          mbar_expect_tx(smem_u32(&B.k_full[s]), C::QT);
+          Mma<HD>::load(sb + C::K + s * C::QT, &tmK, smem_u32(&B.k_full[s]), kh, j);
+          if (!mbar_wait(smem_u32(&B.v_empty[s]), ph, p.wait_ns)) {
             ok = false;
-            mbar_wait(smem_u32(&k_full[s]), (n / C::RING) & 1);
+            mbar_wait(smem_u32(&B.k_full[s]), (n / RING) & 1);  // this K is in flight
             break;
           }
-          mbar_expect_tx(smem_u32(&v_full[s]), C::QT);
-          Mma<HD>::load(sb + C::V + s * C::QT, &tmV, smem_u32(&v_full[s]), it.kh, j);
+          mbar_expect_tx(smem_u32(&B.v_full[s]), C::QT);
+          Mma<HD>::load(sb + C::V + s * C::QT, &tmV, smem_u32(&B.v_full[s]), kh, j);
         }
+        if (!ok || *abort_flag) { ok = false; break; }
+        const int next = src.take();
+        if (next >= 0) it = describe<false, true>(p, next);
+        else it.h = -1;
       }
       if (!ok) give_up();
       // bounded wait for the fills that may still be in flight
       bool drained = true;
-      if (nq > 0)
-        for (int st = 0; st < 2; ++st) drained &= mbar_wait(smem_u32(&stream_bars[7 * st]), (nq - 1) & 1);
-      for (uint32_t m = 0; m < (n < uint32_t(C::RING) ? n : uint32_t(C::RING)); ++m) {
+      for (int st = 0; st < 2; ++st)
+        if (nq[st] > 0) drained &= mbar_wait(smem_u32(&B.st[st].q_full), (nq[st] - 1) & 1);
+      for (uint32_t m = 0; m < (n < RING ? n : RING); ++m) {
         const uint32_t g = n - 1 - m;
-        drained &= mbar_wait(smem_u32(&k_full[g % C::RING]), (g / C::RING) & 1);
-        drained &= mbar_wait(smem_u32(&v_full[g % C::RING]), (g / C::RING) & 1);
+        drained &= mbar_wait(smem_u32(&B.k_full[g % RING]), (g / RING) & 1);
+        drained &= mbar_wait(smem_u32(&B.v_full[g % RING]), (g / RING) & 1);
       }
       if (!drained) give_up();
-    } else if ((warp == 1 || warp == 2) && lane == 0) {
-      // -------------------------------------------------------------- MMA issuer of stream warp − 1
-      const int st = warp - 1;
-      uint64_t* b = stream_bars + 7 * st;
-      const uint32_t tS = tbase + uint32_t(256 * st), tP = tS + (C::OWN_P ? 128u : 0u), tO = tbase + 256 * st + (C::OWN_P ? 192u : 128u);
-      const uint32_t qs = sb + C::Q + st * C::QT;
-      uint32_t n0 = 0, nq = 0, g = 0;  // K / V tiles of earlier items, items, score tiles of this stream
+    } else if (warp >= 1 && warp <= C::ISSUERS && lane == 0) {
+      // -------------------------------------------------------------- MMA issuer: of stream warp − 1, or of both
+      const int st0 = C::OWN_P ? warp - 1 : 0, st1 = C::OWN_P ? warp - 1 : 1;
+      uint32_t n0 = 0;                       // K / V tiles of earlier items
+      uint32_t g[2] = {0, 0};                // score tiles of each stream
       bool ok = true;
-      auto pv = [&](uint32_t n, uint32_t gg, bool first) -> bool {  // O += P V of ring tile n, score tile gg
-        const uint32_t s = n % C::RING;
-        if (!mbar_wait_spin(smem_u32(&b[4]), gg & 1, p.wait_ns) ||
-            !mbar_wait_spin(smem_u32(&v_full[s]), (n / C::RING) & 1, p.wait_ns)) return false;
+      auto tS = [&](int st) { return tbase + uint32_t(256 * st); };
+      auto pv = [&](int st, uint32_t n, bool first) -> bool {  // O += P V of ring tile n, the stream's last score tile
+        auto& b = B.st[st];
+        const uint32_t s = n % RING;
+        const uint32_t gg = C::OWN_P ? g[0] : g[st];
+        if (!spin(smem_u32(&b.p_full), (gg - 1) & 1, p.wait_ns) ||
+            !spin(smem_u32(&B.v_full[s]), (n / RING) & 1, p.wait_ns)) return false;
         tc_fence_after();
-        Mma<HD>::tn(tO, tP, 32, sb + C::V + s * C::QT, first);
-        tc_commit(smem_u32(&v_empty[s]));
-        tc_commit(smem_u32(&b[5]));
+        Mma<HD>::tn(tS(st) + (C::OWN_P ? 192u : 128u), tS(st) + (C::OWN_P ? 128u : 0u), 32, sb + C::V + s * C::QT,
+                    first);
+        tc_commit(smem_u32(&b.pv_done));
         return true;
       };
 #pragma unroll 1
-      for (int r = 0; r * int(gridDim.x) < items && ok && !*abort_flag; ++r) {
-        const int i = snake(r);
-        if (i >= items) continue;
-        const FwdItem it = fwd_item(p, i);
-        const int4 rg = st ? it.r1 : it.r0;
-        if (!mbar_wait_spin(smem_u32(&b[0]), nq & 1, p.wait_ns)) { ok = false; break; }
-        ++nq;
-        tc_fence_after();
-        int pend = -1;  // ring tile whose P V is still to be issued
-        bool first = true;
-        bool held = true;  // Q still needed
-#pragma unroll 1
-        for (int j = it.a; j < it.b && ok; ++j) {
-          const uint32_t n = n0 + uint32_t(j - it.a), s = n % C::RING, ph = (n / C::RING) & 1;
-          const bool mine = j >= rg.x && j < rg.y;
-          if (*abort_flag) { ok = false; break; }
-          if (pend >= 0 && (!mine || !C::OWN_P)) {
-            if (!pv(uint32_t(pend), g - 1, first)) { ok = false; break; }
-            first = false;
-            pend = -1;
-          }
-          if (!mbar_wait_spin(smem_u32(&k_full[s]), ph, p.wait_ns)) { ok = false; break; }
-          if (!mine) {  // the other stream's tile
-            mbar_arrive(smem_u32(&k_empty[s]));
-            if (!mbar_wait_spin(smem_u32(&v_full[s]), ph, p.wait_ns)) { ok = false; break; }
-            mbar_arrive(smem_u32(&v_empty[s]));
-            continue;
-          }
-          if (C::OWN_P && !mbar_wait_spin(smem_u32(&b[3]), (g & 1) ^ 1, p.wait_ns)) { ok = false; break; }
-          tc_fence_after();
-          Mma<HD>::nt(tS, qs, sb + C::K + s * C::QT);
-          tc_commit(smem_u32(&k_empty[s]));
-          tc_commit(smem_u32(&b[2]));
-          if (j == rg.y - 1) {
-            tc_commit(smem_u32(&b[1]));
-            held = false;
-          }
-          if (pend >= 0) {
-            if (!pv(uint32_t(pend), g - 1, first)) { ok = false; break; }
-            first = false;
-          }
-          pend = int(n);
-          ++g;
-        }
+      for (uint32_t ni = 0; ok; ++ni) {
+        Item it;
+        if (*abort_flag || !next_item<false>(&B.queue, ni, it, p.wait_ns)) { ok = false; break; }
+        if (it.h < 0) break;
+        for (int st = st0; st <= st1 && ok; ++st) ok = spin(smem_u32(&B.st[st].q_full), ni & 1, p.wait_ns);
         if (!ok) break;
-        if (pend >= 0 && !pv(uint32_t(pend), g - 1, first)) { ok = false; break; }
-        if (held) mbar_arrive(smem_u32(&b[1]));
+        tc_fence_after();
+        if constexpr (C::OWN_P) {
+          // S of a tile goes ahead of P V of the one before
+          auto& b = B.st[st0];
+          const int4 rg = st0 ? it.r1 : it.r0;
+          int pend = -1;  // ring tile whose P V is still to be issued
+          bool first = true, held = true;
+#pragma unroll 1
+          for (int j = it.a; j < it.b; ++j) {
+            const uint32_t n = n0 + uint32_t(j - it.a), s = n % RING, ph = (n / RING) & 1;
+            const bool mine = j >= rg.x && j < rg.y;
+            if (*abort_flag) { ok = false; break; }
+            if (pend >= 0 && !mine) {
+              if (!pv(st0, uint32_t(pend), first)) { ok = false; break; }
+              tc_commit(smem_u32(&B.v_empty[uint32_t(pend) % RING]));
+              first = false;
+              pend = -1;
+            }
+            if (!spin(smem_u32(&B.k_full[s]), ph, p.wait_ns)) { ok = false; break; }
+            if (!mine) {  // the other stream's tile
+              mbar_arrive(smem_u32(&B.k_empty[s]));
+              if (!spin(smem_u32(&B.v_full[s]), ph, p.wait_ns)) { ok = false; break; }
+              mbar_arrive(smem_u32(&B.v_empty[s]));
+              continue;
+            }
+            if (!spin(smem_u32(&b.s_free), (g[0] & 1) ^ 1, p.wait_ns)) { ok = false; break; }
+            tc_fence_after();
+            Mma<HD>::nt(tS(st0), sb + C::Q + st0 * C::QT, sb + C::K + s * C::QT);
+            tc_commit(smem_u32(&B.k_empty[s]));
+            tc_commit(smem_u32(&b.s_full));
+            if (j == rg.y - 1) {
+              tc_commit(smem_u32(&b.q_empty));
+              held = false;
+            }
+            if (pend >= 0) {
+              if (!pv(st0, uint32_t(pend), first)) { ok = false; break; }
+              tc_commit(smem_u32(&B.v_empty[uint32_t(pend) % RING]));
+              first = false;
+            }
+            pend = int(n);
+            ++g[0];
+          }
+          if (!ok) break;
+          if (pend >= 0) {
+            if (!pv(st0, uint32_t(pend), first)) { ok = false; break; }
+            tc_commit(smem_u32(&B.v_empty[uint32_t(pend) % RING]));
+          }
+          if (held) mbar_arrive(smem_u32(&b.q_empty));
+        } else {
+          bool pend[2] = {false, false}, first[2] = {true, true}, held[2] = {true, true};
+#pragma unroll 1
+          for (int j = it.a; j <= it.b && ok; ++j) {  // one step more than tiles: the last P V
+            const uint32_t n = n0 + uint32_t(j - it.a), s = n % RING;
+            if (*abort_flag) { ok = false; break; }
+            if (j < it.b && !spin(smem_u32(&B.k_full[s]), (n / RING) & 1, p.wait_ns)) { ok = false; break; }
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              auto& b = B.st[st];
+              const int4 rg = st ? it.r1 : it.r0;
+              if (pend[st]) {
+                if (!pv(st, n - 1, first[st])) { ok = false; break; }
+                first[st] = false;
+                pend[st] = false;
+              }
+              if (j < it.b && j >= rg.x && j < rg.y) {
+                tc_fence_after();
+                Mma<HD>::nt(tS(st), sb + C::Q + st * C::QT, sb + C::K + s * C::QT);
+                tc_commit(smem_u32(&b.s_full));
+                if (j == rg.y - 1) {
+                  tc_commit(smem_u32(&b.q_empty));
+                  held[st] = false;
+                }
+                pend[st] = true;
+                ++g[st];
+              }
+            }
+            if (!ok) break;
+            if (j < it.b) tc_commit(smem_u32(&B.k_empty[s]));
+            if (j > it.a) {
+              const uint32_t m = n - 1;
+              if (!spin(smem_u32(&B.v_full[m % RING]), (m / RING) & 1, p.wait_ns)) { ok = false; break; }
+              tc_commit(smem_u32(&B.v_empty[m % RING]));
+            }
+          }
+          if (!ok) break;
+          for (int st = 0; st < 2; ++st)
+            if (held[st]) mbar_arrive(smem_u32(&B.st[st].q_empty));
+        }
         n0 += uint32_t(it.b - it.a);
       }
       if (!ok) give_up();
       // every MMA issued has completed (also after a give-up) before TMEM is released
-      tc_commit(smem_u32(&b[6]));
-      if (!mbar_wait(smem_u32(&b[6]), 0)) give_up();
+      tc_commit(smem_u32(&B.mma_done[warp - 1]));
+      if (!mbar_wait(smem_u32(&B.mma_done[warp - 1]), 0)) give_up();
     }
   } else {
     regs_inc<kFwdRegsRows>();
     // ---------------------------------------------------------------- softmax rows, epilogue
     const int st = wg - 1;
-    uint64_t* b = stream_bars + 7 * st;
+    auto& b = B.st[st];
     const int qw = warp & 3;
     const int rr = qw * 32 + lane;
     const uint32_t lane_off = uint32_t(qw * 32) << 16;
@@ -501,24 +761,33 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
                    tO = tS + (C::OWN_P ? 192u : 128u);
     uint32_t g = 0;
 #pragma unroll 1
-    for (int r = 0; r * int(gridDim.x) < items; ++r) {
-      const int i = snake(r);
-      if (i >= items) continue;
-      if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      const FwdItem it = fwd_item(p, i);
-      const int tile = it.t0 + st;
+    for (uint32_t ni = 0;; ++ni) {
+      bool ok = !__shfl_sync(0xffffffffu, *abort_flag, 0);
+      int h, tile;
+      int4 rg;
+      {
+        Item it;
+        it.h = -1;
+        if (ok) ok = next_item<true>(&B.queue, ni, it, p.wait_ns);
+        h = it.h;
+        tile = it.tile + st;
+        rg = st ? it.r1 : it.r0;
+      }
+      if (!ok) {
+        if (lane == 0) give_up();
+        break;
+      }
+      if (h < 0) break;
       if (tile >= p.plan.tiles) continue;
-      const int4 rg = st ? it.r1 : it.r0;
       const int row = tile * BT + rr;
       const int2 iv = __ldg(p.plan.q_iv + row);
-      const float slope2 = BIAS ? __ldg(p.slopes + it.h) * kLog2e : 0.f;
+      const float slope2 = BIAS ? __ldg(p.slopes + h) * kLog2e : 0.f;
       float m = -INFINITY;  // running max, of the raw scores or (CAP, BIAS) of s·log₂e
       float l = 0.f;        // running Σ 2^(s − m)
       const float unit = (CAP || BIAS) ? 1.f : p.sc;
-      bool ok = true;
 #pragma unroll 1
       for (int j = rg.x; j < rg.y; ++j, ++g) {
-        if (!warp_wait(smem_u32(&b[2]), g & 1, p.wait_ns)) { ok = false; break; }
+        if (!warp_wait(smem_u32(&b.s_full), g & 1, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[128];
 #pragma unroll
@@ -527,7 +796,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         if (C::OWN_P) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&b[3]));
+          if (lane == 0) mbar_arrive(smem_u32(&b.s_free));
         }
         if constexpr (CAP || BIAS)
           to_log2<128, CAP, BIAS>(s, p, slope2, j * BT - row, j < tile ? 1 : j > tile ? -1 : 0);
@@ -547,7 +816,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         const bool need = m_new > m && (m == -INFINITY || (m_new - m) * unit > kRescale);
         // the previous tile's P V is complete before P is rewritten and O rescaled (with P over S the
         // scores' arrival says so: they were computed after it)
-        if (C::OWN_P && !warp_wait(smem_u32(&b[5]), (g & 1) ^ 1, p.wait_ns)) { ok = false; break; }
+        if (C::OWN_P && !warp_wait(smem_u32(&b.pv_done), (g & 1) ^ 1, p.wait_ns)) { ok = false; break; }
         if (j > rg.x && __any_sync(0xffffffffu, need)) {
           if (C::OWN_P) tc_fence_after();
           const float a = need ? exp2f((m - m_new) * unit) : 1.f;
@@ -588,9 +857,9 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&b[4]));
+        if (lane == 0) mbar_arrive(smem_u32(&b.p_full));
       }
-      if (ok && rg.y > rg.x && !warp_wait(smem_u32(&b[5]), (g - 1) & 1, p.wait_ns)) ok = false;
+      if (ok && rg.y > rg.x && !warp_wait(smem_u32(&b.pv_done), (g - 1) & 1, p.wait_ns)) ok = false;
       if (!ok) {
         if (lane == 0) give_up();
         break;
@@ -598,9 +867,10 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
       // ---- epilogue: O / l
       const bool seen = m > -INFINITY || l != 0.f;  // l: a NaN score leaves m at −∞
       const float inv = seen ? 1.f / l : 0.f;
+      const bool real = row < p.plan.T;
       tc_fence_after();
-      bf16* orow = p.o + int64_t(row) * p.ldo + int64_t(it.h) * HD;
-      bf16* lrow = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + int64_t(it.h) * HD : nullptr;
+      bf16* orow = p.o + int64_t(row) * p.ldo + int64_t(h) * HD;
+      bf16* lrow = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + int64_t(h) * HD : nullptr;
       float bad = 0.f;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
@@ -615,7 +885,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
           bad = fmaf(x, 0.f, bad);
           o[e] = __float_as_uint(x);
         }
-        if (row < p.plan.T) {
+        if (real) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint32_t hi[4], lo[4];
@@ -631,28 +901,11 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         }
       }
       tc_fence_before();
-      if (row < p.plan.T)
-        p.lse[int64_t(it.h) * p.plan.T + row] = seen ? (m * unit + log2f(l)) * kLn2 : -INFINITY;
-      // rows that a masked NaN or infinity reached through the products
-      uint32_t redo = __ballot_sync(0xffffffffu, bad != 0.f && l == l && row < p.plan.T);
-      while (redo) {
-        const int src = __ffs(redo) - 1;
-        redo &= redo - 1;
-        const int rw = __shfl_sync(0xffffffffu, row, src), lo = __shfl_sync(0xffffffffu, iv.x, src),
-                  hi = __shfl_sync(0xffffffffu, iv.y, src);
-        const float m2 = __shfl_sync(0xffffffffu, m * unit, src), iv2 = __shfl_sync(0xffffffffu, inv, src);
-        float acc[HD / 32] = {};
-        redo_row<HD, false, true, CAP, BIAS>(p, it.h, it.kh, rw, lo, hi, m2, 0.f, acc, nullptr);
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < HD / 32; ++e) {
-          const int64_t at = int64_t(rw) * p.ldo + int64_t(it.h) * HD + lane * (HD / 32) + e;
-          const float x = acc[e] * iv2;
-          const bf16 hi_x = __float2bfloat16_rn(x);
-          p.o[at] = hi_x;
-          if (p.o_lo) p.o_lo[at] = __float2bfloat16_rn(x - __bfloat162float(hi_x));
-        }
-      }
+      if (real) p.lse[int64_t(h) * p.plan.T + row] = seen ? (m * unit + log2f(l)) * kLn2 : -INFINITY;
+      const uint32_t rows = __ballot_sync(0xffffffffu, bad != 0.f && l == l && real);
+      if (rows)
+        repair<HD, false, true, CAP, BIAS>(p, h, 1, h / p.group, row, iv, rows, rg.x * BT, rg.y * BT, m * unit, 0.f,
+                                           inv, 0, 1, 0);
     }
   }
   __syncthreads();
@@ -665,48 +918,50 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // ------------------------------------------------------------------------------ backward
 //
 // One kernel for both directions.  KEY: an item is a key tile of a key head, a thread's row a key, the
-// columns queries; dK and dV sum over the query tiles that see the tile, for every query head of the group
-// in turn.  else: an item is a query tile of a head, a row a query, the columns keys; dQ sums over key tiles.
+// columns queries; dK and dV sum over the query tiles that see the tile, for the query heads of the group in
+// turn.  else: an item is a query tile of a head, a row a query, the columns keys; dQ sums over key tiles.
 // Per tile: S = (row tile)(column tile)ᵀ and dP likewise into TMEM; the rows form P = 2^(s − lse) and (KEY)
 // write it over S for dV += P dO; then dS = P∘(dP − D)∘(1 − tanh²) over dP for dK (dQ) += dS Q (K).
-// Eight row warps, two per TMEM lane quadrant, each half of a tile's 128 columns.  The next S is issued
-// before this tile's second products wherever its buffer allows (two S buffers, or KEY at hd 128 one), so
-// the tensor core works while the rows are at their exponentials.  The query pass also forms D (its rows'
-// dO·O) and leaves it in the workspace for the key pass, which follows it: no kernel of its own for D.
-constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 MMA, 2 and 3 idle, 4–11 rows
+//
+// A tile's time is the rows' chain of tensor-memory loads, exponentials, stores and barriers, several times the
+// work in it, so two chains run side by side: each half of a tile's 128 columns has its own MMA issuer, four row
+// warps (one per TMEM lane quadrant), S and dP buffers, accumulators and barriers; P and dS are elementwise, so
+// the halves never need each other until their accumulators are added at the end of an item, in the halves' order
+// (deterministic).  One chain's products and loads run during the other's exponentials.  The key pass at hd 128 has
+// tensor memory for one set of accumulators: there the halves' rows share one chain of 128 columns.
+// MEASURED-BWD
+//
+// The query pass also forms D (its rows' dO·O) and leaves −lse·log₂e and −D in the workspace, rows padded to
+// whole tiles, from where the key pass copies them in with each query tile: no kernel of its own for D.
+constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
 constexpr uint32_t kBwdRegsCtl = 72, kBwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
+constexpr int PW = BT / 2;        // columns of a row warp
 
 template <int HD, bool KEY>
 struct BwdCfg {
   static constexpr int QT = HD / 64 * TILE;
   static constexpr int RING = HD == 64 ? 4 : 2;          // column tiles (pairs) in flight
-  static constexpr int NS = (HD == 64 || !KEY) ? 2 : 1;  // S buffers
-  static constexpr uint32_t DP = NS * 128, ACC1 = DP + 128, ACC2 = ACC1 + HD;  // TMEM columns
+  static constexpr int CH = KEY && HD == 128 ? 1 : 2;    // chains
+  // TMEM columns: S, dP (the halves' side by side), each chain's accumulators dK or dQ, each chain's dV
+  static constexpr uint32_t DP = 128, ACC1 = 256, ACC2 = ACC1 + CH * HD;
   static constexpr int A = 0;                            // the row tiles: K, V or Q, dO
   static constexpr int R = A + 2 * QT;                   // ring of column tile pairs: Q, dO or K, V
-  static constexpr int VEC = R + RING * 2 * QT;          // 2 × (lse·log₂e, D) × 128 floats
-  static constexpr int BARS = VEC + 2048;
-  static constexpr int BYTES = 1024 + BARS + 256;
-  static_assert(ACC2 + (KEY ? HD : 0) <= 512, "TMEM columns");
+  static constexpr int VEC = R + RING * 2 * QT;          // (KEY) ring of −lse·log₂e and −D, 128 floats each
+  static constexpr int BARS = VEC + RING * 1024;
+  static constexpr int BYTES = 1024 + BARS + 512;
+  static_assert(ACC2 + (KEY ? CH * HD : 0) <= 512, "TMEM columns");
 };
 
-struct BwdItem {
-  int h0, kh, tile;   // first query head, key head, row tile
-  int4 rg;            // column tiles
-  int heads, n;       // query heads, column tiles in all
+template <int HD, bool KEY>
+struct BwdBars {
+  Queue queue;
+  uint64_t a_full, a_empty, r_full[BwdCfg<HD, KEY>::RING], r_empty[BwdCfg<HD, KEY>::RING];
+  struct Chain {
+    uint64_t s_full, s_free, dp_full, p_full, ds_full, acc_full, mma_done;
+  } ch[2];
+  uint64_t acc_free;
+  uint32_t tmem, abort;
 };
-template <bool KEY>
-__device__ __forceinline__ BwdItem bwd_item(const Params& p, int i) {
-  BwdItem it;
-  const int heads = KEY ? p.Hkv : p.H, n = i / heads, h = i - n * heads;
-  it.tile = __ldg((KEY ? p.plan.k_order : p.plan.q_order) + n);
-  it.rg = __ldg((KEY ? p.plan.krange : p.plan.qrange) + it.tile);
-  it.kh = KEY ? h : h / p.group;
-  it.h0 = KEY ? h * p.group : h;
-  it.heads = KEY ? p.group : 1;
-  it.n = max(it.rg.y - it.rg.x, 0) * it.heads;
-  return it;
-}
 
 template <int HD, bool KEY, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreadsBwd, 1)
@@ -714,32 +969,34 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ Params p) {
   using C = BwdCfg<HD, KEY>;
-  constexpr uint32_t TCOLS = 512;
+  constexpr uint32_t TCOLS = 512, RING = C::RING;
+  constexpr int CH = C::CH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
-  uint64_t* a_full = bars;
-  uint64_t* a_empty = bars + 1;
-  uint64_t* r_full = bars + 2;            // [RING]
-  uint64_t* r_empty = bars + 6;           // [RING]
-  uint64_t* s_full = bars + 10;           // [NS]
-  uint64_t* dp_full = bars + 12;
-  uint64_t* p_full = bars + 13;
-  uint64_t* ds_full = bars + 14;
-  uint64_t* acc_full = bars + 15;
-  uint64_t* vec_full = bars + 16;         // [2]
-  uint64_t* mma_done = bars + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* vec = reinterpret_cast<float*>(smem + C::VEC);
+  BwdBars<HD, KEY>& B = *reinterpret_cast<BwdBars<HD, KEY>*>(smem + C::BARS);
+  static_assert(sizeof(BwdBars<HD, KEY>) <= 512, "barrier space");
+  volatile uint32_t* abort_flag = &B.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 19; ++i) {
-      const int n = (i == 13 || i == 14) ? 8 : (i == 16 || i == 17) ? 256 : 1;
-      mbar_init(smem_u32(&bars[i]), n);
+    queue_init(&B.queue, 8 + CH);
+    mbar_init(smem_u32(&B.a_full), 1);
+    mbar_init(smem_u32(&B.a_empty), CH);
+    for (uint32_t i = 0; i < RING; ++i) {
+      mbar_init(smem_u32(&B.r_full[i]), 1);
+      mbar_init(smem_u32(&B.r_empty[i]), CH);
     }
-    *abort_flag = 0;
+    for (int c = 0; c < CH; ++c) {
+      mbar_init(smem_u32(&B.ch[c].s_full), 1);
+      mbar_init(smem_u32(&B.ch[c].s_free), 8 / CH);
+      mbar_init(smem_u32(&B.ch[c].dp_full), 1);
+      mbar_init(smem_u32(&B.ch[c].p_full), 8 / CH);
+      mbar_init(smem_u32(&B.ch[c].ds_full), 8 / CH);
+      mbar_init(smem_u32(&B.ch[c].acc_full), 1);
+      mbar_init(smem_u32(&B.ch[c].mma_done), 1);
+    }
+    mbar_init(smem_u32(&B.acc_free), 8);
+    B.abort = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -749,144 +1006,179 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
     prefetch_tmap(&tmDO);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), TCOLS);
+    tmem_alloc(smem_u32(&B.tmem), TCOLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = B.tmem;
   pdl_begin();
   auto give_up = [&]() {
     *abort_flag = 1;
     flag_error(p.flag, XT_DEVERR_TIMEOUT);
   };
-  const bool ok_plan = attn_plan::valid(p.plan);
-  if (!ok_plan && blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.flag, XT_DEVERR_PLAN);
-  const int items = ok_plan ? p.plan.tiles * (KEY ? p.Hkv : p.H) : 0;
-  const CUtensorMap *tmA1 = KEY ? &tmK : &tmQ, *tmA2 = KEY ? &tmV : &tmDO;
-  const CUtensorMap *tmR1 = KEY ? &tmQ : &tmK, *tmR2 = KEY ? &tmDO : &tmV;
+  const int64_t Tp = int64_t(p.plan.tiles) * BT;  // row stride of nl and nd
 
   if (warp < 4) {
     regs_dec<kBwdRegsCtl>();
     if (warp == 0 && lane == 0) {
-      // -------------------------------------------------------------- TMA producer
+      // -------------------------------------------------------------- TMA producer, work items
+      const CUtensorMap *tmA1 = KEY ? &tmK : &tmQ, *tmA2 = KEY ? &tmV : &tmDO;
+      const CUtensorMap *tmR1 = KEY ? &tmQ : &tmK, *tmR2 = KEY ? &tmDO : &tmV;
       uint32_t na = 0, n = 0;
       bool ok = true;
+      Source src{&B.queue};
+      Item it;
+      it.h = -1;
+      if (attn_plan::valid(p.plan)) it = describe<KEY, false>(p, int(blockIdx.x));
+      else if (blockIdx.x == 0) flag_error(p.flag, XT_DEVERR_PLAN);
 #pragma unroll 1
-      for (int r = 0; r * int(gridDim.x) < items && ok && !*abort_flag; ++r) {
-        const int i = snake(r);
-        if (i >= items) continue;
-        const BwdItem it = bwd_item<KEY>(p, i);
-        if (it.n == 0) continue;
-        if (!mbar_wait(smem_u32(a_empty), (na & 1) ^ 1, p.wait_ns)) { ok = false; break; }
-        mbar_expect_tx(smem_u32(a_full), 2 * C::QT);
-        Mma<HD>::load(sb + C::A, tmA1, smem_u32(a_full), KEY ? it.kh : it.h0, it.tile);
-        Mma<HD>::load(sb + C::A + C::QT, tmA2, smem_u32(a_full), KEY ? it.kh : it.h0, it.tile);
-        ++na;
-        int h = it.h0, t = it.rg.x;
-#pragma unroll 1
-        for (int j = 0; j < it.n; ++j, ++n) {
-          const uint32_t s = n % C::RING;
-          if (*abort_flag || !mbar_wait(smem_u32(&r_empty[s]), ((n / C::RING) & 1) ^ 1, p.wait_ns)) { ok = false; break; }
-          const uint32_t fb = smem_u32(&r_full[s]), dst = sb + C::R + s * 2 * C::QT;
-          mbar_expect_tx(fb, 2 * C::QT);
-          Mma<HD>::load(dst, tmR1, fb, KEY ? h : it.kh, t);
-          Mma<HD>::load(dst + C::QT, tmR2, fb, KEY ? h : it.kh, t);
-          if (++t == it.rg.y) { t = it.rg.x; ++h; }
+      for (;;) {
+        if (!src.publish(it, p.wait_ns)) { ok = false; break; }
+        if (it.h < 0) break;
+        const int tiles = it.r0.y - it.r0.x, kh = KEY ? it.h : it.h / p.group;
+        if (tiles > 0) {
+          if (!mbar_wait(smem_u32(&B.a_empty), (na & 1) ^ 1, p.wait_ns)) { ok = false; break; }
+          mbar_expect_tx(smem_u32(&B.a_full), 2 * C::QT);
+          Mma<HD>::load(sb + C::A, tmA1, smem_u32(&B.a_full), it.h, it.tile);
+          Mma<HD>::load(sb + C::A + C::QT, tmA2, smem_u32(&B.a_full), it.h, it.tile);
+          ++na;
         }
+#pragma unroll 1
+        for (int u = 0; u < it.b && ok; ++u)
+#pragma unroll 1
+          for (int t = it.r0.x; t < it.r0.y; ++t, ++n) {
+            const uint32_t s = n % RING;
+            if (*abort_flag || !mbar_wait(smem_u32(&B.r_empty[s]), ((n / RING) & 1) ^ 1, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = smem_u32(&B.r_full[s]), dst = sb + C::R + s * 2 * C::QT;
+            mbar_expect_tx(fb, 2 * C::QT + (KEY ? 1024 : 0));
+            Mma<HD>::load(dst, tmR1, fb, KEY ? it.a + u : kh, t);
+            Mma<HD>::load(dst + C::QT, tmR2, fb, KEY ? it.a + u : kh, t);
+            if constexpr (KEY) {
+              const int64_t at = int64_t(it.a + u) * Tp + int64_t(t) * BT;
+              copy_in(sb + C::VEC + s * 1024, p.nl + at, 512, fb);
+              copy_in(sb + C::VEC + s * 1024 + 512, p.nd + at, 512, fb);
+            }
+          }
+        if (!ok || *abort_flag) { ok = false; break; }
+        const int next = src.take();
+        if (next >= 0) it = describe<KEY, false>(p, next);
+        else it.h = -1;
       }
       if (!ok) give_up();
       bool drained = true;
-      if (na > 0) drained &= mbar_wait(smem_u32(a_full), (na - 1) & 1);
-      for (uint32_t m = 0; m < (n < uint32_t(C::RING) ? n : uint32_t(C::RING)); ++m) {
+      if (na > 0) drained &= mbar_wait(smem_u32(&B.a_full), (na - 1) & 1);
+      for (uint32_t m = 0; m < (n < RING ? n : RING); ++m) {
         const uint32_t g = n - 1 - m;
-        drained &= mbar_wait(smem_u32(&r_full[g % C::RING]), (g / C::RING) & 1);
+        drained &= mbar_wait(smem_u32(&B.r_full[g % RING]), (g / RING) & 1);
       }
       if (!drained) give_up();
-    } else if (warp == 1 && lane == 0) {
-      // -------------------------------------------------------------- MMA issuer
-      uint32_t na = 0, g = 0;
+    } else if (warp >= 1 && warp <= CH && lane == 0) {
+      // -------------------------------------------------------------- MMA issuer of chain warp − 1
+      const int c = warp - 1;
+      auto& b = B.ch[c];
+      uint32_t na = 0, g = 0;  // items with tiles, tiles
       bool ok = true;
       const uint32_t a1 = sb + C::A, a2 = a1 + C::QT;
-      auto slot = [&](uint32_t n) { return sb + C::R + (n % C::RING) * 2 * C::QT; };
+      const uint32_t tS = tbase + PW * c, tDP = tS + C::DP, acc1 = tbase + C::ACC1 + HD * c, acc2 = tbase + C::ACC2 + HD * c;
+      auto slot = [&](uint32_t n) { return sb + C::R + (n % RING) * 2 * C::QT + uint32_t(c) * (PW * 128); };
       auto issue_s = [&](uint32_t n) -> bool {
-        if (!mbar_wait_spin(smem_u32(&r_full[n % C::RING]), (n / C::RING) & 1, p.wait_ns)) return false;
+        if (!spin(smem_u32(&B.r_full[n % RING]), (n / RING) & 1, p.wait_ns)) return false;
         tc_fence_after();
-        Mma<HD>::nt(tbase + (n % C::NS) * 128, a1, slot(n));
-        tc_commit(smem_u32(&s_full[n % C::NS]));
+        Mma<HD>::template nt<BT / CH>(tS, a1, slot(n));
+        tc_commit(smem_u32(&b.s_full));
         return true;
       };
       auto issue_dp = [&](uint32_t n) {
-        Mma<HD>::nt(tbase + C::DP, a2, slot(n) + C::QT);
-        tc_commit(smem_u32(dp_full));
+        Mma<HD>::template nt<BT / CH>(tDP, a2, slot(n) + C::QT);
+        tc_commit(smem_u32(&b.dp_full));
       };
 #pragma unroll 1
-      for (int r = 0; r * int(gridDim.x) < items && ok && !*abort_flag; ++r) {
-        const int i = snake(r);
-        if (i >= items) continue;
-        const BwdItem it = bwd_item<KEY>(p, i);
-        if (it.n == 0) continue;
-        if (!mbar_wait_spin(smem_u32(a_full), na & 1, p.wait_ns)) { ok = false; break; }
+      for (uint32_t ni = 0; ok; ++ni) {
+        Item it;
+        if (*abort_flag || !next_item<false>(&B.queue, ni, it, p.wait_ns)) { ok = false; break; }
+        if (it.h < 0) break;
+        const int n = (it.r0.y - it.r0.x) * it.b;
+        if (n <= 0) continue;
+        if (!spin(smem_u32(&B.a_full), na & 1, p.wait_ns)) { ok = false; break; }
         ++na;
         tc_fence_after();
         if (!issue_s(g)) { ok = false; break; }
         issue_dp(g);
+        // the rows of both halves have read the last item's accumulators
+        if (!spin(smem_u32(&B.acc_free), na & 1, p.wait_ns)) { ok = false; break; }
 #pragma unroll 1
-        for (int j = 0; j < it.n; ++j, ++g) {
-          const bool next = j + 1 < it.n;
+        for (int j = 0; j < n; ++j, ++g) {
+          const bool next = j + 1 < n;
           if (*abort_flag) { ok = false; break; }
-          if (C::NS == 2 && next && !issue_s(g + 1)) { ok = false; break; }
-          if (KEY) {
-            if (!mbar_wait_spin(smem_u32(p_full), g & 1, p.wait_ns)) { ok = false; break; }
-            tc_fence_after();
-            Mma<HD>::tn(tbase + C::ACC2, tbase + (g % C::NS) * 128, 64, slot(g) + C::QT, j == 0);  // dV += Pᵀ dO
-          }
-          if (C::NS == 1 && next && !issue_s(g + 1)) { ok = false; break; }
-          if (!mbar_wait_spin(smem_u32(ds_full), g & 1, p.wait_ns)) { ok = false; break; }
+          // the next S follows as soon as P has been multiplied (it lies over S), or S been read
+          if (!spin(smem_u32(KEY ? &b.p_full : &b.s_free), g & 1, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
-          Mma<HD>::tn(tbase + C::ACC1, tbase + C::DP, 64, slot(g), j == 0);  // dK += dSᵀ Q, dQ += dS K
-          tc_commit(smem_u32(&r_empty[g % C::RING]));
+          if (KEY) Mma<HD>::template tn<BT / CH>(acc2, tS, PW, slot(g) + C::QT, j == 0);  // dV += Pᵀ dO
+          if (next && !issue_s(g + 1)) { ok = false; break; }
+          if (!spin(smem_u32(&b.ds_full), g & 1, p.wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          Mma<HD>::template tn<BT / CH>(acc1, tDP, PW, slot(g), j == 0);  // dK += dSᵀ Q, dQ += dS K
+          tc_commit(smem_u32(&B.r_empty[g % RING]));
           if (next) issue_dp(g + 1);
         }
         if (!ok) break;
-        tc_commit(smem_u32(acc_full));
-        tc_commit(smem_u32(a_empty));
+        tc_commit(smem_u32(&b.acc_full));
+        tc_commit(smem_u32(&B.a_empty));
       }
       if (!ok) give_up();
-      tc_commit(smem_u32(mma_done));
-      if (!mbar_wait(smem_u32(mma_done), 0)) give_up();
+      tc_commit(smem_u32(&b.mma_done));
+      if (!mbar_wait(smem_u32(&b.mma_done), 0)) give_up();
     }
   } else {
-    // ---------------------------------------------------------------- rows
     regs_inc<kBwdRegsRows>();
-    const int qw = warp & 3, half = (warp - 4) >> 2, col0 = 64 * half;
+    // ---------------------------------------------------------------- rows
+    const int qw = warp & 3, half = (warp - 4) >> 2, col0 = PW * half;
     const int rr = qw * 32 + lane;
     const uint32_t lane_off = uint32_t(qw * 32) << 16;
-    const uint32_t tDP = tbase + C::DP + lane_off + uint32_t(col0);
-    uint32_t g = 0, na = 0, nv = 0;
+    const uint32_t tS = tbase + lane_off + uint32_t(col0);
+    const uint32_t tDP = tS + C::DP;
+    auto& b = B.ch[CH == 2 ? half : 0];
+    const int64_t T = p.plan.T;
+    uint32_t g = 0, na = 0;
 #pragma unroll 1
-    for (int r = 0; r * int(gridDim.x) < items; ++r) {
-      const int i = snake(r);
-      if (i >= items) continue;
-      if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      const BwdItem it = bwd_item<KEY>(p, i);
-      const int row = it.tile * BT + rr;
-      const int64_t T = p.plan.T;
+    for (uint32_t ni = 0;; ++ni) {
+      bool ok = !__shfl_sync(0xffffffffu, *abort_flag, 0);
+      int h, tile, h0, heads, sp;
+      int4 rg;
+      {
+        Item it;
+        it.h = -1;
+        if (ok) ok = next_item<true>(&B.queue, ni, it, p.wait_ns);
+        h = it.h;
+        tile = it.tile;
+        h0 = it.a;
+        heads = it.b;
+        rg = it.r0;
+        sp = it.r1.x;
+      }
+      if (!ok) {
+        if (lane == 0) give_up();
+        break;
+      }
+      if (h < 0) break;
+      const int row = tile * BT + rr;
       const bool real = row < T;
       const int2 iv = __ldg((KEY ? p.plan.k_iv : p.plan.q_iv) + row);
-      float lse2 = INFINITY, Dr = 0.f;  // of the row (not KEY)
-      bool ok = true;
+      const int n = max(rg.y - rg.x, 0) * heads;
+      float nlse = -INFINITY, nD = 0.f;  // of the row (not KEY)
       if constexpr (!KEY) {
-        // D of the row: each half warp group adds its half of the columns, the halves meet in shared memory
-        float acc = 0.f;
         if (real && iv.y > iv.x) {
-          const int64_t c0 = int64_t(it.h0) * HD + half * (HD / 2);
-          const bf16* o = p.o + int64_t(row) * p.ldo + c0;
-          const bf16* ol = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + c0 : nullptr;
-          const bf16* go = p.d_o + int64_t(row) * p.lddo + c0;
-#pragma unroll
-          for (int c = 0; c < HD / 2; c += 8) {
+          const bf16* o = p.o + int64_t(row) * p.ldo + int64_t(h) * HD;
+          const bf16* ol = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + int64_t(h) * HD : nullptr;
+          const bf16* go = p.d_o + int64_t(row) * p.lddo + int64_t(h) * HD;
+          const float lse = p.lse[int64_t(h) * T + row];
+#pragma unroll 8
+          for (int c = 0; c < HD; c += 8) {
             float x[8], y[8], z[8];
             Vec<bf16>::load(o + c, x);
             Vec<bf16>::load(go + c, y);
@@ -896,89 +1188,68 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
               for (int e = 0; e < 8; ++e) x[e] += z[e];
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc = fmaf(x[e], y[e], acc);
+            for (int e = 0; e < 8; ++e) nD = fmaf(-x[e], y[e], nD);
           }
-          lse2 = p.lse[int64_t(it.h0) * T + row] * kLog2e;
-          if (lse2 == -INFINITY) lse2 = INFINITY;
+          if (lse != -INFINITY) nlse = lse * -kLog2e;
         }
-        float* dv = vec + (nv & 1) * 256;
-        dv[half * 128 + rr] = acc;
-        mbar_arrive(smem_u32(&vec_full[nv & 1]));
-        if (!warp_wait(smem_u32(&vec_full[nv & 1]), (nv >> 1) & 1, p.wait_ns)) {
-          if (lane == 0) give_up();
-          break;
-        }
-        ++nv;
-        Dr = dv[rr] + dv[128 + rr];
-        if (half == 0 && real) p.D[int64_t(it.h0) * T + row] = Dr;
-      }
-      int h = it.h0, t = it.rg.x;
-      // KEY: this thread's entry of a column tile's −lse·log₂e (half 0) or −D (half 1), read one tile ahead
-      auto vec_entry = [&](int hh, int tt) -> float {
-        const int q = tt * BT + rr;
         if (half == 0) {
-          const float x = q < T ? p.lse[int64_t(hh) * T + q] * -kLog2e : -INFINITY;
-          return x == INFINITY ? -INFINITY : x;
+          p.nl[int64_t(h) * Tp + row] = nlse;
+          p.nd[int64_t(h) * Tp + row] = nD;
         }
-        return q < T ? -p.D[int64_t(hh) * T + q] : 0.f;
-      };
-      float vnext = 0.f;
-      if (KEY && it.n > 0) vnext = vec_entry(h, t);
+      }
+      int hq = KEY ? h0 : h, t = rg.x;
 #pragma unroll 1
-      for (int j = 0; j < it.n; ++j, ++g) {
-        int h2 = h, t2 = t + 1;
-        if (t2 == it.rg.y) { t2 = it.rg.x; ++h2; }
-        const float* lv = vec + (g & 1) * 256;
-        if constexpr (KEY) {
-          // a thread refills a slot only after all have arrived for the tile in between, having read it
-          vec[(g & 1) * 256 + half * 128 + rr] = vnext;
-          if (j + 1 < it.n) vnext = vec_entry(h2, t2);
-          mbar_arrive(smem_u32(&vec_full[g & 1]));
-          if (!warp_wait(smem_u32(&vec_full[g & 1]), (g >> 1) & 1, p.wait_ns)) { ok = false; break; }
-        }
-        const float slope2 = BIAS ? __ldg(p.slopes + h) * kLog2e : 0.f;
-        const uint32_t tS = tbase + (g % C::NS) * 128 + lane_off + uint32_t(col0);
-        if (!warp_wait(smem_u32(&s_full[g % C::NS]), (g / C::NS) & 1, p.wait_ns)) { ok = false; break; }
+      for (int j = 0; j < n; ++j, ++g) {
+        const float* lv = reinterpret_cast<const float*>(smem + C::VEC + (g % RING) * 1024) + col0;
+        const float slope2 = BIAS ? __ldg(p.slopes + hq) * kLog2e : 0.f;
+        if (!warp_wait(smem_u32(&b.s_full), g & 1, p.wait_ns)) { ok = false; break; }
+        // (complete: S was computed from the same arrival; the wait makes the copied vectors visible here)
+        if (KEY && !warp_wait(smem_u32(&B.r_full[g % RING]), (g / RING) & 1, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
-        uint32_t s[64];
+        uint32_t s[PW];
         tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
+        if constexpr (!KEY) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&b.s_free));
+        }
         const float unit = (CAP || BIAS) ? 1.f : p.sc;
-        const int side = t < it.tile ? 1 : t > it.tile ? -1 : 0;
-        float slack[CAP ? 64 : 1];  // 1 − tanh²
+        const int side = t < tile ? 1 : t > tile ? -1 : 0;
+        float slack[CAP ? PW : 1];  // 1 − tanh²
         if constexpr (CAP) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {  // as to_log2, keeping u = 1/(1 + e^{2a/cap}): 1 − tanh² = 4u(1 − u)
+          for (int c = 0; c < PW; ++c) {  // as to_log2, keeping u = 1/(1 + e^{2a/cap}): 1 − tanh² = 4u(1 − u)
             const float u = rcp(1.f + ex2(__uint_as_float(s[c]) * p.capk));
             s[c] = __float_as_uint(fmaf(-2.f * p.cap2, u, p.cap2));
             slack[c] = 4.f * u * (1.f - u);
           }
           if constexpr (BIAS) add_bias(s, slope2, t * BT + col0 - row, side);
         } else if constexpr (BIAS) {
-          to_log2<64, CAP, BIAS>(s, p, slope2, t * BT + col0 - row, side);
+          to_log2<PW, CAP, BIAS>(s, p, slope2, t * BT + col0 - row, side);
         }
-        const bool edge = t < it.rg.z || t >= it.rg.w;
+        const bool edge = t < rg.z || t >= rg.w;
         const int lo = iv.x - t * BT - col0, hi = iv.y - t * BT - col0;
         if (edge) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < PW; ++c)
             if (c < lo || c >= hi) {
               s[c] = __float_as_uint(-INFINITY);
               if constexpr (CAP) slack[c] = 0.f;
             }
         }
-        const uint64_t unit2 = f32x2_pack(unit, unit), nl2 = f32x2_pack(-lse2, -lse2);
+        const uint64_t unit2 = f32x2_pack(unit, unit);
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
+        for (int c = 0; c < PW; c += 32) {  // 32 columns at a time: 16 registers of P
           uint32_t pk[16];
 #pragma unroll
           for (int e = c; e < c + 32; e += 4) {
-            float4 nl;
-            if constexpr (KEY) nl = *reinterpret_cast<const float4*>(lv + col0 + e);
+            float4 nl = make_float4(nlse, nlse, nlse, nlse);
+            if constexpr (KEY) nl = *reinterpret_cast<const float4*>(lv + e);
             float x[4];
-            f32x2_unpack(f32x2_fma(pair(s[e], s[e + 1]), unit2, KEY ? f32x2_pack(nl.x, nl.y) : nl2), x[0], x[1]);
-            f32x2_unpack(f32x2_fma(pair(s[e + 2], s[e + 3]), unit2, KEY ? f32x2_pack(nl.z, nl.w) : nl2), x[2], x[3]);
+            f32x2_unpack(f32x2_fma(pair(s[e], s[e + 1]), unit2, f32x2_pack(nl.x, nl.y)), x[0], x[1]);
+            f32x2_unpack(f32x2_fma(pair(s[e + 2], s[e + 3]), unit2, f32x2_pack(nl.z, nl.w)), x[2], x[3]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
             if constexpr (KEY) {
@@ -997,27 +1268,26 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(p_full));
+          if (lane == 0) mbar_arrive(smem_u32(&b.p_full));
         }
-        if (!warp_wait(smem_u32(dp_full), g & 1, p.wait_ns)) { ok = false; break; }
+        if (!warp_wait(smem_u32(&b.dp_full), g & 1, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
-        uint32_t d[64];
+        uint32_t d[PW];
         tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(d));
         tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
         tmem_ld_wait();
-        const uint64_t nd2 = f32x2_pack(-Dr, -Dr);
         auto form_ds = [&](auto masked) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
+          for (int c = 0; c < PW; c += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = c; e < c + 32; e += 4) {
-              float4 nd;
-              if constexpr (KEY) nd = *reinterpret_cast<const float4*>(lv + 128 + col0 + e);
+              float4 nd = make_float4(nD, nD, nD, nD);
+              if constexpr (KEY) nd = *reinterpret_cast<const float4*>(lv + 128 + e);
               float x[4];
-              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e], d[e + 1]), KEY ? f32x2_pack(nd.x, nd.y) : nd2),
-                                     pair(s[e], s[e + 1])), x[0], x[1]);
-              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e + 2], d[e + 3]), KEY ? f32x2_pack(nd.z, nd.w) : nd2),
+              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e], d[e + 1]), f32x2_pack(nd.x, nd.y)), pair(s[e], s[e + 1])),
+                           x[0], x[1]);
+              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e + 2], d[e + 3]), f32x2_pack(nd.z, nd.w)),
                                      pair(s[e + 2], s[e + 3])), x[2], x[3]);
               if constexpr (decltype(masked)::value) {  // a masked column's dP or D may be NaN
 #pragma unroll
@@ -1035,12 +1305,14 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(ds_full));
-        h = h2;
-        t = t2;
+        if (lane == 0) mbar_arrive(smem_u32(&b.ds_full));
+        if (++t == rg.y) {
+          t = rg.x;
+          ++hq;
+        }
       }
-      if (ok && it.n > 0) {
-        if (!warp_wait(smem_u32(acc_full), na & 1, p.wait_ns)) ok = false;
+      if (ok && n > 0) {
+        for (int c = 0; c < CH; ++c) ok = ok && warp_wait(smem_u32(&B.ch[c].acc_full), na & 1, p.wait_ns);
         ++na;
       }
       if (!ok) {
@@ -1052,27 +1324,44 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       float bad = 0.f;
 #pragma unroll
       for (int w = 0; w < (KEY ? 2 : 1); ++w) {
-        bf16* out = w ? p.dv + int64_t(row) * p.lddv : KEY ? p.dk + int64_t(row) * p.lddk : p.dq + int64_t(row) * p.lddq;
-        out += int64_t(KEY ? it.kh : it.h0) * HD + half * (HD / 2);
-        const float mul = w ? 1.f : p.scale;
+        const int64_t col = int64_t(h) * HD + half * (HD / 2);
+        bf16* out =
+            (w ? p.dv + int64_t(row) * p.lddv : KEY ? p.dk + int64_t(row) * p.lddk : p.dq + int64_t(row) * p.lddq) + col;
+        float* raw = KEY && p.split > 1
+                         ? (w ? p.part_v : p.part_k) + (int64_t(sp) * T + row) * (int64_t(p.Hkv) * HD) + col
+                         : nullptr;
+        const float mul = w || raw ? 1.f : p.scale;
         const uint32_t acc = tbase + (w ? C::ACC2 : C::ACC1) + lane_off + uint32_t(half * (HD / 2));
 #pragma unroll
-        for (int c = 0; c < HD / 64; ++c) {
+        for (int c = 0; c < HD / 2; c += 32) {
           uint32_t o[32];
-          if (it.n > 0) {
-            tmem_ld32(acc + uint32_t(c * 32), o);
-            tmem_ld_wait();
+          if (n > 0) {
+            tmem_ld32(acc + uint32_t(c), o);
+            if constexpr (CH == 2) {
+              uint32_t o1[32];
+              tmem_ld32(acc + uint32_t(HD + c), o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]));
+            } else {
+              tmem_ld_wait();
+            }
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float x = it.n > 0 ? __uint_as_float(o[e]) * mul : 0.f;
+            const float x = n > 0 ? __uint_as_float(o[e]) * mul : 0.f;
             bad = fmaf(x, 0.f, bad);
             o[e] = __float_as_uint(x);
           }
-          if (real) {
+          if (!real) continue;
+          if (raw) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(raw + c + u * 4) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              *reinterpret_cast<uint4*>(out + c * 32 + u * 8) =
+              *reinterpret_cast<uint4*>(out + c + u * 8) =
                   make_uint4(pack_bf16(__uint_as_float(o[8 * u]), __uint_as_float(o[8 * u + 1])),
                              pack_bf16(__uint_as_float(o[8 * u + 2]), __uint_as_float(o[8 * u + 3])),
                              pack_bf16(__uint_as_float(o[8 * u + 4]), __uint_as_float(o[8 * u + 5])),
@@ -1081,26 +1370,12 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         }
       }
       tc_fence_before();
-      // rows that a masked NaN or infinity reached through the products: this half's columns once more
-      uint32_t redo = __ballot_sync(0xffffffffu, bad != 0.f && real);
-      while (redo) {
-        const int src = __ffs(redo) - 1;
-        redo &= redo - 1;
-        const int rw = __shfl_sync(0xffffffffu, row, src), lo = __shfl_sync(0xffffffffu, iv.x, src),
-                  hi = __shfl_sync(0xffffffffu, iv.y, src);
-        const float m2 = __shfl_sync(0xffffffffu, lse2, src), dr = __shfl_sync(0xffffffffu, Dr, src);
-        float a1[HD / 32] = {}, a2[HD / 32] = {};
-        for (int hh = it.h0; hh < it.h0 + it.heads; ++hh)
-          redo_row<HD, KEY, false, CAP, BIAS>(p, hh, it.kh, rw, lo, hi, m2, dr, a1, a2);
-        __syncwarp();
-        if ((lane >> 4) != half) continue;
-#pragma unroll
-        for (int e = 0; e < HD / 32; ++e) {
-          const int64_t c = int64_t(KEY ? it.kh : it.h0) * HD + lane * (HD / 32) + e;
-          (KEY ? p.dk + int64_t(rw) * p.lddk : p.dq + int64_t(rw) * p.lddq)[c] = __float2bfloat16_rn(a1[e] * p.scale);
-          if constexpr (KEY) p.dv[int64_t(rw) * p.lddv + c] = __float2bfloat16_rn(a2[e]);
-        }
-      }
+      __syncwarp();
+      if (n > 0 && lane == 0) mbar_arrive(smem_u32(&B.acc_free));
+      const uint32_t rows = __ballot_sync(0xffffffffu, bad != 0.f && real);
+      if (rows)
+        repair<HD, KEY, false, CAP, BIAS>(p, KEY ? h0 : h, heads, KEY ? h : h / p.group, row, iv, rows, rg.x * BT,
+                                          rg.y * BT, -nlse, -nD, 0.f, half, 2, sp);
     }
   }
   __syncthreads();
@@ -1130,7 +1405,7 @@ int launch_bwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk
     auto k = attnm_fwd_kernel<HD, CAP, BIAS>;                                                                    \
     XT_TRY(prepare_kernel(reinterpret_cast<const void*>(k), FwdCfg<HD>::BYTES, 168));                            \
     const int64_t items = int64_t((p.plan.tiles + 1) / 2) * p.H;                                                 \
-    launch(k, unsigned(items < num_sms() ? items : num_sms()), kThreadsFwd, FwdCfg<HD>::BYTES, s, tq, tk, tv, p); \
+    launch(k, unsigned(items), kThreadsFwd, FwdCfg<HD>::BYTES, s, tq, tk, tv, p);                                \
     return check_launch("xt_attention_masked_fwd");                                                              \
   }                                                                                                              \
   template <>                                                                                                    \
@@ -1146,9 +1421,8 @@ int launch_bwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk
                      const Params& p, cudaStream_t s) {                                                          \
     auto k = attnm_bwd_kernel<HD, KEY, CAP, BIAS>;                                                               \
     XT_TRY(prepare_kernel(reinterpret_cast<const void*>(k), BwdCfg<HD, KEY>::BYTES, 168));                         \
-    const int64_t items = int64_t(p.plan.tiles) * (KEY ? p.Hkv : p.H);                                           \
-    launch(k, unsigned(items < num_sms() ? items : num_sms()), kThreadsBwd, BwdCfg<HD, KEY>::BYTES, s, tq, tk,   \
-           tv, tdo, p);                                                                                          \
+    const int64_t items = int64_t(p.plan.tiles) * (KEY ? p.Hkv * p.split : p.H);                                 \
+    launch(k, unsigned(items), kThreadsBwd, BwdCfg<HD, KEY>::BYTES, s, tq, tk, tv, tdo, p);                      \
     return check_launch("xt_attention_masked_bwd");                                                              \
   }                                                                                                              \
   template <>                                                                                                    \

@@ -1,10 +1,11 @@
 // Builds the plan of masked attention (attention_plan.cuh) from the documents of a batch.
 //
 // Two launches, one where eight tiles or fewer make up the batch (1024 tokens: the launch is most
-// of its time).  The first gives each token a thread: a binary search finds its document, warps and
-// shared memory reduce the intervals of a 128-token tile to the tile's ranges.  The second orders
-// the tiles by their work: a tile's place is the number of tiles with more work than it (or as much
-// and a lower number), counted by one thread per tile, so the order never depends on timing.
+// of its time).  The first gives each token a thread: a binary search (in shared memory, which holds
+// the offsets of up to kOffsets documents) finds its document, warps and shared memory reduce the
+// intervals of a 128-token tile to the tile's ranges.  The second writes the tiles' records in the
+// order of their work: a tile's place is the number of tiles with more work than it (or as much and a
+// lower number), counted by one warp per tile, so the order never depends on timing.
 #include "attention_plan.cuh"
 #include "internal.cuh"
 
@@ -14,6 +15,7 @@ namespace {
 
 constexpr int kTilesPerCta = 8;
 constexpr int kThreads = BT * kTilesPerCta;
+constexpr int kOffsets = 2048;  // document offsets searched in shared memory
 
 struct Docs {
   const int32_t *off, *len, *prefix;
@@ -27,18 +29,19 @@ struct Doc {
   int a, end, pe;  // first token, end of the valid part, end of the prefix
 };
 
-__device__ __forceinline__ Doc doc_of(const Docs& p, int t) {
+// `off`: p.off or its copy in shared memory.
+__device__ __forceinline__ Doc doc_of(const Docs& p, const int32_t* off, int t) {
   int d, a, e;
-  if (p.off) {
+  if (off) {
     int lo = 0, hi = p.n - 1;  // the last document that starts at or before t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.off[mid] <= t) lo = mid;
+      if (off[mid] <= t) lo = mid;
       else hi = mid - 1;
     }
     d = lo;
-    a = p.n ? p.off[d] : 0;
-    e = p.n ? p.off[d + 1] : 0;
+    a = p.n ? off[d] : 0;
+    e = p.n ? off[d + 1] : 0;
   } else {
     const int span = p.n ? int(p.T / p.n) : 1;
     d = t / span;
@@ -62,29 +65,44 @@ __device__ __forceinline__ int pair_cost(int4 a, int4 b) {
   return max(a.y, b.y) - min(a.x, b.x);
 }
 
-__device__ void order_tiles(const Docs& p, int i) {
+// One warp: the records of tile i and, for an even share of them, of pair i.
+__device__ void order_tile(const Docs& p, int i) {
   const Layout l(p.T);
-  const int nt = int(l.tiles), np = (nt + 1) / 2;
+  const int nt = int(l.tiles), np = (nt + 1) / 2, lane = threadIdx.x & 31;
   if (i >= nt) return;
   const int4* q = reinterpret_cast<const int4*>(p.plan + l.qrange);
   const int4* k = reinterpret_cast<const int4*>(p.plan + l.krange);
   const int4 none = make_int4(0, 0, 0, 0);
-  const int cq = cost(q[i]), ck = cost(k[i]);
-  const int cp = i < np ? pair_cost(q[2 * i], 2 * i + 1 < nt ? q[2 * i + 1] : none) : 0;
+  const bool has_pair = i < np;
+  const int4 q0 = has_pair ? q[2 * i] : none, q1 = has_pair && 2 * i + 1 < nt ? q[2 * i + 1] : none;
+  const int4 qi = q[i], ki = k[i];
+  const int cq = cost(qi), ck = cost(ki), cp = pair_cost(q0, q1);
   int rq = 0, rk = 0, rp = 0;
-  for (int j = 0; j < nt; ++j) {
+  for (int j = lane; j < nt; j += 32) {
     const int a = cost(q[j]), b = cost(k[j]);
     rq += a > cq || (a == cq && j < i);
     rk += b > ck || (b == ck && j < i);
+    if (has_pair && j < np) {
+      const int c = pair_cost(q[2 * j], 2 * j + 1 < nt ? q[2 * j + 1] : none);
+      rp += c > cp || (c == cp && j < i);
+    }
   }
-  p.plan[l.q_order + rq] = i;
-  p.plan[l.k_order + rk] = i;
-  if (i >= np) return;
-  for (int j = 0; j < np; ++j) {
-    const int a = pair_cost(q[2 * j], 2 * j + 1 < nt ? q[2 * j + 1] : none);
-    rp += a > cp || (a == cp && j < i);
-  }
-  p.plan[l.pair_order + rp] = i;
+  rq = __reduce_add_sync(0xffffffffu, rq);
+  rk = __reduce_add_sync(0xffffffffu, rk);
+  rp = __reduce_add_sync(0xffffffffu, rp);
+  if (lane != 0) return;
+  int4* out = reinterpret_cast<int4*>(p.plan + l.qs) + 2 * rq;
+  out[0] = make_int4(i, 0, 0, 0);
+  out[1] = qi;
+  out = reinterpret_cast<int4*>(p.plan + l.ks) + 2 * rk;
+  out[0] = make_int4(i, 0, 0, 0);
+  out[1] = ki;
+  if (!has_pair) return;
+  out = reinterpret_cast<int4*>(p.plan + l.pairs) + 3 * rp;
+  const int first = cost(q0) == 0 ? q1.x : cost(q1) == 0 ? q0.x : min(q0.x, q1.x);
+  out[0] = make_int4(2 * i, first, first + cp, 0);
+  out[1] = q0;
+  out[2] = q1;
 }
 
 __device__ __forceinline__ int4 tile_range(int lo_min, int hi_max, int lo_max, int hi_min) {
@@ -107,11 +125,18 @@ __global__ void __launch_bounds__(kThreads) plan_tiles_kernel(const Docs p) {
       if (p.prefix) bad |= p.prefix[d] < 0;
       if (bad) flag_error(p.flag, XT_DEVERR_INDEX);
     }
+  __shared__ int32_t offs[kOffsets];
+  const int32_t* off = p.off;
+  if (p.off && p.n < kOffsets) {
+    for (int d = threadIdx.x; d <= p.n; d += kThreads) offs[d] = p.off[d];
+    off = offs;
+    __syncthreads();
+  }
   const bool real = t < p.T;
   int2 q = make_int2(0, 0), k = make_int2(0, 0);
   if (real) {
     const int i = int(t);
-    const Doc d = doc_of(p, i);
+    const Doc d = doc_of(p, off, i);
     if (i >= d.a && i < d.end) {
       q = make_int2(d.a, p.causal ? max(i + 1, d.pe) : d.end);
       k = make_int2(p.causal && i >= d.pe ? i : d.a, d.end);
@@ -150,13 +175,13 @@ __global__ void __launch_bounds__(kThreads) plan_tiles_kernel(const Docs p) {
   }
   if (gridDim.x == 1) {
     __syncthreads();
-    order_tiles(p, int(threadIdx.x));
+    if (warp < kTilesPerCta) order_tile(p, warp);
   }
 }
 
 __global__ void __launch_bounds__(256) plan_order_kernel(const Docs p) {
   pdl_begin();
-  order_tiles(p, int(blockIdx.x) * 256 + int(threadIdx.x));
+  order_tile(p, int(blockIdx.x) * 8 + int(threadIdx.x >> 5));
 }
 
 }  // namespace
@@ -193,7 +218,7 @@ int xt_attention_plan(int64_t T, int n_docs, const int32_t* doc_off, const int32
   launch(plan_tiles_kernel, grid, kThreads, 0, s, p);
   XT_TRY(check_launch("xt_attention_plan (tiles)"));
   if (grid > 1) {
-    launch(plan_order_kernel, unsigned(ceil_div(l.tiles, 256)), 256, 0, s, p);
+    launch(plan_order_kernel, unsigned(ceil_div(l.tiles, 8)), 256, 0, s, p);
     XT_TRY(check_launch("xt_attention_plan (order)"));
   }
   return XT_OK;

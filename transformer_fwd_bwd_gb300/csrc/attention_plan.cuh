@@ -21,29 +21,28 @@ constexpr int kHeader = 16;           // ints
 
 // First element of each part, in ints from the plan's start (every part 16-byte aligned).
 struct Layout {
-  int64_t tiles, qrange, krange, pair_order, q_order, k_order, q_iv, k_iv, total;
+  int64_t tiles, qrange, krange, pairs, qs, ks, q_iv, k_iv, total;
   __host__ __device__ explicit Layout(int64_t T) {
     tiles = (T + BT - 1) / BT;
-    const int64_t t4 = (tiles + 3) & ~int64_t(3);
     qrange = kHeader;
     krange = qrange + 4 * tiles;
-    pair_order = krange + 4 * tiles;
-    q_order = pair_order + t4;
-    k_order = q_order + t4;
-    q_iv = k_order + t4;
+    pairs = krange + 4 * tiles;
+    qs = pairs + 12 * ((tiles + 1) / 2);
+    ks = qs + 8 * tiles;
+    q_iv = ks + 8 * tiles;
     k_iv = q_iv + 2 * BT * tiles;
     total = k_iv + 2 * BT * tiles;
   }
 };
 
-// A plan as a kernel reads it.
+// A plan as a kernel reads it.  Ranges are (first, end, full first, full end) of opposite tiles.
 struct View {
   const int32_t* base;
   int64_t T;
   int tiles;
-  const int4 *qrange, *krange;                    // first, end, full first, full end (opposite tiles)
-  const int32_t *pair_order, *q_order, *k_order;  // tile pairs / query tiles / key tiles, most work first
-  const int2 *q_iv, *k_iv;                        // per token [first, end)
+  const int4* pairs;         // pairs of query tiles, most work first: (first tile, first key tile, end, 0), two ranges
+  const int4 *qs, *ks;       // query tiles and key tiles, most work first: (tile, 0, 0, 0), range
+  const int2 *q_iv, *k_iv;   // per token [first, end)
 };
 
 inline View view(const void* plan, int64_t T) {
@@ -53,11 +52,9 @@ inline View view(const void* plan, int64_t T) {
   v.base = b;
   v.T = T;
   v.tiles = int(l.tiles);
-  v.qrange = reinterpret_cast<const int4*>(b + l.qrange);
-  v.krange = reinterpret_cast<const int4*>(b + l.krange);
-  v.pair_order = b + l.pair_order;
-  v.q_order = b + l.q_order;
-  v.k_order = b + l.k_order;
+  v.pairs = reinterpret_cast<const int4*>(b + l.pairs);
+  v.qs = reinterpret_cast<const int4*>(b + l.qs);
+  v.ks = reinterpret_cast<const int4*>(b + l.ks);
   v.q_iv = reinterpret_cast<const int2*>(b + l.q_iv);
   v.k_iv = reinterpret_cast<const int2*>(b + l.k_iv);
   return v;
