@@ -173,6 +173,13 @@ struct Mma {
   }
 };
 
+// Bits of the columns base .. base + 31 that lie in [lo, hi).
+__device__ __forceinline__ uint32_t visible_bits(int lo, int hi, int base) {
+  const uint32_t below_hi = uint32_t(~(~0ull << min(max(hi - base, 0), 32)));
+  const uint32_t below_lo = uint32_t(~(~0ull << min(max(lo - base, 0), 32)));
+  return below_hi & ~below_lo;
+}
+
 // r[c] −= slope₂·|d0 + c|.
 template <int N>
 __device__ __forceinline__ void add_bias(uint32_t (&r)[N], float slope2, int d0, int side) {
@@ -801,10 +808,13 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         if constexpr (CAP || BIAS)
           to_log2<128, CAP, BIAS>(s, p, slope2, j * BT - row, j < tile ? 1 : j > tile ? -1 : 0);
         if (j < rg.z || j >= rg.w) {
-          const int lo = iv.x - j * BT, hi = iv.y - j * BT;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < lo || c >= hi) s[c] = __float_as_uint(-INFINITY);
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t seen = visible_bits(iv.x - j * BT, iv.y - j * BT, 32 * w);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(seen & (1u << c))) s[32 * w + c] = __float_as_uint(-INFINITY);
+          }
         }
         float mx[4];
 #pragma unroll
@@ -946,7 +956,7 @@ struct BwdCfg {
   static constexpr uint32_t DP = 128, ACC1 = 256, ACC2 = ACC1 + CH * HD;
   static constexpr int A = 0;                            // the row tiles: K, V or Q, dO
   static constexpr int R = A + 2 * QT;                   // ring of column tile pairs: Q, dO or K, V
-  static constexpr int VEC = R + RING * 2 * QT;          // (KEY) ring of −lse·log₂e and −D, 128 floats each
+  static constexpr int VEC = R + RING * 2 * QT;          // (KEY) ring of −lse·log₂e and −D, 128 floats each; or D
   static constexpr int BARS = VEC + RING * 1024;
   static constexpr int BYTES = 1024 + BARS + 512;
   static_assert(ACC2 + (KEY ? CH * HD : 0) <= 512, "TMEM columns");
@@ -959,7 +969,7 @@ struct BwdBars {
   struct Chain {
     uint64_t s_full, s_free, dp_full, p_full, ds_full, acc_full, mma_done;
   } ch[2];
-  uint64_t acc_free;
+  uint64_t acc_free, d_full[4];
   uint32_t tmem, abort;
 };
 
@@ -996,6 +1006,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       mbar_init(smem_u32(&B.ch[c].mma_done), 1);
     }
     mbar_init(smem_u32(&B.acc_free), 8);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&B.d_full[i]), 2);
     B.abort = 0;
     fence_barrier_init();
   }
@@ -1109,6 +1120,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tc_fence_after();
         if (!issue_s(g)) { ok = false; break; }
         issue_dp(g);
+        if (n == 1) tc_commit(smem_u32(&B.a_empty));
         // the rows of both halves have read the last item's accumulators
         if (!spin(smem_u32(&B.acc_free), na & 1, p.wait_ns)) { ok = false; break; }
 #pragma unroll 1
@@ -1124,11 +1136,13 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
           tc_fence_after();
           Mma<HD>::template tn<BT / CH>(acc1, tDP, PW, slot(g), j == 0);  // dK += dSᵀ Q, dQ += dS K
           tc_commit(smem_u32(&B.r_empty[g % RING]));
-          if (next) issue_dp(g + 1);
+          if (next) {
+            issue_dp(g + 1);
+            if (j + 2 == n) tc_commit(smem_u32(&B.a_empty));  // the last tile's S and dP: the row tiles are free
+          }
         }
         if (!ok) break;
         tc_commit(smem_u32(&b.acc_full));
-        tc_commit(smem_u32(&B.a_empty));
       }
       if (!ok) give_up();
       tc_commit(smem_u32(&b.mma_done));
@@ -1172,13 +1186,16 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       const int n = max(rg.y - rg.x, 0) * heads;
       float nlse = -INFINITY, nD = 0.f;  // of the row (not KEY)
       if constexpr (!KEY) {
+        // each half adds its half of the head's columns, the halves of a row meet in shared memory
+        float acc = 0.f;
         if (real && iv.y > iv.x) {
-          const bf16* o = p.o + int64_t(row) * p.ldo + int64_t(h) * HD;
-          const bf16* ol = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + int64_t(h) * HD : nullptr;
-          const bf16* go = p.d_o + int64_t(row) * p.lddo + int64_t(h) * HD;
+          const int64_t c0 = int64_t(h) * HD + half * (HD / 2);
+          const bf16* o = p.o + int64_t(row) * p.ldo + c0;
+          const bf16* ol = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + c0 : nullptr;
+          const bf16* go = p.d_o + int64_t(row) * p.lddo + c0;
           const float lse = p.lse[int64_t(h) * T + row];
-#pragma unroll 8
-          for (int c = 0; c < HD; c += 8) {
+#pragma unroll
+          for (int c = 0; c < HD / 2; c += 8) {
             float x[8], y[8], z[8];
             Vec<bf16>::load(o + c, x);
             Vec<bf16>::load(go + c, y);
@@ -1188,10 +1205,19 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
               for (int e = 0; e < 8; ++e) x[e] += z[e];
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) nD = fmaf(-x[e], y[e], nD);
+            for (int e = 0; e < 8; ++e) acc = fmaf(-x[e], y[e], acc);
           }
           if (lse != -INFINITY) nlse = lse * -kLog2e;
         }
+        float* meet = reinterpret_cast<float*>(smem + C::VEC) + (ni & 1) * 256;
+        meet[half * 128 + rr] = acc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B.d_full[qw]));
+        if (!warp_wait(smem_u32(&B.d_full[qw]), ni & 1, p.wait_ns)) {
+          if (lane == 0) give_up();
+          break;
+        }
+        nD = meet[rr] + meet[128 + rr];
         if (half == 0) {
           p.nl[int64_t(h) * Tp + row] = nlse;
           p.nd[int64_t(h) * Tp + row] = nD;
@@ -1230,14 +1256,18 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
           to_log2<PW, CAP, BIAS>(s, p, slope2, t * BT + col0 - row, side);
         }
         const bool edge = t < rg.z || t >= rg.w;
-        const int lo = iv.x - t * BT - col0, hi = iv.y - t * BT - col0;
+        uint32_t seen[2] = {~0u, ~0u};
         if (edge) {
 #pragma unroll
-          for (int c = 0; c < PW; ++c)
-            if (c < lo || c >= hi) {
-              s[c] = __float_as_uint(-INFINITY);
-              if constexpr (CAP) slack[c] = 0.f;
-            }
+          for (int w = 0; w < 2; ++w) {
+            seen[w] = visible_bits(iv.x - t * BT, iv.y - t * BT, col0 + 32 * w);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(seen[w] & (1u << c))) {
+                s[32 * w + c] = __float_as_uint(-INFINITY);
+                if constexpr (CAP) slack[32 * w + c] = 0.f;
+              }
+          }
         }
         const uint64_t unit2 = f32x2_pack(unit, unit);
 #pragma unroll
@@ -1292,7 +1322,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
               if constexpr (decltype(masked)::value) {  // a masked column's dP or D may be NaN
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  if (e + k < lo || e + k >= hi) x[k] = 0.f;
+                  if (!(seen[c / 32] & (1u << (e - c + k)))) x[k] = 0.f;
               }
               pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
               pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
