@@ -8,10 +8,12 @@
 // Angles.  An angle matters modulo a turn only, and pos is an integer, so f_i/2π is held as a
 // 64-bit fraction of a turn and pos·(f_i/2π) mod 1 is one 64-bit integer product, whose wrap-around
 // is the reduction: no position is too far (a float32 product is off by 0.06 rad at position 10⁶).
-// The fraction's top 24 bits give cos and sin (error ≤ 2π·2⁻²⁵ in the angle).
+// The nearest quarter turn comes off in integers too, and what is left, at most an eighth of a turn,
+// goes through the Taylor series of sin and cos (next terms below 2⁻²⁵), some twenty instructions for
+// the pair of them.
 //
 // Memory-bound: x is read once and y written once.  A thread keeps one token's VW pairs: it forms
-// their cos and sin once and applies them to several heads, kInFlight heads' loads in flight.
+// their cos and sin once and applies them to several heads, the loads of some heads in flight.
 #include <cmath>
 
 #include "internal.cuh"
@@ -22,7 +24,18 @@ namespace {
 constexpr int kMaxPairs = 128;  // hd ≤ 256
 constexpr int kMaxAxes = 4;
 constexpr int kThreads = 256;
-constexpr int kInFlight = 4;
+
+// sin and cos of a turn's fraction u·2⁻³².
+__device__ __forceinline__ void sincos_turn(uint32_t u, float& sn, float& cs) {
+  const uint32_t q = (u + 0x20000000u) >> 30;                            // nearest quarter turn
+  const float y = float(int32_t(u - (q << 30))) * 1.46291807926716e-9f;  // 2π·2⁻³²; |y| ≤ π/4
+  const float z = y * y;
+  const float s = fmaf(y * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), y);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float a = (q & 1) ? c : s, b = (q & 1) ? s : c;
+  sn = __uint_as_float(__float_as_uint(a) ^ ((q & 2) << 30));
+  cs = __uint_as_float(__float_as_uint(b) ^ (((q + 1) & 2) << 30));
+}
 
 struct RopeAxes {
   uint64_t turn[kMaxPairs];  // f_i / 2π mod 1, in units of 2⁻⁶⁴
@@ -35,7 +48,7 @@ struct RopeAxes {
 };
 
 template <typename T, bool BWD, int VW>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const T* x, T* y, const __grid_constant__ RopeAxes a) {
+__global__ void __launch_bounds__(kThreads, VW == 8 ? 6 : 3) rope_axes_kernel(const T* x, T* y, const __grid_constant__ RopeAxes a) {
   __shared__ uint64_t turn[kMaxPairs];
   __shared__ uint8_t axis[kMaxPairs];
   for (int i = threadIdx.x; i < a.half; i += kThreads) {
@@ -44,6 +57,11 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const T* x, T* y, c
   }
   __syncthreads();
   pdl_begin();
+  // Heads whose loads are in flight, and blocks per SM: eight bf16 pairs fill a thread, so one head at a time and
+  // many threads (50001 tokens x 40 heads of 128, forward and backward: 338 us, 6.06 TB/s; two heads and four blocks
+  // 378, four heads at 112 registers 510); four float32 pairs leave room for four heads (8192 x 24 x 64: 37.6 us
+  // against 39.2 with one).
+  constexpr int kInFlight = VW == 8 ? 1 : 4;
   const int chunks = a.half / VW;
   const int64_t total = a.T * a.groups * chunks;
   for (int64_t v = int64_t(blockIdx.x) * kThreads + threadIdx.x; v < total; v += int64_t(gridDim.x) * kThreads) {
@@ -59,10 +77,7 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const T* x, T* y, c
     for (int e = 0; e < VW; ++e) {
       const int ax = axis[i0 + e];
       const uint32_t p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
-      // signed fraction of a turn in [−½, ½), then cos and sin of π·(2·fraction)
-      const uint64_t f = uint64_t(int64_t(int32_t(p))) * turn[i0 + e];
-      const float r = float(int32_t(f >> 32)) * 0x1.0p-31f;
-      sincospif(r, &s[e], &c[e]);
+      sincos_turn(uint32_t((uint64_t(int64_t(int32_t(p))) * turn[i0 + e]) >> 32), s[e], c[e]);
       if (BWD) s[e] = -s[e];
     }
     const T* xr = x + t * a.ld_x + i0;

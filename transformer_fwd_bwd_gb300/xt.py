@@ -273,8 +273,8 @@ def ptr(t, contiguous=True):
 
 
 def stream(s=None):
-    if s is None:
-        return torch.cuda.current_stream().cuda_stream
+    if s is None:  # torch.cuda.current_stream().cuda_stream without the Stream object (4 us less per call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return s.cuda_stream if hasattr(s, "cuda_stream") else s
 
 
@@ -490,17 +490,19 @@ def xt_rope_bwd(d, dx, table, B, S, H, hd, ld, acc=0, s=None):
 
 
 def _rope_axes(name, x, y, pos, sections, H, hd, base, per_axis, acc, s):
-    if x.dtype != y.dtype or x.dim() != 2 or y.shape[0] != x.shape[0]:
+    T, cols = x.shape
+    if x.dtype != y.dtype or y.dim() != 2 or y.shape[0] != T:
         raise ValueError("x and y are [T, >= H*hd] tensors of one dtype")
-    if x.shape[1] < H * hd or y.shape[1] < H * hd or (x.numel() and (x.stride(1) != 1 or y.stride(1) != 1)):
+    (ldx, cx), (ldy, cy) = x.stride(), y.stride()
+    if cols < H * hd or y.shape[1] < H * hd or (T and (cx != 1 or cy != 1)):
         raise ValueError("x and y need unit column stride and H*hd columns")
-    if pos.dtype != torch.int32 or tuple(pos.shape) != (len(sections), x.shape[0]):
+    n = len(sections)
+    if pos.dtype != torch.int32 or pos.shape != (n, T):
         raise ValueError("pos must be int32 [len(sections), T]")
-    T = x.shape[0]
-    sec = (C.c_int32 * max(1, len(sections)))(*sections)
-    ld = lambda t: t.stride(0) if T > 1 else max(t.stride(0), H * hd)  # noqa: E731
-    call(name, ptr(x, False), ld(x), ptr(y, False), ld(y), ptr(pos), len(sections), sec, int(per_axis), float(base), T,
-         H, hd, dt(x), *acc, stream(s))
+    if T == 1:  # a single row's stride says nothing
+        ldx, ldy = max(ldx, H * hd), max(ldy, H * hd)
+    call(name, ptr(x, False), ldx, ptr(y, False), ldy, ptr(pos), n, (C.c_int32 * max(1, n))(*sections), int(per_axis),
+         float(base), T, H, hd, dt(x), *acc, stream(s))
 
 
 def xt_rope_axes_fwd(x, y, pos, sections, H, hd, base=10000.0, per_axis=0, s=None):
@@ -780,12 +782,12 @@ def _ptrs(tensors):
 def _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale):
     if not (len(m_code) == len(r_code) == len(m_scale) == len(r_scale) == n):
         raise ValueError("the lists must have the same length")
-    for lst, dtype in ((m_code, torch.int8), (r_code, torch.uint8), (m_scale, torch.float32), (r_scale, torch.float32)):
-        scales = dtype == torch.float32
+    for lst, dtype, per in ((m_code, torch.int8, 1), (r_code, torch.uint8, 1), (m_scale, torch.float32, 256),
+                            (r_scale, torch.float32, 256)):
         for t, k in zip(lst, numel):
-            if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+            if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("codes are contiguous int8 (m) and uint8 (r), scales float32 CUDA tensors")
-            if t.numel() != (adamw8_scales(k) if scales else k):
+            if t.numel() != -(-k // per):
                 raise ValueError("code and scale sizes must match the tensors")
 
 
