@@ -170,21 +170,40 @@ class NativeBlock:
 
     # -------------------------------------------------------------------------- optimizer
 
-    def init_optimizer(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, max_grad_norm=1.0):
+    def init_optimizer(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, max_grad_norm=1.0, state_bits=32):
         """AdamW state ([BP] § Optimiser-tillståndet): float32 master weights (the parameters
         themselves when they are float32; for bf16 parameters a float32 copy, the bf16 tensors
-        then being the working copy every step rewrites), first and second moments at zero."""
+        then being the working copy every step rewrites), first and second moments at zero, in
+        float32 or (state_bits=8) as 8-bit codes with a scale per 256 elements (xt_adamw8_step)."""
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
         if self.gdt != torch.float32:
             raise ValueError("the optimizer reads float32 gradients (grad_dtype='f32')")
         self.hyper = dict(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
                           max_grad_norm=max_grad_norm)
         self._names = list(self.p)
         self.master = {k: (v if v.dtype == torch.float32 else v.float().contiguous()) for k, v in self.p.items()}
-        self.m = {k: torch.zeros(v.shape, dtype=torch.float32, device=self.device) for k, v in self.p.items()}
-        self.v = {k: torch.zeros(v.shape, dtype=torch.float32, device=self.device) for k, v in self.p.items()}
+        self.state_bits = state_bits
         self.opt_step = 0
         self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
-        self._opt_ws = xt.adamw_workspace([self.p[k].numel() for k in self._names], self.device)
+        numels = [self.p[k].numel() for k in self._names]
+        if state_bits == 8:
+            self.state8 = xt.adamw8_state([self.p[k] for k in self._names])
+            self._opt_ws = xt.adamw8_workspace(numels, self.device)
+            return
+        self.m = {k: torch.zeros(v.shape, dtype=torch.float32, device=self.device) for k, v in self.p.items()}
+        self.v = {k: torch.zeros(v.shape, dtype=torch.float32, device=self.device) for k, v in self.p.items()}
+        self._opt_ws = xt.adamw_workspace(numels, self.device)
+
+    def moments(self):
+        """The first and second moments as float32 tensors by parameter name (for inspection or a checkpoint; with
+        8-bit state the values that the codes stand for)."""
+        if self.state_bits == 32:
+            return self.m, self.v
+        m = {k: torch.empty(self.p[k].shape, dtype=torch.float32, device=self.device) for k in self._names}
+        v = {k: torch.empty(self.p[k].shape, dtype=torch.float32, device=self.device) for k in self._names}
+        xt.xt_adamw8_decode(*self.state8, list(m.values()), list(v.values()))
+        return m, v
 
     def optimizer_step(self, n_microbatches=1, stream=None):
         """Clipped AdamW over every parameter with the gradients scaled by 1 / n_microbatches
@@ -198,6 +217,10 @@ class NativeBlock:
         shadows = None
         if self.dt != torch.float32:
             shadows = [self.p[k] for k in names]
+        if self.state_bits == 8:
+            xt.xt_adamw8_step(cfg, [self.master[k] for k in names], [self.g[k] for k in names], *self.state8,
+                              shadows=shadows, norm_out=self.grad_norm, ws=self._opt_ws, s=stream)
+            return
         xt.xt_adamw_step(cfg, [self.master[k] for k in names], [self.g[k] for k in names],
                          [self.m[k] for k in names], [self.v[k] for k in names], shadows=shadows,
                          norm_out=self.grad_norm, ws=self._opt_ws, s=stream)

@@ -367,6 +367,39 @@ def attention(q: Var, k: Var, v: Var, causal: bool = True) -> Var:
     return _bmm(probs, v, trans_b=False, alpha=1.0)
 
 
+def rope_axes(x: Var, pos: torch.Tensor, sections, H: int, hd: int, base: float = 10000.0, per_axis: bool = False) -> Var:
+    """Rotary positions over several axes on [T, H·hd] rows (pos int32 [axes, T], sections: pairs per axis)."""
+    y = _empty_like(x.value)
+    xt.xt_rope_axes_fwd(x.value, y, pos, sections, H, hd, base, int(per_axis))
+
+    def bw(g, ps):
+        g = _as(g, ps[0].value)
+        dx = _empty_like(g)
+        xt.xt_rope_axes_bwd(g, dx, pos, sections, H, hd, base, int(per_axis))
+        push(ps[0], dx, owned=True)
+    return Var(y, [x], bw)
+
+
+def attention_masked(q: Var, k: Var, v: Var, plan: torch.Tensor, H: int, Hkv: int, hd: int, scale=None, cap: float = 0.0,
+                     slopes=None) -> Var:
+    """Fused attention over packed documents on bf16 rows: q [T, H·hd], k and v [T, Hkv·hd], plan from
+    xt_attention_plan (what each token sees); cap and slopes as in xt_attention_masked_fwd.  O's rounding residual is
+    kept for the backward."""
+    T = q.value.shape[0]
+    o, o_lo = _empty_like(q.value), _empty_like(q.value)
+    lse = torch.empty((H, T), dtype=_F32, device=q.value.device)
+    kw = dict(scale=scale, cap=cap, slopes=slopes, o_lo=o_lo)
+    xt.xt_attention_masked_fwd(q.value, k.value, v.value, o, lse, plan, H, Hkv, hd, **kw)
+
+    def bw(g, ps):
+        g = _as(g, o)
+        dq, dk, dv = (_empty_like(p.value) for p in ps)
+        xt.xt_attention_masked_bwd(ps[0].value, ps[1].value, ps[2].value, o, g, lse, dq, dk, dv, plan, H, Hkv, hd, **kw)
+        for p, d in zip(ps, (dq, dk, dv)):
+            push(p, d, owned=True)
+    return Var(o, [q, k, v], bw)
+
+
 def _bmm(a: Var, b: Var, trans_b: bool, alpha: float) -> Var:
     """Batched C[z] = alpha·A[z] @ op(B[z]) over contiguous [Z, ·, ·] operands."""
     A, B = a.value, b.value
