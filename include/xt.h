@@ -299,7 +299,7 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  *   (dK and dV are sums over the query heads that share them; slopes are constants).
  * What i sees is the plan's: keys of its own document's valid tokens, with causal = 1 only those at or
  * before i and those of the document's prefix.  A token outside every document's valid part sees nothing and
- * is not seen: O = 0, lse = −∞, gradients 0; its rows of q, k, v, o and d_o may hold anything.  NaN or ∞ in a
+ * is not seen: O = 0, lse = −∞, gradients 0; its rows of q, k, v and d_o may hold anything.  NaN or ∞ in a
  * token reaches only the rows that see it.
  *
  * xt_attention_plan makes the plan of a batch, which every layer's forward and backward then use:
@@ -314,10 +314,10 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  * attention call writes nothing.
  *
  * Layout: token t of q is row t (ld_q elements apart), its head h columns [h·hd, h·hd + hd); k, v likewise
- * with Hkv heads, o, o_lo, d_o and dq as q, dk and dv as k.  lse: float32 [H][T].  o_lo (may be NULL; o's
- * layout) receives O − bf16(O), and passed to the backward is part of the O that D is formed from, as for
- * xt_attention_fwd.  scale = 0 means 1/√hd.  Gradients are overwritten.  The backward's workspace holds D (and partial sums where few shared
- * key heads are split over more of the GPU).
+ * with Hkv heads, o, d_o and dq as q, dk and dv as k.  lse: float32 [H][T].  scale = 0 means 1/√hd.
+ * Gradients are overwritten.  The backward takes the forward's o and lse; o's bf16 rounding does not reach the
+ * gradients (D is formed again from P and dP in float32; xt_attention_bwd wants the residual o_lo for that).  Its
+ * workspace holds D and lse by whole tiles (and partial sums where few shared key heads are split over the GPU).
  * Supported: dtype = XT_BF16, hd 64 or 128, row strides multiples of 8 elements, all pointers 16-byte
  * aligned, T < 2³⁰ (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
  * device-side waits are bounded (XT_DEVERR_TIMEOUT).
@@ -334,12 +334,12 @@ int xt_attention_plan_size(int64_t T, size_t* bytes);
 int xt_attention_plan(int64_t T, int n_docs, const int32_t* doc_off, const int32_t* doc_len, const int32_t* prefix,
                       int causal, void* plan, size_t plan_bytes, void* stream);
 int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
-                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* o, void* o_lo,
+                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* o,
                             int64_t ld_o, float* lse, void* stream);
 int xt_attention_masked_bwd_workspace_size(const xt_attention_desc* desc, size_t* bytes);
 int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
                             int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* o,
-                            const void* o_lo, int64_t ld_o, const void* d_o, int64_t ld_do, const float* lse, void* dq,
+                            int64_t ld_o, const void* d_o, int64_t ld_do, const float* lse, void* dq,
                             int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, void* ws, size_t ws_bytes,
                             void* stream);
 

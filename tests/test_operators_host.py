@@ -83,13 +83,13 @@ def test_adamw8_refusals(xt):
 
 
 def masked(xt, T=256, H=2, Hkv=1, hd=64, dtype=1, scale=0.0, cap=0.0, plan=16, plan_bytes=1 << 20, q=16, ld_q=128,
-           ld_k=64, o=16, o_lo=None, lse=16, bwd=False, ws=16, ws_bytes=1 << 20, dk=16, ld_dk=64):
+           ld_k=64, o=16, lse=16, bwd=False, ws=16, ws_bytes=1 << 20, dk=16, ld_dk=64):
     d = xt.AttentionDesc(T, H, Hkv, hd, dtype, scale, cap, None)
     L = xt.lib()
     if bwd:
-        return L.xt_attention_masked_bwd(C.byref(d), plan, plan_bytes, q, ld_q, 16, ld_k, 16, ld_k, o, o_lo, 128, 16, 128,
+        return L.xt_attention_masked_bwd(C.byref(d), plan, plan_bytes, q, ld_q, 16, ld_k, 16, ld_k, o, 128, 16, 128,
                                          lse, 16, 128, dk, ld_dk, 16, 64, ws, ws_bytes, None)
-    return L.xt_attention_masked_fwd(C.byref(d), plan, plan_bytes, q, ld_q, 16, ld_k, 16, ld_k, o, o_lo, 128, lse, None)
+    return L.xt_attention_masked_fwd(C.byref(d), plan, plan_bytes, q, ld_q, 16, ld_k, 16, ld_k, o, 128, lse, None)
 
 
 @pytest.mark.parametrize("bwd", [False, True])
@@ -104,7 +104,7 @@ def test_masked_attention_refusals(xt, bwd):
     assert go(cap=-1.0) == bad and go(cap=float("inf")) == bad
     assert go(plan=None) == bad and go(plan=8) == ali and go(plan_bytes=100) == bad
     assert go(q=None) == bad and go(q=24) == ali and go(ld_q=120) == bad and go(ld_q=132) == ali
-    assert go(ld_k=56) == bad and go(o=None) == bad and go(o_lo=8) == ali and go(lse=None) == bad
+    assert go(ld_k=56) == bad and go(o=None) == bad and go(lse=None) == bad
     assert go(T=0, plan=None, lse=None, q=None, o=None) == xt.XT_OK
     if bwd:
         assert go(ws=None) == bad and go(ws=8) == ali and go(ws_bytes=100) == bad

@@ -142,13 +142,12 @@ using namespace xt::attnm;
 extern "C" {
 
 int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
-                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* o, void* o_lo,
+                            int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* o,
                             int64_t ld_o, float* lse, void* stream) {
   const char* fn = "xt_attention_masked_fwd";
   const int H = desc ? desc->H : 0, Hkv = desc ? desc->Hkv : 0;
   XT_TRY(check(fn, desc, plan, plan_bytes, lse, {{q, ld_q, H}, {k, ld_k, Hkv}, {v, ld_v, Hkv}, {o, ld_o, H}}));
   if (desc->T == 0) return XT_OK;
-  if (!aligned16(o_lo)) return fail(XT_ERR_ALIGNMENT, "%s: o_lo must be 16-byte aligned", fn);
   attnm::Params p = attnm::params(desc, plan);
   p.q = static_cast<const bf16*>(q);
   p.k = static_cast<const bf16*>(k);
@@ -157,7 +156,6 @@ int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, siz
   p.ldk = ld_k;
   p.ldv = ld_v;
   p.o = static_cast<bf16*>(o);
-  p.o_lo = static_cast<bf16*>(o_lo);
   p.ldo = ld_o;
   p.lse = lse;
   CUtensorMap tq, tk, tv;
@@ -180,7 +178,7 @@ int xt_attention_masked_bwd_workspace_size(const xt_attention_desc* desc, size_t
 
 int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, size_t plan_bytes, const void* q,
                             int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* o,
-                            const void* o_lo, int64_t ld_o, const void* d_o, int64_t ld_do, const float* lse, void* dq,
+                            int64_t ld_o, const void* d_o, int64_t ld_do, const float* lse, void* dq,
                             int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, void* ws, size_t ws_bytes,
                             void* stream) {
   const char* fn = "xt_attention_masked_bwd";
@@ -189,7 +187,6 @@ int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, siz
                {{q, ld_q, H}, {k, ld_k, Hkv}, {v, ld_v, Hkv}, {o, ld_o, H}, {d_o, ld_do, H}, {dq, ld_dq, H},
                 {dk, ld_dk, Hkv}, {dv, ld_dv, Hkv}}));
   if (desc->T == 0) return XT_OK;
-  if (!aligned16(o_lo)) return fail(XT_ERR_ALIGNMENT, "%s: o_lo must be 16-byte aligned", fn);
   size_t need = 0;
   XT_TRY(xt_attention_masked_bwd_workspace_size(desc, &need));
   XT_REQUIRE(ws && ws_bytes >= need, "%s: workspace too small (%zu < %zu)", fn, ws_bytes, need);
@@ -202,7 +199,6 @@ int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, siz
   p.ldk = ld_k;
   p.ldv = ld_v;
   p.o = const_cast<bf16*>(static_cast<const bf16*>(o));
-  p.o_lo = const_cast<bf16*>(static_cast<const bf16*>(o_lo));
   p.ldo = ld_o;
   p.d_o = static_cast<const bf16*>(d_o);
   p.lddo = ld_do;

@@ -53,8 +53,8 @@ struct Params {
   const float* slopes;    // [H] (BIAS)
   const bf16 *q, *k, *v;  // rows of ldq, ldk, ldv elements
   int64_t ldq, ldk, ldv;
-  bf16 *o, *o_lo;         // o_lo: O − bf16(O), or null
-  const bf16 *d_o;
+  bf16* o;
+  const bf16* d_o;
   int64_t ldo, lddo;
   float *lse;             // [H][T]
   float *nl, *nd;         // workspace, [H][tiles·128]: −lse·log₂e (−∞ where nothing is seen) and −D
@@ -115,8 +115,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // D[tmem] (+)= A[tmem]·B: A is 128 rows × 16 bf16, two per 32-bit column, row = lane.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -361,10 +359,7 @@ __device__ __noinline__ void repair(const Params& p, int h0, int heads, int kh, 
     for (int e = 0; e < W; ++e) {
       const int64_t c = int64_t(KEY ? kh : h0) * HD + lane * W + e;
       if constexpr (FWD) {
-        const float x = a1[e] * mul;
-        const bf16 hi_x = __float2bfloat16_rn(x);
-        p.o[int64_t(rw) * p.ldo + c] = hi_x;
-        if (p.o_lo) p.o_lo[int64_t(rw) * p.ldo + c] = __float2bfloat16_rn(x - __bfloat162float(hi_x));
+        p.o[int64_t(rw) * p.ldo + c] = __float2bfloat16_rn(a1[e] * mul);
       } else if constexpr (!KEY) {
         p.dq[int64_t(rw) * p.lddq + c] = __float2bfloat16_rn(a1[e] * p.scale);
       } else if (p.split > 1) {
@@ -880,7 +875,6 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
       const bool real = row < p.plan.T;
       tc_fence_after();
       bf16* orow = p.o + int64_t(row) * p.ldo + int64_t(h) * HD;
-      bf16* lrow = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + int64_t(h) * HD : nullptr;
       float bad = 0.f;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
@@ -897,17 +891,12 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         }
         if (real) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = __uint_as_float(o[8 * u + 2 * e]), y = __uint_as_float(o[8 * u + 2 * e + 1]);
-              hi[e] = pack_bf16(x, y);
-              lo[e] = pack_bf16(x - lo_bf16(hi[e]), y - hi_bf16(hi[e]));
-            }
-            *reinterpret_cast<uint4*>(orow + c * 32 + u * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (lrow) *reinterpret_cast<uint4*>(lrow + c * 32 + u * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(orow + c * 32 + u * 8) =
+                make_uint4(pack_bf16(__uint_as_float(o[8 * u]), __uint_as_float(o[8 * u + 1])),
+                           pack_bf16(__uint_as_float(o[8 * u + 2]), __uint_as_float(o[8 * u + 3])),
+                           pack_bf16(__uint_as_float(o[8 * u + 4]), __uint_as_float(o[8 * u + 5])),
+                           pack_bf16(__uint_as_float(o[8 * u + 6]), __uint_as_float(o[8 * u + 7])));
         }
       }
       tc_fence_before();
@@ -930,19 +919,23 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // One kernel for both directions.  KEY: an item is a key tile of a key head, a thread's row a key, the
 // columns queries; dK and dV sum over the query tiles that see the tile, for the query heads of the group in
 // turn.  else: an item is a query tile of a head, a row a query, the columns keys; dQ sums over key tiles.
-// Per tile: S = (row tile)(column tile)ᵀ and dP likewise into TMEM; the rows form P = 2^(s − lse) and (KEY)
-// write it over S for dV += P dO; then dS = P∘(dP − D)∘(1 − tanh²) over dP for dK (dQ) += dS Q (K).
+// Per tile: S = (row tile)(column tile)ᵀ and dP likewise into TMEM; the rows form P = 2^(s − lse) and write it
+// over S for dV += P dO (KEY); then dS = P∘(dP − D)∘(1 − tanh²) over dP for dK (dQ) += dS Q (K).
+//
+// D.  D = Σ_j P dP over a whole row, but is wanted from the row's first tile on; dO·O has it up to the rounding of
+// the stored O, 2⁻⁹ of |dO||O|, which where P is peaked is several times the error of everything else in dS (dQ
+// off by 5.8e-3 against 2.5e-3, texts of 12 tokens).  So the query pass takes D₀ = dO·O for its dS, sums
+// T = Σ_j P(dP − D₀) beside it in float32, and adds up W K, W = P∘(1 − tanh²), as a second product: with
+// D = D₀ + T,  dQ = scale·(Σ dS₀ K − T·Σ W K)  exactly.  It leaves −lse·log₂e and −D in the workspace, rows padded
+// to whole tiles, from where the key pass, which follows it, copies them in with each query tile.
 //
 // A tile's time is the rows' chain of tensor-memory loads, exponentials, stores and barriers, several times the
 // work in it, so two chains run side by side: each half of a tile's 128 columns has its own MMA issuer, four row
 // warps (one per TMEM lane quadrant), S and dP buffers, accumulators and barriers; P and dS are elementwise, so
 // the halves never need each other until their accumulators are added at the end of an item, in the halves' order
-// (deterministic).  One chain's products and loads run during the other's exponentials.  The key pass at hd 128 has
-// tensor memory for one set of accumulators: there the halves' rows share one chain of 128 columns.
+// (deterministic).  One chain's products and loads run during the other's exponentials.  At hd 128 there is tensor
+// memory for one set of accumulators: there the halves' rows share one chain of 128 columns.
 // MEASURED-BWD
-//
-// The query pass also forms D (its rows' dO·O) and leaves −lse·log₂e and −D in the workspace, rows padded to
-// whole tiles, from where the key pass copies them in with each query tile: no kernel of its own for D.
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
 constexpr uint32_t kBwdRegsCtl = 72, kBwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
 constexpr int PW = BT / 2;        // columns of a row warp
@@ -951,15 +944,15 @@ template <int HD, bool KEY>
 struct BwdCfg {
   static constexpr int QT = HD / 64 * TILE;
   static constexpr int RING = HD == 64 ? 4 : 2;          // column tiles (pairs) in flight
-  static constexpr int CH = KEY && HD == 128 ? 1 : 2;    // chains
-  // TMEM columns: S, dP (the halves' side by side), each chain's accumulators dK or dQ, each chain's dV
+  static constexpr int CH = HD == 128 ? 1 : 2;           // chains
+  // TMEM columns: S, dP (the halves' side by side), each chain's dK or dQ, each chain's dV or W K
   static constexpr uint32_t DP = 128, ACC1 = 256, ACC2 = ACC1 + CH * HD;
   static constexpr int A = 0;                            // the row tiles: K, V or Q, dO
   static constexpr int R = A + 2 * QT;                   // ring of column tile pairs: Q, dO or K, V
-  static constexpr int VEC = R + RING * 2 * QT;          // (KEY) ring of −lse·log₂e and −D, 128 floats each; or D
+  static constexpr int VEC = R + RING * 2 * QT;          // (KEY) ring of −lse·log₂e and −D, 128 floats each; or sums of halves
   static constexpr int BARS = VEC + RING * 1024;
   static constexpr int BYTES = 1024 + BARS + 512;
-  static_assert(ACC2 + (KEY ? CH * HD : 0) <= 512, "TMEM columns");
+  static_assert(ACC2 + CH * HD <= 512, "TMEM columns");
 };
 
 template <int HD, bool KEY>
@@ -967,9 +960,9 @@ struct BwdBars {
   Queue queue;
   uint64_t a_full, a_empty, r_full[BwdCfg<HD, KEY>::RING], r_empty[BwdCfg<HD, KEY>::RING];
   struct Chain {
-    uint64_t s_full, s_free, dp_full, p_full, ds_full, acc_full, mma_done;
+    uint64_t s_full, dp_full, p_full, ds_full, acc_full, mma_done;
   } ch[2];
-  uint64_t acc_free, d_full[4];
+  uint64_t acc_free, met[4];
   uint32_t tmem, abort;
 };
 
@@ -998,7 +991,6 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
     }
     for (int c = 0; c < CH; ++c) {
       mbar_init(smem_u32(&B.ch[c].s_full), 1);
-      mbar_init(smem_u32(&B.ch[c].s_free), 8 / CH);
       mbar_init(smem_u32(&B.ch[c].dp_full), 1);
       mbar_init(smem_u32(&B.ch[c].p_full), 8 / CH);
       mbar_init(smem_u32(&B.ch[c].ds_full), 8 / CH);
@@ -1006,7 +998,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       mbar_init(smem_u32(&B.ch[c].mma_done), 1);
     }
     mbar_init(smem_u32(&B.acc_free), 8);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&B.d_full[i]), 2);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&B.met[i]), 2);
     B.abort = 0;
     fence_barrier_init();
   }
@@ -1127,10 +1119,10 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         for (int j = 0; j < n; ++j, ++g) {
           const bool next = j + 1 < n;
           if (*abort_flag) { ok = false; break; }
-          // the next S follows as soon as P has been multiplied (it lies over S), or S been read
-          if (!spin(smem_u32(KEY ? &b.p_full : &b.s_free), g & 1, p.wait_ns)) { ok = false; break; }
+          // the next S follows as soon as P has been multiplied (it lies over S)
+          if (!spin(smem_u32(&b.p_full), g & 1, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
-          if (KEY) Mma<HD>::template tn<BT / CH>(acc2, tS, PW, slot(g) + C::QT, j == 0);  // dV += Pᵀ dO
+          Mma<HD>::template tn<BT / CH>(acc2, tS, PW, slot(g) + (KEY ? C::QT : 0), j == 0);  // dV += Pᵀ dO, or W K
           if (next && !issue_s(g + 1)) { ok = false; break; }
           if (!spin(smem_u32(&b.ds_full), g & 1, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
@@ -1158,7 +1150,18 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
     const uint32_t tDP = tS + C::DP;
     auto& b = B.ch[CH == 2 ? half : 0];
     const int64_t T = p.plan.T;
-    uint32_t g = 0, na = 0;
+    uint32_t g = 0, na = 0, nm = 0;
+    // x of both halves' threads of a row, added in the halves' order; false when the wait ran out
+    auto add_halves = [&](float x, float& sum) -> bool {
+      float* meet = reinterpret_cast<float*>(smem + C::VEC) + (nm & 1) * 256;
+      meet[half * 128 + rr] = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B.met[qw]));
+      if (!warp_wait(smem_u32(&B.met[qw]), nm & 1, p.wait_ns)) return false;
+      ++nm;
+      sum = meet[rr] + meet[128 + rr];
+      return true;
+    };
 #pragma unroll 1
     for (uint32_t ni = 0;; ++ni) {
       bool ok = !__shfl_sync(0xffffffffu, *abort_flag, 0);
@@ -1184,48 +1187,30 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       const bool real = row < T;
       const int2 iv = __ldg((KEY ? p.plan.k_iv : p.plan.q_iv) + row);
       const int n = max(rg.y - rg.x, 0) * heads;
-      float nlse = -INFINITY, nD = 0.f;  // of the row (not KEY)
+      float nlse = -INFINITY, nD = 0.f, T1 = 0.f;  // not KEY: −lse·log₂e, −D₀ and this half's share of T of the row
       if constexpr (!KEY) {
         // each half adds its half of the head's columns, the halves of a row meet in shared memory
         float acc = 0.f;
         if (real && iv.y > iv.x) {
           const int64_t c0 = int64_t(h) * HD + half * (HD / 2);
           const bf16* o = p.o + int64_t(row) * p.ldo + c0;
-          const bf16* ol = p.o_lo ? p.o_lo + int64_t(row) * p.ldo + c0 : nullptr;
           const bf16* go = p.d_o + int64_t(row) * p.lddo + c0;
           const float lse = p.lse[int64_t(h) * T + row];
 #pragma unroll
           for (int c = 0; c < HD / 2; c += 8) {
-            float x[8], y[8], z[8];
+            float x[8], y[8];
             Vec<bf16>::load(o + c, x);
             Vec<bf16>::load(go + c, y);
-            if (ol) {
-              Vec<bf16>::load(ol + c, z);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] += z[e];
-            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc = fmaf(-x[e], y[e], acc);
           }
           if (lse != -INFINITY) nlse = lse * -kLog2e;
         }
-        float* meet = reinterpret_cast<float*>(smem + C::VEC) + (ni & 1) * 256;
-        meet[half * 128 + rr] = acc;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&B.d_full[qw]));
-        if (!warp_wait(smem_u32(&B.d_full[qw]), ni & 1, p.wait_ns)) {
-          if (lane == 0) give_up();
-          break;
-        }
-        nD = meet[rr] + meet[128 + rr];
-        if (half == 0) {
-          p.nl[int64_t(h) * Tp + row] = nlse;
-          p.nd[int64_t(h) * Tp + row] = nD;
-        }
+        ok = add_halves(acc, nD);
       }
       int hq = KEY ? h0 : h, t = rg.x;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j, ++g) {
+      for (int j = 0; j < n && ok; ++j, ++g) {
         const float* lv = reinterpret_cast<const float*>(smem + C::VEC + (g % RING) * 1024) + col0;
         const float slope2 = BIAS ? __ldg(p.slopes + hq) * kLog2e : 0.f;
         if (!warp_wait(smem_u32(&b.s_full), g & 1, p.wait_ns)) { ok = false; break; }
@@ -1236,11 +1221,6 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
-        if constexpr (!KEY) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&b.s_free));
-        }
         const float unit = (CAP || BIAS) ? 1.f : p.sc;
         const int side = t < tile ? 1 : t > tile ? -1 : 0;
         float slack[CAP ? PW : 1];  // 1 − tanh²
@@ -1282,50 +1262,54 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
             f32x2_unpack(f32x2_fma(pair(s[e + 2], s[e + 3]), unit2, f32x2_pack(nl.z, nl.w)), x[2], x[3]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
-            if constexpr (KEY) {
-              pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
-              pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
-            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if constexpr (CAP) x[k] *= slack[e + k];
-              s[e + k] = __float_as_uint(x[k]);
+            for (int k = 0; k < 4; ++k) s[e + k] = __float_as_uint(x[k]);
+            if constexpr (!KEY && CAP) {  // W
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] *= slack[e + k];
             }
+            pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
+            pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
           }
-          if constexpr (KEY) tmem_st16(tS + uint32_t(c / 2), pk);
+          tmem_st16(tS + uint32_t(c / 2), pk);
         }
-        if constexpr (KEY) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&b.p_full));
-        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&b.p_full));
         if (!warp_wait(smem_u32(&b.dp_full), g & 1, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
-        uint32_t d[PW];
-        tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(d));
-        tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
-        tmem_ld_wait();
+        uint64_t dot[2] = {0, 0};
         auto form_ds = [&](auto masked) {
 #pragma unroll
           for (int c = 0; c < PW; c += 32) {
-            uint32_t pk[16];
+            uint32_t d[32], pk[16];
+            tmem_ld32(tDP + uint32_t(c), d);
+            tmem_ld_wait();
 #pragma unroll
-            for (int e = c; e < c + 32; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
               float4 nd = make_float4(nD, nD, nD, nD);
-              if constexpr (KEY) nd = *reinterpret_cast<const float4*>(lv + 128 + e);
+              if constexpr (KEY) nd = *reinterpret_cast<const float4*>(lv + 128 + c + e);
               float x[4];
-              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e], d[e + 1]), f32x2_pack(nd.x, nd.y)), pair(s[e], s[e + 1])),
+              f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e], d[e + 1]), f32x2_pack(nd.x, nd.y)), pair(s[c + e], s[c + e + 1])),
                            x[0], x[1]);
               f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e + 2], d[e + 3]), f32x2_pack(nd.z, nd.w)),
-                                     pair(s[e + 2], s[e + 3])), x[2], x[3]);
+                                     pair(s[c + e + 2], s[c + e + 3])), x[2], x[3]);
               if constexpr (decltype(masked)::value) {  // a masked column's dP or D may be NaN
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  if (!(seen[c / 32] & (1u << (e - c + k)))) x[k] = 0.f;
+                  if (!(seen[c / 32] & (1u << (e + k)))) x[k] = 0.f;
               }
-              pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
-              pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
+              if constexpr (!KEY) {
+                dot[0] = f32x2_add(dot[0], f32x2_pack(x[0], x[1]));
+                dot[1] = f32x2_add(dot[1], f32x2_pack(x[2], x[3]));
+              }
+              if constexpr (CAP) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] *= slack[c + e + k];
+              }
+              pk[e >> 1] = pack_bf16(x[0], x[1]);
+              pk[(e >> 1) + 1] = pack_bf16(x[2], x[3]);
             }
             tmem_st16(tDP + uint32_t(c / 2), pk);
           }
@@ -1336,6 +1320,11 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&b.ds_full));
+        if constexpr (!KEY) {
+          float u, w;
+          f32x2_unpack(f32x2_add(dot[0], dot[1]), u, w);
+          T1 += u + w;
+        }
         if (++t == rg.y) {
           t = rg.x;
           ++hq;
@@ -1345,6 +1334,14 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         for (int c = 0; c < CH; ++c) ok = ok && warp_wait(smem_u32(&B.ch[c].acc_full), na & 1, p.wait_ns);
         ++na;
       }
+      float Tr = 0.f;
+      if constexpr (!KEY) {
+        ok = ok && add_halves(T1, Tr);
+        if (ok && half == 0) {
+          p.nl[int64_t(h) * Tp + row] = nlse;
+          p.nd[int64_t(h) * Tp + row] = nD - Tr;
+        }
+      }
       if (!ok) {
         if (lane == 0) give_up();
         break;
@@ -1352,6 +1349,18 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       // ---- epilogue: this half's HD/2 columns of the accumulators
       tc_fence_after();
       float bad = 0.f;
+      auto load_acc = [&](uint32_t at, uint32_t(&o)[32]) {  // 32 columns of both chains' accumulators
+        tmem_ld32(at, o);
+        if constexpr (CH == 2) {
+          uint32_t o1[32];
+          tmem_ld32(at + HD, o1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]));
+        } else {
+          tmem_ld_wait();
+        }
+      };
 #pragma unroll
       for (int w = 0; w < (KEY ? 2 : 1); ++w) {
         const int64_t col = int64_t(h) * HD + half * (HD / 2);
@@ -1365,17 +1374,13 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
 #pragma unroll
         for (int c = 0; c < HD / 2; c += 32) {
           uint32_t o[32];
-          if (n > 0) {
-            tmem_ld32(acc + uint32_t(c), o);
-            if constexpr (CH == 2) {
-              uint32_t o1[32];
-              tmem_ld32(acc + uint32_t(HD + c), o1);
-              tmem_ld_wait();
+          if (n > 0) load_acc(acc + uint32_t(c), o);
+          if constexpr (!KEY) {
+            uint32_t wk[32];
+            if (n > 0) load_acc(tbase + C::ACC2 + lane_off + uint32_t(half * (HD / 2) + c), wk);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]));
-            } else {
-              tmem_ld_wait();
-            }
+            for (int e = 0; e < 32; ++e)
+              if (n > 0) o[e] = __float_as_uint(fmaf(-Tr, __uint_as_float(wk[e]), __uint_as_float(o[e])));
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -1405,7 +1410,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       const uint32_t rows = __ballot_sync(0xffffffffu, bad != 0.f && real);
       if (rows)
         repair<HD, KEY, false, CAP, BIAS>(p, KEY ? h0 : h, heads, KEY ? h : h / p.group, row, iv, rows, rg.x * BT,
-                                          rg.y * BT, -nlse, -nD, 0.f, half, 2, sp);
+                                          rg.y * BT, -nlse, Tr - nD, 0.f, half, 2, sp);
     }
   }
   __syncthreads();

@@ -383,12 +383,11 @@ def rope_axes(x: Var, pos: torch.Tensor, sections, H: int, hd: int, base: float 
 def attention_masked(q: Var, k: Var, v: Var, plan: torch.Tensor, H: int, Hkv: int, hd: int, scale=None, cap: float = 0.0,
                      slopes=None) -> Var:
     """Fused attention over packed documents on bf16 rows: q [T, H·hd], k and v [T, Hkv·hd], plan from
-    xt_attention_plan (what each token sees); cap and slopes as in xt_attention_masked_fwd.  O's rounding residual is
-    kept for the backward."""
+    xt_attention_plan (what each token sees); cap and slopes as in xt_attention_masked_fwd."""
     T = q.value.shape[0]
-    o, o_lo = _empty_like(q.value), _empty_like(q.value)
+    o = _empty_like(q.value)
     lse = torch.empty((H, T), dtype=_F32, device=q.value.device)
-    kw = dict(scale=scale, cap=cap, slopes=slopes, o_lo=o_lo)
+    kw = dict(scale=scale, cap=cap, slopes=slopes)
     xt.xt_attention_masked_fwd(q.value, k.value, v.value, o, lse, plan, H, Hkv, hd, **kw)
 
     def bw(g, ps):

@@ -125,11 +125,11 @@ _SIGS = {
                          _I, _I, _I, _I, _I, _I, _VP],
     "xt_attention_plan_size": [_I64, _SZP],
     "xt_attention_plan": [_I64, _I, _VP, _VP, _VP, _I, _VP, C.c_size_t, _VP],
-    "xt_attention_masked_fwd": [C.POINTER(AttentionDesc), _VP, C.c_size_t, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP,
-                                _I64, _VP, _VP],
+    "xt_attention_masked_fwd": [C.POINTER(AttentionDesc), _VP, C.c_size_t, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64,
+                                _VP, _VP],
     "xt_attention_masked_bwd_workspace_size": [C.POINTER(AttentionDesc), _SZP],
-    "xt_attention_masked_bwd": [C.POINTER(AttentionDesc), _VP, C.c_size_t, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP,
-                                _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, C.c_size_t, _VP],
+    "xt_attention_masked_bwd": [C.POINTER(AttentionDesc), _VP, C.c_size_t, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64,
+                                _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, C.c_size_t, _VP],
     "xt_cross_entropy_workspace_size": [_I64, _SZP],
     "xt_cross_entropy_fwd": [_VP, _VP, _VP, _VP, _I64, _I64, _I, _VP, _VP],
     "xt_cross_entropy_fwd_bwd": [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I, _VP, _VP],
@@ -585,26 +585,22 @@ def _token_rows(T, hd, dtype, *pairs):
     return out
 
 
-def xt_attention_masked_fwd(q, k, v, o, lse, plan, H, Hkv, hd, scale=None, cap=0.0, slopes=None, o_lo=None, s=None):
+def xt_attention_masked_fwd(q, k, v, o, lse, plan, H, Hkv, hd, scale=None, cap=0.0, slopes=None, s=None):
     """q, o [T, H·hd], k, v [T, Hkv·hd] bf16 views with unit column stride, lse float32 [H, T]; plan: from
     xt_attention_plan; cap: tanh cap of the scores (0: none); slopes: float32 [H] or None."""
     T = q.shape[0]
-    if o_lo is not None and (o_lo.shape != o.shape or o_lo.stride() != o.stride() or o_lo.dtype != o.dtype):
-        raise ValueError("o_lo must have o's layout")
     if lse.dtype != torch.float32 or lse.numel() != H * T:
         raise ValueError("lse must be float32 [H, T]")
     d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
     q_, k_, v_, o_ = (_token_rows(T, hd, q.dtype, x) for x in ((q, H), (k, Hkv), (v, Hkv), (o, H)))
-    call("xt_attention_masked_fwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, o_[0],
-         ptr(o_lo, False), o_[1], ptr(lse), stream(s))
+    call("xt_attention_masked_fwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, *o_,
+         ptr(lse), stream(s))
 
 
 def xt_attention_masked_bwd(q, k, v, o, d_o, lse, dq, dk, dv, plan, H, Hkv, hd, scale=None, cap=0.0, slopes=None,
-                            o_lo=None, ws=None, s=None):
-    """Gradients of xt_attention_masked_fwd (its o, lse and o_lo); dq, dk, dv in the layouts of q, k, v."""
+                            ws=None, s=None):
+    """Gradients of xt_attention_masked_fwd (its o and lse); dq, dk, dv [T, heads·hd] views like q, k, v."""
     T = q.shape[0]
-    if o_lo is not None and (o_lo.shape != o.shape or o_lo.stride() != o.stride() or o_lo.dtype != o.dtype):
-        raise ValueError("o_lo must have o's layout")
     if lse.dtype != torch.float32 or lse.numel() != H * T:
         raise ValueError("lse must be float32 [H, T]")
     d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
@@ -612,8 +608,8 @@ def xt_attention_masked_bwd(q, k, v, o, d_o, lse, dq, dk, dv, plan, H, Hkv, hd, 
         ws = attention_masked_workspace(T, H, Hkv, hd, q.device)
     q_, k_, v_, o_, do_, dq_, dk_, dv_ = (_token_rows(T, hd, q.dtype, x) for x in (
         (q, H), (k, Hkv), (v, Hkv), (o, H), (d_o, H), (dq, H), (dk, Hkv), (dv, Hkv)))
-    call("xt_attention_masked_bwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, o_[0],
-         ptr(o_lo, False), o_[1], *do_, ptr(lse), *dq_, *dk_, *dv_, ptr(ws), ws.numel() * ws.element_size(), stream(s))
+    call("xt_attention_masked_bwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, *o_,
+         *do_, ptr(lse), *dq_, *dk_, *dv_, ptr(ws), ws.numel() * ws.element_size(), stream(s))
 
 
 def xt_softmax_bwd(d, y, dx, causal=0, q_len=0, acc=0, s=None):
