@@ -1,4 +1,5 @@
 // Entry points of masked attention: argument checks, tensor maps, launches (the kernels: attention_masked.cuh).
+#include <cstring>
 #include <mutex>
 #include <set>
 #include <utility>
@@ -123,7 +124,15 @@ attnm::Params params(const xt_attention_desc* d, const void* plan) {
   p.scale = float(scale);
   p.sc = float(scale * log2e);
   if (d->cap > 0.f) {
+    p.capy = float(scale / double(d->cap));
     p.capk = float(2.0 * log2e * scale / double(d->cap));
+    constexpr float kTanh[7] = {0.9999997019767761f,  -0.33332130312919617f,  0.13319583237171173f, -0.05326583608984947f,
+                                0.019973281770944595f, -0.005951280705630779f, 0.0009637721814215183f};
+    for (int k = 0; k < 7; ++k) {
+      uint32_t w;
+      std::memcpy(&w, &kTanh[k], 4);
+      p.tanh_c[k] = uint64_t(w) << 32 | w;
+    }
     p.cap2 = float(double(d->cap) * log2e);
   }
   p.slopes = d->slopes;

@@ -26,6 +26,8 @@
 // when its last load of this one is issued and leaves its description in shared memory for the other warps.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "attention_plan.cuh"
@@ -49,7 +51,8 @@ struct Params {
   int split, share;       // key pass: items per key head and tile, query heads of each (but the last)
   float sc;               // scale·log₂e
   float scale;
-  float capk, cap2;       // 2·log₂e·scale/cap, cap·log₂e (CAP)
+  float capy, capk, cap2; // scale/cap, 2·log₂e·scale/cap, cap·log₂e (CAP)
+  uint64_t tanh_c[7];     // coefficients of tanh(y)/y in y², twice each
   const float* slopes;    // [H] (BIAS)
   const bf16 *q, *k, *v;  // rows of ldq, ldk, ldv elements
   int64_t ldq, ldk, ldv;
@@ -178,37 +181,77 @@ __device__ __forceinline__ uint32_t visible_bits(int lo, int hi, int base) {
   return below_hi & ~below_lo;
 }
 
-// r[c] −= slope₂·|d0 + c|.
+// r[c] = unit·r[c] − slope₂·|d0 + c|.  d0: column 0 minus the row, in tokens; side: +1 / −1 where every column of the
+// tile lies before / behind the row (the distance is then linear in c), 0 else.
 template <int N>
-__device__ __forceinline__ void add_bias(uint32_t (&r)[N], float slope2, int d0, int side) {
+__device__ __forceinline__ void add_bias(uint32_t (&r)[N], float unit, float slope2, int d0, int side) {
   if (side != 0) {
     const float st = side > 0 ? slope2 : -slope2, b0 = st * float(d0);
+    const uint64_t unit2 = f32x2_pack(unit, unit), step2 = f32x2_pack(2.f * st, 2.f * st);
 #pragma unroll
-    for (int c = 0; c < N; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + fmaf(float(c), st, b0));
+    for (int c = 0; c < N; c += 16) {  // two columns at a time; afresh every 16, so that the steps' roundings stay few
+      uint64_t b = f32x2_pack(fmaf(float(c), st, b0), fmaf(float(c + 1), st, b0));
+#pragma unroll
+      for (int e = c; e < c + 16; e += 2) {
+        float x, y;
+        f32x2_unpack(f32x2_fma(pair(r[e], r[e + 1]), unit2, b), x, y);
+        r[e] = __float_as_uint(x);
+        r[e + 1] = __float_as_uint(y);
+        b = f32x2_add(b, step2);
+      }
+    }
   } else {
     const float d = float(d0);
 #pragma unroll
-    for (int c = 0; c < N; ++c) r[c] = __float_as_uint(fmaf(-slope2, fabsf(d + float(c)), __uint_as_float(r[c])));
+    for (int c = 0; c < N; ++c)
+      r[c] = __float_as_uint(fmaf(-slope2, fabsf(d + float(c)), unit * __uint_as_float(r[c])));
   }
 }
 
-// Scores of one row, r[c] = q·k of column base + c, to s·log₂e (CAP or BIAS; without both the caller
-// scales).  d0: column 0 minus the row, in tokens; side: +1 / −1 where every column of the tile lies before
-// / behind the row (the distance is then linear in c), 0 else.
-template <int N, bool CAP, bool BIAS>
-__device__ __forceinline__ void to_log2(uint32_t (&r)[N], const Params& p, float slope2, int d0, int side) {
-  if constexpr (CAP) {
+// r[c] = tanh(scale·r[c]/cap) = 1 − 2/(1 + e^{2y}), one exponential and one reciprocal.  Where no element of the
+// warp's rows is beyond the cap the special-function unit and the multipliers share the work: of four columns two go
+// through y·p(y²), p of degree 6 fitted to tanh(y)/y over |y| ≤ 1 (least squares reweighted to equal extremes,
+// Lawson's method; error 9e-8), and two through exponentials and the reciprocal of the product of their
+// denominators, 1/a = b·1/(ab) (at most 8.4² there).
+// MEASURED-CAP
+template <int N>
+__device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      // cap·tanh(a/cap) = cap − 2·cap/(1 + e^{2a/cap}): one exponential, one reciprocal, absolute error ~2⁻²²·cap
-      const float e = ex2(__uint_as_float(r[c]) * p.capk);
-      r[c] = __float_as_uint(fmaf(-2.f * p.cap2, rcp(1.f + e), p.cap2));
-    }
+  for (int c = 0; c < N; c += 2)
+    top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(__uint_as_float(r[c])), fabsf(__uint_as_float(r[c + 1])));
+  const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.capy;
+  if (__any_sync(0xffffffffu, !(most <= 1.f))) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      r[c] = __float_as_uint(fmaf(-2.f, rcp(1.f + ex2(__uint_as_float(r[c]) * p.capk)), 1.f));
   } else {
+    const uint64_t y2 = f32x2_pack(p.capy, p.capy), k2 = f32x2_pack(p.capk, p.capk), one2 = f32x2_pack(1.f, 1.f);
 #pragma unroll
-    for (int c = 0; c < N; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * p.sc);
+    for (int c = 0; c < N; c += 4) {
+      float u, w;
+      f32x2_unpack(f32x2_mul(pair(r[c + 2], r[c + 3]), k2), u, w);
+      u = ex2(u);
+      w = ex2(w);
+      const uint64_t y = f32x2_mul(pair(r[c], r[c + 1]), y2), z = f32x2_mul(y, y);
+      uint64_t q = p.tanh_c[6];
+#pragma unroll
+      for (int k = 5; k >= 0; --k) q = f32x2_fma(q, z, p.tanh_c[k]);
+      f32x2_unpack(f32x2_add(f32x2_pack(u, w), one2), u, w);
+      const float i = -2.f * rcp(u * w);
+      r[c + 2] = __float_as_uint(fmaf(i, w, 1.f));
+      r[c + 3] = __float_as_uint(fmaf(i, u, 1.f));
+      f32x2_unpack(f32x2_mul(y, q), u, w);
+      r[c] = __float_as_uint(u);
+      r[c + 1] = __float_as_uint(w);
+    }
   }
-  if constexpr (BIAS) add_bias(r, slope2, d0, side);
+}
+
+// What the scores are multiplied by on their way into the exponential (base 2), after the two steps above.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score_unit(const Params& p) {
+  return BIAS ? 1.f : CAP ? p.cap2 : p.sc;
 }
 
 // ------------------------------------------------------------------------------ the careful path
@@ -784,9 +827,9 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
       const int row = tile * BT + rr;
       const int2 iv = __ldg(p.plan.q_iv + row);
       const float slope2 = BIAS ? __ldg(p.slopes + h) * kLog2e : 0.f;
-      float m = -INFINITY;  // running max, of the raw scores or (CAP, BIAS) of s·log₂e
-      float l = 0.f;        // running Σ 2^(s − m)
-      const float unit = (CAP || BIAS) ? 1.f : p.sc;
+      float m = -INFINITY;  // running max of the scores before `unit`
+      float l = 0.f;        // running Σ 2^((s − m)·unit)
+      const float unit = score_unit<CAP, BIAS>(p);
 #pragma unroll 1
       for (int j = rg.x; j < rg.y; ++j, ++g) {
         if (!warp_wait(smem_u32(&b.s_full), g & 1, p.wait_ns)) { ok = false; break; }
@@ -800,8 +843,8 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&b.s_free));
         }
-        if constexpr (CAP || BIAS)
-          to_log2<128, CAP, BIAS>(s, p, slope2, j * BT - row, j < tile ? 1 : j > tile ? -1 : 0);
+        if constexpr (CAP) tanh_cap(s, p);
+        if constexpr (BIAS) add_bias(s, CAP ? p.cap2 : p.sc, slope2, j * BT - row, j < tile ? 1 : j > tile ? -1 : 0);
         if (j < rg.z || j >= rg.w) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -1221,20 +1264,22 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
-        const float unit = (CAP || BIAS) ? 1.f : p.sc;
-        const int side = t < tile ? 1 : t > tile ? -1 : 0;
-        float slack[CAP ? PW : 1];  // 1 − tanh²
+        const float unit = score_unit<CAP, BIAS>(p);
+        // 1 − tanh² ∈ [0, 1], as f16: half a step of 2⁻¹² beside dS's own bf16 rounding of 2⁻⁹, for half the registers
+        __half2 slack[CAP ? PW / 2 : 1];
         if constexpr (CAP) {
+          tanh_cap(s, p);
+          const uint64_t one2 = f32x2_pack(1.f, 1.f), neg2 = f32x2_pack(-1.f, -1.f);
 #pragma unroll
-          for (int c = 0; c < PW; ++c) {  // as to_log2, keeping u = 1/(1 + e^{2a/cap}): 1 − tanh² = 4u(1 − u)
-            const float u = rcp(1.f + ex2(__uint_as_float(s[c]) * p.capk));
-            s[c] = __float_as_uint(fmaf(-2.f * p.cap2, u, p.cap2));
-            slack[c] = 4.f * u * (1.f - u);
+          for (int c = 0; c < PW; c += 2) {
+            const uint64_t y = pair(s[c], s[c + 1]);
+            float u, w;
+            f32x2_unpack(f32x2_fma(f32x2_mul(y, neg2), y, one2), u, w);
+            slack[c / 2] = __floats2half2_rn(u, w);
           }
-          if constexpr (BIAS) add_bias(s, slope2, t * BT + col0 - row, side);
-        } else if constexpr (BIAS) {
-          to_log2<PW, CAP, BIAS>(s, p, slope2, t * BT + col0 - row, side);
         }
+        if constexpr (BIAS)
+          add_bias(s, CAP ? p.cap2 : p.sc, slope2, t * BT + col0 - row, t < tile ? 1 : t > tile ? -1 : 0);
         const bool edge = t < rg.z || t >= rg.w;
         uint32_t seen[2] = {~0u, ~0u};
         if (edge) {
@@ -1243,10 +1288,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
             seen[w] = visible_bits(iv.x - t * BT, iv.y - t * BT, col0 + 32 * w);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (!(seen[w] & (1u << c))) {
-                s[32 * w + c] = __float_as_uint(-INFINITY);
-                if constexpr (CAP) slack[32 * w + c] = 0.f;
-              }
+              if (!(seen[w] & (1u << c))) s[32 * w + c] = __float_as_uint(-INFINITY);
           }
         }
         const uint64_t unit2 = f32x2_pack(unit, unit);
@@ -1264,9 +1306,13 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
             for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[e + k] = __float_as_uint(x[k]);
-            if constexpr (!KEY && CAP) {  // W
+            if constexpr (!KEY && CAP) {  // W (a masked column's tanh may be NaN: its P stays 0)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] *= slack[e + k];
+              for (int k = 0; k < 4; k += 2) {
+                const float2 u = __half22float2(slack[(e + k) / 2]);
+                x[k] = x[k] == 0.f ? 0.f : x[k] * u.x;
+                x[k + 1] = x[k + 1] == 0.f ? 0.f : x[k + 1] * u.y;
+              }
             }
             pk[(e - c) >> 1] = pack_bf16(x[0], x[1]);
             pk[((e - c) >> 1) + 1] = pack_bf16(x[2], x[3]);
@@ -1295,19 +1341,27 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
                            x[0], x[1]);
               f32x2_unpack(f32x2_mul(f32x2_add(pair(d[e + 2], d[e + 3]), f32x2_pack(nd.z, nd.w)),
                                      pair(s[c + e + 2], s[c + e + 3])), x[2], x[3]);
-              if constexpr (decltype(masked)::value) {  // a masked column's dP or D may be NaN
+              auto hide = [&]() {  // a masked column's dP, D or tanh may be NaN
+                if constexpr (decltype(masked)::value) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (!(seen[c / 32] & (1u << (e + k)))) x[k] = 0.f;
-              }
+                  for (int k = 0; k < 4; ++k)
+                    if (!(seen[c / 32] & (1u << (e + k)))) x[k] = 0.f;
+                }
+              };
               if constexpr (!KEY) {
+                hide();
                 dot[0] = f32x2_add(dot[0], f32x2_pack(x[0], x[1]));
                 dot[1] = f32x2_add(dot[1], f32x2_pack(x[2], x[3]));
               }
               if constexpr (CAP) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] *= slack[c + e + k];
+                for (int k = 0; k < 4; k += 2) {
+                  const float2 u = __half22float2(slack[(c + e + k) / 2]);
+                  x[k] *= u.x;
+                  x[k + 1] *= u.y;
+                }
               }
+              if constexpr (KEY || CAP) hide();
               pk[e >> 1] = pack_bf16(x[0], x[1]);
               pk[(e >> 1) + 1] = pack_bf16(x[2], x[3]);
             }
