@@ -238,6 +238,22 @@ def test_masked_values_that_are_not_finite(hd, bad):
     assert not bool(torch.isfinite(got["o"][195]).any())
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("first", [129, 130, 131, 132])
+def test_capped_scores_beside_a_masked_nan(hd, first):
+    """A document's first column beside the NaN of the last token before it, at each place among four columns."""
+    c = Case(off=[0, first, 270], H=2, Hkv=1, hd=hd, cap=20.0)
+    val, tol = c.reference()
+    for t in (c.qkv, c.do):
+        t[first - 1] = float("nan")
+    got = c.run()
+    keep = slice(first, 270)
+    for n in ("o", "dq", "dk", "dv"):
+        compare({n: got[n][keep]}, {n: val[n][keep]}, {n: tol[n][keep]}, (n,))
+    early = slice(0, first - 1)  # causal: they do not see it, and no gradient of O comes from it
+    compare({"o": got["o"][early]}, {"o": val["o"][early]}, {"o": tol["o"][early]}, ("o",))
+
+
 def test_deterministic_strides_stream_and_capture():
     c = Case(off=[0, 300, 700], H=4, Hkv=2, hd=64, cap=20.0, bias=True)
     a = c.run()

@@ -83,6 +83,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+// NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -212,15 +218,16 @@ __device__ __forceinline__ void add_bias(uint32_t (&r)[N], float unit, float slo
 // warp's rows is beyond the cap the special-function unit and the multipliers share the work: of four columns two go
 // through y·p(y²), p of degree 6 fitted to tanh(y)/y over |y| ≤ 1 (least squares reweighted to equal extremes,
 // Lawson's method; error 9e-8), and two through exponentials and the reciprocal of the product of their
-// denominators, 1/a = b·1/(ab) (at most 8.4² there).
+// denominators, 1/a = b·1/(ab) (at most 8.4² there).  A NaN, which may stand in a masked column, must not reach the
+// column it would share a reciprocal with: it counts as beyond the cap.
 // MEASURED-CAP
 template <int N>
 __device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < N; c += 2)
-    top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(__uint_as_float(r[c])), fabsf(__uint_as_float(r[c + 1])));
-  const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.capy;
+    top[(c >> 1) & 3] = max3_nan(top[(c >> 1) & 3], fabsf(__uint_as_float(r[c])), fabsf(__uint_as_float(r[c + 1])));
+  const float most = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], 0.f) * p.capy;
   if (__any_sync(0xffffffffu, !(most <= 1.f))) {
 #pragma unroll
     for (int c = 0; c < N; ++c)
