@@ -318,15 +318,16 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  * Gradients are overwritten.  The backward takes the forward's o and lse; o's bf16 rounding does not reach the
  * gradients (D is formed again from P and dP in float32; xt_attention_bwd wants the residual o_lo for that).  Its
  * workspace holds D and lse by whole tiles (and partial sums where few shared key heads are split over the GPU).
+ * Outputs, inputs, the plan and the workspace must not overlap (views of one buffer's columns do not).
  * Supported: dtype = XT_BF16, hd 64 or 128, row strides multiples of 8 elements, all pointers 16-byte
- * aligned, T < 2³⁰ (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
+ * aligned, T < 2³⁰, n_docs < 2³⁰, cap ≤ 1024 (a larger one leaves bf16-sized scores as they are: use 0) (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
  * device-side waits are bounded (XT_DEVERR_TIMEOUT).
  * ------------------------------------------------------------------------------- */
 typedef struct xt_attention_desc {
   int64_t T;
   int32_t H, Hkv, hd, dtype;
   float scale;         /* 0: 1/sqrt(hd) */
-  float cap;           /* 0: scores are not capped */
+  float cap;           /* at most 1024; 0: scores are not capped */
   const float* slopes; /* device, [H], or NULL: no distance bias */
 } xt_attention_desc;
 

@@ -171,6 +171,7 @@ CASES = {
     "tail-outside": dict(off=[3, 200], H=2, T=333),
     "cap": dict(off=[0, 140, 270], H=2, cap=30.0, qstd=8.0),
     "cap-128": dict(off=[0, 140, 270], H=4, Hkv=2, hd=128, cap=50.0, qstd=8.0),
+    "cap-large": dict(off=[0, 140, 270], H=2, cap=1000.0, qstd=8.0),
     "cap-small": dict(off=[0, 200], H=1, cap=0.5, qstd=1.0),
     "bias": dict(off=[0, 140, 470], H=3, bias=True),
     "bias-128": dict(off=[0, 140, 470], H=3, hd=128, bias=True),

@@ -102,6 +102,8 @@ def test_masked_attention_refusals(xt, bwd):
     assert go(hd=32) == uns and go(hd=96) == uns
     assert go(scale=-1.0) == bad and go(scale=float("nan")) == bad
     assert go(cap=-1.0) == bad and go(cap=float("inf")) == bad
+    # caps beyond what one exponential resolves, and so small that the scores' multiplier overflows
+    assert go(cap=1025.0) == bad and go(cap=1e-40) == bad and go(cap=1e-6, scale=1e34) == bad
     assert go(plan=None) == bad and go(plan=8) == ali and go(plan_bytes=100) == bad
     assert go(q=None) == bad and go(q=24) == ali and go(ld_q=120) == bad and go(ld_q=132) == ali
     assert go(ld_k=56) == bad and go(o=None) == bad and go(lse=None) == bad
@@ -119,7 +121,7 @@ def test_attention_plan_refusals(xt):
     assert L.xt_attention_plan_size(1000, C.byref(n)) == xt.XT_OK
     go = lambda T=1000, docs=4, off=None, causal=1, plan=16, size=n.value: L.xt_attention_plan(  # noqa: E731
         T, docs, off, None, None, causal, plan, size, None)
-    assert go(T=-1) == bad and go(T=1 << 30) == bad and go(docs=-1) == bad
+    assert go(T=-1) == bad and go(T=1 << 30) == bad and go(docs=-1) == bad and go(docs=1 << 30, off=16) == bad
     assert go(docs=3) == bad and go(docs=0) == bad     # equal spans need a divisor
     assert go(causal=2) == bad and go(plan=None) == bad and go(size=n.value - 1) == bad
     assert go(plan=8) == xt.XT_ERR_ALIGNMENT

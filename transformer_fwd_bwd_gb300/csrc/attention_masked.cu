@@ -70,6 +70,31 @@ struct Strided {
   int heads;
 };
 
+// The part of the kernels' parameters that the desc gives.
+attnm::Params params_of(const xt_attention_desc* d) {
+  Params p{};
+  p.H = d->H;
+  p.Hkv = d->Hkv;
+  p.group = d->H / d->Hkv;
+  const double scale = d->scale > 0.f ? double(d->scale) : 1.0 / std::sqrt(double(d->hd)), log2e = 1.4426950408889634;
+  p.scale = float(scale);
+  p.sc = float(scale * log2e);
+  if (d->cap > 0.f) {
+    p.capy = float(scale / double(d->cap));
+    p.capk = float(2.0 * log2e * scale / double(d->cap));
+    constexpr float kTanh[7] = {0.9999997019767761f,  -0.33332130312919617f,  0.13319583237171173f, -0.05326583608984947f,
+                                0.019973281770944595f, -0.005951280705630779f, 0.0009637721814215183f};
+    for (int k = 0; k < 7; ++k) {
+      uint32_t w;
+      std::memcpy(&w, &kTanh[k], 4);
+      p.tanh_c[k] = uint64_t(w) << 32 | w;
+    }
+    p.cap2 = float(double(d->cap) * log2e);
+  }
+  p.slopes = d->slopes;
+  return p;
+}
+
 int check(const char* fn, const xt_attention_desc* d, const void* plan, size_t plan_bytes, const void* lse,
           std::initializer_list<Strided> xs) {
   XT_REQUIRE(d != nullptr, "%s: desc is NULL", fn);
@@ -78,7 +103,10 @@ int check(const char* fn, const xt_attention_desc* d, const void* plan, size_t p
   if (d->dtype != XT_BF16) return fail(XT_ERR_UNSUPPORTED, "%s: only bf16 is supported", fn);
   if (d->hd != 64 && d->hd != 128) return fail(XT_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", fn);
   XT_REQUIRE(std::isfinite(d->scale) && d->scale >= 0.f, "%s: scale must be finite and not negative", fn);
-  XT_REQUIRE(std::isfinite(d->cap) && d->cap >= 0.f, "%s: cap must be finite and not negative", fn);
+  // the capped scores' exponential form is off by 2⁻²³ of the cap, 1.2e-4 at the largest one taken; the scores'
+  // multiplier of a tiny cap must stay finite
+  XT_REQUIRE(d->cap >= 0.f && d->cap <= 1024.f, "%s: cap must be in [0, 1024]", fn);
+  XT_REQUIRE(d->cap == 0.f || std::isfinite(params_of(d).capk), "%s: cap too small for this scale", fn);
   const attn_plan::Layout l(d->T);
   if (l.tiles * d->H >= (int64_t(1) << 30)) return fail(XT_ERR_UNSUPPORTED, "%s: too many tokens times heads", fn);
   if (d->T == 0) return XT_OK;
@@ -92,6 +120,14 @@ int check(const char* fn, const xt_attention_desc* d, const void* plan, size_t p
     if (!aligned16(x.p)) return fail(XT_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned", fn);
   }
   return XT_OK;
+}
+
+attnm::Params params(const xt_attention_desc* d, const void* plan) {
+  Params p = params_of(d);
+  p.plan = attn_plan::view(plan, d->T);
+  p.flag = errflag();
+  p.wait_ns = wait_limit_ns();
+  return p;
 }
 
 // Items of the key pass per key tile and head: shared key heads leave few of them, each over the whole group
@@ -112,33 +148,6 @@ size_t d_bytes(const xt_attention_desc* d) {  // nl and nd, rows of whole tiles
 }
 size_t part_bytes(const xt_attention_desc* d, int split) {
   return (size_t(split) * size_t(d->T) * size_t(d->Hkv) * size_t(d->hd) * 4 + 255) & ~size_t(255);
-}
-
-attnm::Params params(const xt_attention_desc* d, const void* plan) {
-  Params p{};
-  p.plan = attn_plan::view(plan, d->T);
-  p.H = d->H;
-  p.Hkv = d->Hkv;
-  p.group = d->H / d->Hkv;
-  const double scale = d->scale > 0.f ? double(d->scale) : 1.0 / std::sqrt(double(d->hd)), log2e = 1.4426950408889634;
-  p.scale = float(scale);
-  p.sc = float(scale * log2e);
-  if (d->cap > 0.f) {
-    p.capy = float(scale / double(d->cap));
-    p.capk = float(2.0 * log2e * scale / double(d->cap));
-    constexpr float kTanh[7] = {0.9999997019767761f,  -0.33332130312919617f,  0.13319583237171173f, -0.05326583608984947f,
-                                0.019973281770944595f, -0.005951280705630779f, 0.0009637721814215183f};
-    for (int k = 0; k < 7; ++k) {
-      uint32_t w;
-      std::memcpy(&w, &kTanh[k], 4);
-      p.tanh_c[k] = uint64_t(w) << 32 | w;
-    }
-    p.cap2 = float(double(d->cap) * log2e);
-  }
-  p.slopes = d->slopes;
-  p.flag = errflag();
-  p.wait_ns = wait_limit_ns();
-  return p;
 }
 
 }  // namespace

@@ -202,7 +202,7 @@ int xt_attention_plan_size(int64_t T, size_t* bytes) {
 int xt_attention_plan(int64_t T, int n_docs, const int32_t* doc_off, const int32_t* doc_len, const int32_t* prefix,
                       int causal, void* plan, size_t plan_bytes, void* stream) {
   XT_REQUIRE(T >= 0 && T < (int64_t(1) << 30), "xt_attention_plan: T must be in [0, 2^30)");
-  XT_REQUIRE(n_docs >= 0, "xt_attention_plan: negative document count");
+  XT_REQUIRE(n_docs >= 0 && n_docs < (1 << 30), "xt_attention_plan: n_docs must be in [0, 2^30)");
   XT_REQUIRE(causal == 0 || causal == 1, "xt_attention_plan: causal must be 0 or 1");
   XT_REQUIRE(doc_off || (n_docs > 0 ? T % n_docs == 0 : T == 0),
              "xt_attention_plan: without doc_off T must be a multiple of n_docs");
