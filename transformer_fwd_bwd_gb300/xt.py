@@ -771,66 +771,52 @@ def adamw8_workspace(numels, device="cuda"):
     return workspace(ws_bytes("xt_adamw8_workspace_size", len(numels), arr), device)
 
 
-def _ptrs(tensors):
-    return (C.c_void_p * max(1, len(tensors)))(*[t.data_ptr() if t is not None else None for t in tensors])
-
-
-def _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale):
-    if not (len(m_code) == len(r_code) == len(m_scale) == len(r_scale) == n):
+def _table(tensors, dtype, numel, per=1):
+    """Device addresses of contiguous CUDA tensors of one dtype with ceil(numel / per) elements each."""
+    if len(tensors) != len(numel):
         raise ValueError("the lists must have the same length")
-    for lst, dtype, per in ((m_code, torch.int8, 1), (r_code, torch.uint8, 1), (m_scale, torch.float32, 256),
-                            (r_scale, torch.float32, 256)):
-        for t, k in zip(lst, numel):
-            if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-                raise ValueError("codes are contiguous int8 (m) and uint8 (r), scales float32 CUDA tensors")
-            if t.numel() != -(-k // per):
-                raise ValueError("code and scale sizes must match the tensors")
+    out = [t.data_ptr() for t, k in zip(tensors, numel)
+           if t.dtype is dtype and t.is_cuda and t.numel() == (k + per - 1) // per and t.is_contiguous()]
+    if len(out) != len(numel):
+        raise ValueError(f"expected contiguous CUDA tensors of {dtype} with the parameters' sizes"
+                         + (f" in blocks of {per}" if per > 1 else ""))
+    return (C.c_void_p * max(1, len(out)))(*out)
+
+
+def _adamw8_tables(numel, m_code, r_code, m_scale, r_scale):
+    return (_table(m_code, torch.int8, numel), _table(r_code, torch.uint8, numel),
+            _table(m_scale, torch.float32, numel, 256), _table(r_scale, torch.float32, numel, 256))
 
 
 def xt_adamw8_step(cfg, params, grads, m_code, r_code, m_scale, r_scale, shadows=None, norm_out=None, ws=None, s=None):
     """One AdamW step with the moments in 8 bits over lists of float32 tensors (see adamw8_state; params and
     the state are updated in place); shadows, norm_out as for xt_adamw_step."""
-    n = len(params)
-    if len(grads) != n:
-        raise ValueError("params and grads must have the same length")
-    for t in list(params) + list(grads):
-        if t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError("params and grads must be contiguous float32 CUDA tensors")
     numel = [t.numel() for t in params]
-    if [t.numel() for t in grads] != numel:
-        raise ValueError("tensor sizes differ")
-    _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale)
+    n = len(numel)
+    tables = (_table(params, torch.float32, numel), _table(grads, torch.float32, numel),
+              *_adamw8_tables(numel, m_code, r_code, m_scale, r_scale))
     sh, sdt = None, XT_F32
     if shadows is not None:
-        dts = {t.dtype for t in shadows if t is not None}
-        if len(dts) > 1 or len(shadows) != n:
-            raise ValueError("shadows must share one dtype, one entry for each tensor")
-        for t, k in zip(shadows, numel):
-            if t is not None and (t.numel() != k or not t.is_contiguous()):
-                raise ValueError("shadow shapes must match params")
         sdt = next((dt(t) for t in shadows if t is not None), XT_F32)
-        sh = _ptrs(shadows)
-    N = (C.c_int64 * max(1, n))(*numel)
+        td = torch.bfloat16 if sdt == XT_BF16 else torch.float32
+        if len(shadows) != n or any(t is not None and (t.dtype is not td or not t.is_cuda or t.numel() != k
+                                                       or not t.is_contiguous()) for t, k in zip(shadows, numel)):
+            raise ValueError("shadows must be contiguous CUDA tensors of one dtype and the parameters' sizes, one "
+                             "entry for each")
+        sh = (C.c_void_p * max(1, n))(*[t.data_ptr() if t is not None else None for t in shadows])
     if ws is None and n and (cfg.max_grad_norm > 0 or norm_out is not None):
         ws = adamw8_workspace(numel, params[0].device)
-    call("xt_adamw8_step", C.byref(cfg), n, _ptrs(params), _ptrs(grads), _ptrs(m_code), _ptrs(r_code), _ptrs(m_scale),
-         _ptrs(r_scale), sh, sdt, N, ptr(norm_out), ptr(ws), ws.numel() if ws is not None else 0, stream(s))
+    call("xt_adamw8_step", C.byref(cfg), n, *tables, sh, sdt, (C.c_int64 * max(1, n))(*numel), ptr(norm_out), ptr(ws),
+         ws.numel() if ws is not None else 0, stream(s))
 
 
 def xt_adamw8_decode(m_code, r_code, m_scale, r_scale, m=None, v=None, s=None):
     """The float32 moments that the codes stand for, into lists m and v (either may be None)."""
     numel = [t.numel() for t in m_code]
     n = len(numel)
-    _check_adamw8(n, numel, m_code, r_code, m_scale, r_scale)
-    for lst in (m, v):
-        if lst is None:
-            continue
-        if len(lst) != n or any(t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != k
-                                for t, k in zip(lst, numel)):
-            raise ValueError("m and v must be contiguous float32 tensors of the codes' sizes")
-    N = (C.c_int64 * max(1, n))(*numel)
-    call("xt_adamw8_decode", n, _ptrs(m_code), _ptrs(r_code), _ptrs(m_scale), _ptrs(r_scale),
-         _ptrs(m) if m is not None else None, _ptrs(v) if v is not None else None, N, stream(s))
+    out = [_table(lst, torch.float32, numel) if lst is not None else None for lst in (m, v)]
+    call("xt_adamw8_decode", n, *_adamw8_tables(numel, m_code, r_code, m_scale, r_scale), *out,
+         (C.c_int64 * max(1, n))(*numel), stream(s))
 
 
 def xt_quantize_fp8(x, out, dequant, ws=None, s=None):
