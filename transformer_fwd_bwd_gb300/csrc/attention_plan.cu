@@ -5,7 +5,8 @@
 // the offsets of up to kOffsets documents) finds its document, warps and shared memory reduce the
 // intervals of a 128-token tile to the tile's ranges.  The second writes the tiles' records in the
 // order of their work: a tile's place is the number of tiles with more work than it (or as much and a
-// lower number), counted by one warp per tile, so the order never depends on timing.
+// lower number), counted by one warp per tile, so the order never depends on timing.  Bound by two launches in
+// a row: 4.7 us for 8192 tokens, 2.4 us for 96 (a cluster barrier in the place of the second launch: 4.5 and 2.9).
 #include "attention_plan.cuh"
 #include "internal.cuh"
 
