@@ -7,7 +7,9 @@ library raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
+import operator
 import os
 
 import torch
@@ -771,39 +773,51 @@ def adamw8_workspace(numels, device="cuda"):
     return workspace(ws_bytes("xt_adamw8_workspace_size", len(numels), arr), device)
 
 
-def _table(tensors, dtype, numel, per=1):
-    """Device addresses of contiguous CUDA tensors of one dtype with ceil(numel / per) elements each."""
+# Lists of a hundred tensors are checked before every step: each property is read by one map over the list (with
+# numel and data_ptr unbound), about half the time of a loop of attribute calls.
+_numel, _data_ptr, _contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+_dtype, _is_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+
+
+def _addresses(addresses):
+    a = array.array("Q", addresses)
+    return (C.c_void_p * len(a)).from_buffer(a) if a else (C.c_void_p * 1)()
+
+
+def _table(tensors, dtype, numel, what="the parameters'"):
+    """Device addresses of contiguous CUDA tensors of one dtype and the given sizes."""
     if len(tensors) != len(numel):
         raise ValueError("the lists must have the same length")
-    out = [t.data_ptr() for t, k in zip(tensors, numel)
-           if t.dtype is dtype and t.is_cuda and t.numel() == (k + per - 1) // per and t.is_contiguous()]
-    if len(out) != len(numel):
-        raise ValueError(f"expected contiguous CUDA tensors of {dtype} with the parameters' sizes"
-                         + (f" in blocks of {per}" if per > 1 else ""))
-    return (C.c_void_p * max(1, len(out)))(*out)
+    if not (list(map(_numel, tensors)) == numel and all(map(_contiguous, tensors)) and all(map(_is_cuda, tensors))
+            and set(map(_dtype, tensors)) <= {dtype}):
+        raise ValueError(f"expected contiguous CUDA tensors of {dtype}, {what} sizes")
+    return _addresses(map(_data_ptr, tensors))
 
 
 def _adamw8_tables(numel, m_code, r_code, m_scale, r_scale):
+    scales = [(k + 255) // 256 for k in numel]
     return (_table(m_code, torch.int8, numel), _table(r_code, torch.uint8, numel),
-            _table(m_scale, torch.float32, numel, 256), _table(r_scale, torch.float32, numel, 256))
+            _table(m_scale, torch.float32, scales, "one scale per 256 elements of the parameters'"),
+            _table(r_scale, torch.float32, scales, "one scale per 256 elements of the parameters'"))
 
 
 def xt_adamw8_step(cfg, params, grads, m_code, r_code, m_scale, r_scale, shadows=None, norm_out=None, ws=None, s=None):
     """One AdamW step with the moments in 8 bits over lists of float32 tensors (see adamw8_state; params and
     the state are updated in place); shadows, norm_out as for xt_adamw_step."""
-    numel = [t.numel() for t in params]
+    numel = list(map(_numel, params))
     n = len(numel)
     tables = (_table(params, torch.float32, numel), _table(grads, torch.float32, numel),
               *_adamw8_tables(numel, m_code, r_code, m_scale, r_scale))
     sh, sdt = None, XT_F32
     if shadows is not None:
-        sdt = next((dt(t) for t in shadows if t is not None), XT_F32)
-        td = torch.bfloat16 if sdt == XT_BF16 else torch.float32
-        if len(shadows) != n or any(t is not None and (t.dtype is not td or not t.is_cuda or t.numel() != k
-                                                       or not t.is_contiguous()) for t, k in zip(shadows, numel)):
-            raise ValueError("shadows must be contiguous CUDA tensors of one dtype and the parameters' sizes, one "
-                             "entry for each")
-        sh = (C.c_void_p * max(1, n))(*[t.data_ptr() if t is not None else None for t in shadows])
+        if len(shadows) != n:
+            raise ValueError("the lists must have the same length")
+        some = [t for t in shadows if t is not None]
+        sdt = dt(some[0]) if some else XT_F32
+        sh = _table(some, some[0].dtype if some else None, [k for t, k in zip(shadows, numel) if t is not None])
+        if len(some) < n:
+            given = iter(sh)
+            sh = (C.c_void_p * n)(*[next(given) if t is not None else None for t in shadows])
     if ws is None and n and (cfg.max_grad_norm > 0 or norm_out is not None):
         ws = adamw8_workspace(numel, params[0].device)
     call("xt_adamw8_step", C.byref(cfg), n, *tables, sh, sdt, (C.c_int64 * max(1, n))(*numel), ptr(norm_out), ptr(ws),
@@ -812,7 +826,7 @@ def xt_adamw8_step(cfg, params, grads, m_code, r_code, m_scale, r_scale, shadows
 
 def xt_adamw8_decode(m_code, r_code, m_scale, r_scale, m=None, v=None, s=None):
     """The float32 moments that the codes stand for, into lists m and v (either may be None)."""
-    numel = [t.numel() for t in m_code]
+    numel = list(map(_numel, m_code))
     n = len(numel)
     out = [_table(lst, torch.float32, numel) if lst is not None else None for lst in (m, v)]
     call("xt_adamw8_decode", n, *_adamw8_tables(numel, m_code, r_code, m_scale, r_scale), *out,
