@@ -45,16 +45,20 @@ __global__ void __launch_bounds__(256) attnm_join_kernel(const __grid_constant__
   }
 }
 
-// [T, heads, hd] view of rows of ld elements, boxes of 128 tokens × 64 elements of one head, 128-byte swizzle.
-int token_map(CUtensorMap* tm, const void* base, int64_t ld, int64_t T, int heads, int hd) {
+// [planes, T, heads, hd] view of bf16 or (f32) float32 with rows of ld elements.  To be read: boxes of 128 tokens × 64
+// elements of one head, 128-byte swizzle; to be written (out): 32 tokens × 64 bytes, 64-byte swizzle.
+int token_map(CUtensorMap* tm, const void* base, int64_t ld, int64_t T, int heads, int hd, bool out = false,
+              bool f32 = false, int planes = 1) {
   auto enc = encode_fn();
   if (!enc) return fail(XT_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  cuuint64_t dims[4] = {cuuint64_t(hd), cuuint64_t(heads), cuuint64_t(T), 1};
-  cuuint64_t strides[3] = {cuuint64_t(hd * 2), cuuint64_t(ld * 2), cuuint64_t(T * ld * 2)};
-  cuuint32_t box[4] = {64, 1, BT, 1}, estr[4] = {1, 1, 1, 1};
-  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const int64_t e = f32 ? 4 : 2;
+  cuuint64_t dims[4] = {cuuint64_t(hd), cuuint64_t(heads), cuuint64_t(T), cuuint64_t(planes)};
+  cuuint64_t strides[3] = {cuuint64_t(hd * e), cuuint64_t(ld * e), cuuint64_t(T * ld * e)};
+  cuuint32_t box[4] = {out ? cuuint32_t(64 / e) : 64u, 1, out ? 32u : cuuint32_t(BT), 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(XT_ERR_CUDA, "masked attention: cuTensorMapEncodeTiled failed (%d)", int(r));
   return XT_OK;
 }
@@ -171,13 +175,14 @@ int xt_attention_masked_fwd(const xt_attention_desc* desc, const void* plan, siz
   p.o = static_cast<bf16*>(o);
   p.ldo = ld_o;
   p.lse = lse;
-  CUtensorMap tq, tk, tv;
-  XT_TRY(token_map(&tq, q, ld_q, desc->T, H, desc->hd));
-  XT_TRY(token_map(&tk, k, ld_k, desc->T, Hkv, desc->hd));
-  XT_TRY(token_map(&tv, v, ld_v, desc->T, Hkv, desc->hd));
+  CUtensorMap tm[4];
+  XT_TRY(token_map(&tm[0], q, ld_q, desc->T, H, desc->hd));
+  XT_TRY(token_map(&tm[1], k, ld_k, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tm[2], v, ld_v, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tm[3], o, ld_o, desc->T, H, desc->hd, true));
   const bool cap = desc->cap > 0.f, bias = desc->slopes != nullptr;
-  return desc->hd == 64 ? launch_fwd<64>(cap, bias, tq, tk, tv, p, as_stream(stream))
-                        : launch_fwd<128>(cap, bias, tq, tk, tv, p, as_stream(stream));
+  return desc->hd == 64 ? launch_fwd<64>(cap, bias, tm, p, as_stream(stream))
+                        : launch_fwd<128>(cap, bias, tm, p, as_stream(stream));
 }
 
 int xt_attention_masked_bwd_workspace_size(const xt_attention_desc* desc, size_t* bytes) {
@@ -224,11 +229,12 @@ int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, siz
   p.lddq = ld_dq;
   p.lddk = ld_dk;
   p.lddv = ld_dv;
-  CUtensorMap tq, tk, tv, tdo;
-  XT_TRY(token_map(&tq, q, ld_q, desc->T, H, desc->hd));
-  XT_TRY(token_map(&tk, k, ld_k, desc->T, Hkv, desc->hd));
-  XT_TRY(token_map(&tv, v, ld_v, desc->T, Hkv, desc->hd));
-  XT_TRY(token_map(&tdo, d_o, ld_do, desc->T, H, desc->hd));
+  CUtensorMap tm[4], tdq, tdk, tdv;
+  XT_TRY(token_map(&tm[0], q, ld_q, desc->T, H, desc->hd));
+  XT_TRY(token_map(&tm[1], k, ld_k, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tm[2], v, ld_v, desc->T, Hkv, desc->hd));
+  XT_TRY(token_map(&tm[3], d_o, ld_do, desc->T, H, desc->hd));
+  XT_TRY(token_map(&tdq, dq, ld_dq, desc->T, H, desc->hd, true));
   const bool cap = desc->cap > 0.f, bias = desc->slopes != nullptr;
   cudaStream_t s = as_stream(stream);
   p.split = key_split(desc);
@@ -236,13 +242,19 @@ int xt_attention_masked_bwd(const xt_attention_desc* desc, const void* plan, siz
   if (p.split > 1) {
     p.part_k = reinterpret_cast<float*>(static_cast<char*>(ws) + d_bytes(desc));
     p.part_v = reinterpret_cast<float*>(reinterpret_cast<char*>(p.part_k) + part_bytes(desc, p.split));
+    const int64_t ld = int64_t(Hkv) * desc->hd;
+    XT_TRY(token_map(&tdk, p.part_k, ld, desc->T, Hkv, desc->hd, true, true, p.split));
+    XT_TRY(token_map(&tdv, p.part_v, ld, desc->T, Hkv, desc->hd, true, true, p.split));
+  } else {
+    XT_TRY(token_map(&tdk, dk, ld_dk, desc->T, Hkv, desc->hd, true));
+    XT_TRY(token_map(&tdv, dv, ld_dv, desc->T, Hkv, desc->hd, true));
   }
   if (desc->hd == 64) {
-    XT_TRY((launch_bwd<64, false>(cap, bias, tq, tk, tv, tdo, p, s)));
-    XT_TRY((launch_bwd<64, true>(cap, bias, tq, tk, tv, tdo, p, s)));
+    XT_TRY((launch_bwd<64, false>(cap, bias, tm, tdq, tdq, p, s)));
+    XT_TRY((launch_bwd<64, true>(cap, bias, tm, tdk, tdv, p, s)));
   } else {
-    XT_TRY((launch_bwd<128, false>(cap, bias, tq, tk, tv, tdo, p, s)));
-    XT_TRY((launch_bwd<128, true>(cap, bias, tq, tk, tv, tdo, p, s)));
+    XT_TRY((launch_bwd<128, false>(cap, bias, tm, tdq, tdq, p, s)));
+    XT_TRY((launch_bwd<128, true>(cap, bias, tm, tdk, tdv, p, s)));
   }
   if (p.split == 1) return XT_OK;
   const int width = Hkv * desc->hd;

@@ -257,28 +257,42 @@ __device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
   }
 }
 
-// 64 bytes of each of the warp's 32 rows, held by the row's lane, to rows of `ld` bytes from `base` on (the first
-// `rows` of them), through the warp's 2 KB of shared memory: a store of every lane's own row would touch 32 rows at a
-// time (the epilogue of 128 keys and 64 columns: 2650 cycles, 3800 so).
-__device__ __forceinline__ void store_rows(uint4* stage, const uint32_t (&w)[16], void* base, int64_t ld, int rows) {
+// What a row warp hands to the TMA: 64 bytes of each of its 32 rows at a time, through two buffers of 2 KB with the
+// 64-byte swizzle.  The copies run while the warp goes on (a lane that stores its own row touches 32 rows at a time:
+// the epilogue of 128 keys and 64 columns took 3800 cycles so, 2650 with four lanes to a row, 1980 like this); rows
+// behind the last token are clipped.
+constexpr int STAGE = 8 * 2 * 2048;  // of the eight row warps
+// w: 64 bytes of this lane's row; to columns c0 on of a head's, rows row0 on, through buffer `buf`.  ALONE: an item
+// has one such piece, and all go through the same buffer.  `stage`: the eight warps' buffers.
+template <bool ALONE>
+__device__ __forceinline__ void put_rows(uint8_t* stage, int buf, const CUtensorMap* tm, const uint32_t (&w)[16], int c0,
+                                         int head, int row0, int plane, int64_t T) {
   const int lane = threadIdx.x & 31;
+  uint4* to = reinterpret_cast<uint4*>(stage + ((threadIdx.x >> 5) - 4) * 4096 + buf * 2048);
+  if (lane == 0) {  // the last copy from this buffer has left it
+    if (ALONE) bulk_wait_read_0();
+    else bulk_wait_read_1();
+  }
   __syncwarp();
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    stage[lane * 4 + (u ^ (lane >> 1 & 3))] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    to[lane * 4 + (u ^ (lane >> 1 & 3))] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  fence_proxy_async_smem();
   __syncwarp();
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int r = u * 8 + (lane >> 2), c = lane & 3;
-    const uint4 x = stage[r * 4 + (c ^ (r >> 1 & 3))];
-    if (r < rows) *reinterpret_cast<uint4*>(static_cast<char*>(base) + r * ld + c * 16) = x;
+  if (lane == 0) {
+    if (row0 < T) tma_store_4d(tm, smem_u32(to), c0, head, row0, plane);
+    bulk_commit();
   }
 }
-constexpr int STAGE = 8 * 2048;  // of the eight row warps
+// Every copy of the warp has arrived: before a row is written again, and before the block ends.
+__device__ __forceinline__ void rows_stored() {
+  if ((threadIdx.x & 31) == 0) bulk_wait_all();
+  __syncwarp();
+}
 
 // Products of 16 rows of a and b (of lda, ldb elements, from `row` on; row T − 1 in the place of later ones), HD / 8
 // lanes to a row: the sums go to out[0 .. 15].  A thread that walks its own row takes 2700 cycles for 64 columns and 9500
-// for 128, these 1650 and 3400.
+// for 128, these 1850 and 3300.
 template <int HD>
 __device__ __forceinline__ void dots16(const bf16* a, int64_t lda, const bf16* b, int64_t ldb, int64_t row, int64_t T,
                                        float* out) {
@@ -605,7 +619,7 @@ __device__ __forceinline__ void queue_init(Queue* q, int readers) {
 // without masks, 12 heads, 259 us, 795 TFLOP/s, 0.42 of measured; at hd 128 as much time goes into the products: 417 us,
 // 989 TFLOP/s, 0.52.  8192 causal tokens 128 us, where the kernel without masks takes 161.
 constexpr int kThreadsFwd = 384;
-constexpr uint32_t kFwdRegsCtl = 72, kFwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
+constexpr uint32_t kFwdRegsCtl = 88, kFwdRegsRows = 208;  // 128·88 + 256·208 = 384·168
 
 template <int HD>
 struct FwdCfg {
@@ -618,7 +632,7 @@ struct FwdCfg {
   static constexpr int V = K + RING * QT;
   static constexpr int ST = V + RING * QT;          // the row warps' output
   static constexpr int BARS = ST + STAGE;
-  static constexpr int BYTES = 1024 + BARS + 1024;
+  static constexpr int BYTES = BARS + 1024;
 };
 
 template <int HD>
@@ -635,11 +649,11 @@ struct FwdBars {
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreadsFwd, 1)
     attnm_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                     const __grid_constant__ Params p) {
   using C = FwdCfg<HD>;
   constexpr uint32_t TCOLS = 512, RING = C::RING;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   FwdBars<HD>& B = *reinterpret_cast<FwdBars<HD>*>(smem + C::BARS);
   static_assert(sizeof(FwdBars<HD>) <= 1024, "barrier space");
@@ -983,9 +997,6 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
       const float inv = seen ? 1.f / l : 0.f;
       const bool real = row < p.plan.T;
       tc_fence_after();
-      const int row0 = row - lane, rows_in = int(min(int64_t(32), p.plan.T - row0));
-      bf16* orow = p.o + int64_t(row0) * p.ldo + int64_t(h) * HD;
-      uint4* stage = reinterpret_cast<uint4*>(smem + C::ST) + (warp - 4) * 128;
       float bad = 0.f;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
@@ -1003,15 +1014,18 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-        store_rows(stage, w, orow + c * 32, p.ldo * 2, rows_in);
+        put_rows<false>(smem + C::ST, c & 1, &tmO, w, c * 32, h, row - lane, 0, p.plan.T);
       }
       tc_fence_before();
       if (real) p.lse[int64_t(h) * p.plan.T + row] = seen ? (m * unit + log2f(l)) * kLn2 : -INFINITY;
       const uint32_t rows = __ballot_sync(0xffffffffu, bad != 0.f && l == l && real);
-      if (rows)
+      if (rows) {
+        rows_stored();
         repair<HD, false, true, CAP, BIAS>(p, h, 1, h / p.group, row, iv, rows, rg.x * BT, rg.y * BT, m * unit, 0.f,
                                            inv, 0, 1, 0);
+      }
     }
+    rows_stored();
   }
   __syncthreads();
   if (warp == 1) {
@@ -1047,7 +1061,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1339 us, 770 and 1231 TFLOP/s,
 // 0.65 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and for the start of an item.
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
-constexpr uint32_t kBwdRegsCtl = 72, kBwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
+constexpr uint32_t kBwdRegsCtl = 88, kBwdRegsRows = 208;  // 128·88 + 256·208 = 384·168
 constexpr int PW = BT / 2;        // columns of a row warp
 
 template <int HD, bool KEY>
@@ -1062,7 +1076,8 @@ struct BwdCfg {
   static constexpr int VEC = R + RING * 2 * QT;          // (KEY) ring of −lse·log₂e and −D, 128 floats each; or sums of halves
   static constexpr int ST = VEC + RING * 1024;           // the row warps' output
   static constexpr int BARS = ST + STAGE;
-  static constexpr int BYTES = 1024 + BARS + 512;
+  static constexpr int BYTES = BARS + 512;
+  static_assert(BYTES <= 227 * 1024, "shared memory");
   static_assert(ACC2 + CH * HD <= 512, "TMEM columns");
 };
 
@@ -1081,12 +1096,12 @@ template <int HD, bool KEY, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreadsBwd, 1)
     attnm_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                     const __grid_constant__ CUtensorMap tmG1, const __grid_constant__ CUtensorMap tmG2,
                      const __grid_constant__ Params p) {
   using C = BwdCfg<HD, KEY>;
   constexpr uint32_t TCOLS = 512, RING = C::RING;
   constexpr int CH = C::CH;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   BwdBars<HD, KEY>& B = *reinterpret_cast<BwdBars<HD, KEY>*>(smem + C::BARS);
   static_assert(sizeof(BwdBars<HD, KEY>) <= 512, "barrier space");
@@ -1464,9 +1479,6 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         break;
       }
       // ---- epilogue: this half's HD/2 columns of the accumulators
-      const int64_t row0 = row - lane;
-      const int rows_in = int(min(int64_t(32), T - row0));
-      uint4* stage = reinterpret_cast<uint4*>(smem + C::ST) + (warp - 4) * 128;
       tc_fence_after();
       float bad = 0.f;
       auto load_acc = [&](uint32_t at, uint32_t(&o)[32]) {  // 32 columns of both chains' accumulators
@@ -1483,12 +1495,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       };
 #pragma unroll
       for (int w = 0; w < (KEY ? 2 : 1); ++w) {
-        const int64_t col = int64_t(h) * HD + half * (HD / 2);
-        bf16* out = (w ? p.dv + row0 * p.lddv : KEY ? p.dk + row0 * p.lddk : p.dq + row0 * p.lddq) + col;
-        const int64_t ld = 2 * (w ? p.lddv : KEY ? p.lddk : p.lddq);
-        float* raw = KEY && p.split > 1
-                         ? (w ? p.part_v : p.part_k) + (int64_t(sp) * T + row0) * (int64_t(p.Hkv) * HD) + col
-                         : nullptr;
+        const CUtensorMap* tm = w ? &tmG2 : &tmG1;
+        const bool raw = KEY && p.split > 1;  // the part's float32 sums
         const float mul = w || raw ? 1.f : p.scale;
         const uint32_t acc = tbase + (w ? C::ACC2 : C::ACC1) + lane_off + uint32_t(half * (HD / 2));
 #pragma unroll
@@ -1509,17 +1517,18 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
             o[e] = __float_as_uint(x);
           }
           uint32_t x[16];
+          const int col = half * (HD / 2) + c;
           if (raw) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = o[16 * u + e];
-              store_rows(stage, x, raw + c + 16 * u, int64_t(p.Hkv) * HD * 4, rows_in);
+              put_rows<false>(smem + C::ST, u, tm, x, col + 16 * u, h, row - lane, sp, T);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            store_rows(stage, x, out + c, ld, rows_in);
+            put_rows<!KEY && HD == 64>(smem + C::ST, (w * (HD / 64) + c / 32) & 1, tm, x, col, h, row - lane, 0, T);
           }
         }
       }
@@ -1527,10 +1536,13 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       __syncwarp();
       if (n > 0 && lane == 0) mbar_arrive(smem_u32(&B.acc_free));
       const uint32_t rows = __ballot_sync(0xffffffffu, bad != 0.f && real);
-      if (rows)
+      if (rows) {
+        rows_stored();
         repair<HD, KEY, false, CAP, BIAS>(p, KEY ? h0 : h, heads, KEY ? h : h / p.group, row, iv, rows, rg.x * BT,
                                           rg.y * BT, -nlse, Tr - nD, 0.f, half, 2, sp);
+      }
     }
+    rows_stored();
   }
   __syncthreads();
   if (warp == 1) {
@@ -1547,47 +1559,43 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
 int prepare_kernel(std::atomic<uint64_t>& ready, const void* kernel, int smem, int regs);
 
 template <int HD>
-int launch_fwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-               const Params& p, cudaStream_t s);
+int launch_fwd(bool cap, bool bias, const CUtensorMap (&tm)[4], const Params& p, cudaStream_t s);
 template <int HD, bool KEY>
-int launch_bwd(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-               const CUtensorMap& tdo, const Params& p, cudaStream_t s);
+int launch_bwd(bool cap, bool bias, const CUtensorMap (&tm)[4], const CUtensorMap& g1, const CUtensorMap& g2,
+               const Params& p, cudaStream_t s);
 
 #define XT_ATTNM_FWD(HD)                                                                                         \
   template <bool CAP, bool BIAS>                                                                                 \
-  static int fwd_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p,       \
-                     cudaStream_t s) {                                                                           \
-    auto k = attnm_fwd_kernel<HD, CAP, BIAS>;                                                                    \
+  static int fwd_one(const CUtensorMap (&tm)[4], const Params& p, cudaStream_t s) {                              \
     static std::atomic<uint64_t> ready{0};                                                                       \
+    auto k = attnm_fwd_kernel<HD, CAP, BIAS>;                                                                    \
     XT_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(k), FwdCfg<HD>::BYTES, 168));                     \
     const int64_t items = int64_t((p.plan.tiles + 1) / 2) * p.H;                                                 \
-    launch(k, unsigned(items), kThreadsFwd, FwdCfg<HD>::BYTES, s, tq, tk, tv, p);                                \
+    launch(k, unsigned(items), kThreadsFwd, FwdCfg<HD>::BYTES, s, tm[0], tm[1], tm[2], tm[3], p);                \
     return check_launch("xt_attention_masked_fwd");                                                              \
   }                                                                                                              \
   template <>                                                                                                    \
-  int launch_fwd<HD>(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,   \
-                     const Params& p, cudaStream_t s) {                                                          \
-    if (cap) return bias ? fwd_one<true, true>(tq, tk, tv, p, s) : fwd_one<true, false>(tq, tk, tv, p, s);       \
-    return bias ? fwd_one<false, true>(tq, tk, tv, p, s) : fwd_one<false, false>(tq, tk, tv, p, s);              \
+  int launch_fwd<HD>(bool cap, bool bias, const CUtensorMap (&tm)[4], const Params& p, cudaStream_t s) {         \
+    if (cap) return bias ? fwd_one<true, true>(tm, p, s) : fwd_one<true, false>(tm, p, s);                       \
+    return bias ? fwd_one<false, true>(tm, p, s) : fwd_one<false, false>(tm, p, s);                              \
   }
 
 #define XT_ATTNM_BWD(HD, KEY)                                                                                    \
   template <bool CAP, bool BIAS>                                                                                 \
-  static int bwd_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo, \
-                     const Params& p, cudaStream_t s) {                                                          \
-    auto k = attnm_bwd_kernel<HD, KEY, CAP, BIAS>;                                                               \
+  static int bwd_one(const CUtensorMap (&tm)[4], const CUtensorMap& g1, const CUtensorMap& g2, const Params& p,  \
+                     cudaStream_t s) {                                                                           \
     static std::atomic<uint64_t> ready{0};                                                                       \
+    auto k = attnm_bwd_kernel<HD, KEY, CAP, BIAS>;                                                               \
     XT_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(k), BwdCfg<HD, KEY>::BYTES, 168));                \
     const int64_t items = int64_t(p.plan.tiles) * (KEY ? p.Hkv * p.split : p.H);                                 \
-    launch(k, unsigned(items), kThreadsBwd, BwdCfg<HD, KEY>::BYTES, s, tq, tk, tv, tdo, p);                      \
+    launch(k, unsigned(items), kThreadsBwd, BwdCfg<HD, KEY>::BYTES, s, tm[0], tm[1], tm[2], tm[3], g1, g2, p);   \
     return check_launch("xt_attention_masked_bwd");                                                              \
   }                                                                                                              \
   template <>                                                                                                    \
-  int launch_bwd<HD, KEY>(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk,                     \
-                          const CUtensorMap& tv, const CUtensorMap& tdo, const Params& p, cudaStream_t s) {      \
-    if (cap)                                                                                                     \
-      return bias ? bwd_one<true, true>(tq, tk, tv, tdo, p, s) : bwd_one<true, false>(tq, tk, tv, tdo, p, s);    \
-    return bias ? bwd_one<false, true>(tq, tk, tv, tdo, p, s) : bwd_one<false, false>(tq, tk, tv, tdo, p, s);    \
+  int launch_bwd<HD, KEY>(bool cap, bool bias, const CUtensorMap (&tm)[4], const CUtensorMap& g1,                \
+                          const CUtensorMap& g2, const Params& p, cudaStream_t s) {                              \
+    if (cap) return bias ? bwd_one<true, true>(tm, g1, g2, p, s) : bwd_one<true, false>(tm, g1, g2, p, s);       \
+    return bias ? bwd_one<false, true>(tm, g1, g2, p, s) : bwd_one<false, false>(tm, g1, g2, p, s);              \
   }
 
 }  // namespace attnm
