@@ -221,8 +221,8 @@ __device__ __forceinline__ void add_bias(uint32_t (&r)[N], float unit, float slo
 // Lawson's method; error 9e-8), and two through exponentials and the reciprocal of the product of their
 // denominators, 1/a = b·1/(ab) (at most 8.4² there).  A NaN, which may stand in a masked column, must not reach the
 // column it would share a reciprocal with: it counts as beyond the cap.
-// 8192 causal tokens, 12 heads of 64, forward: 264 us so shared, 273 with the special-function unit alone, 275 with the
-// polynomial alone (128 us without a cap).
+// 8192 causal tokens, 12 heads of 64, forward: 233 us (128 without a cap); the special-function unit alone takes 3 %
+// more than this mixture, the polynomial alone 4 %.
 template <int N>
 __device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -616,10 +616,10 @@ __device__ __forceinline__ void queue_init(Queue* q, int readers) {
 // in turn (P V and S of stream 0, then of stream 1), which sets the streams half a period apart — one is
 // at its exponentials while the other's products run.
 // What bounds it: the rows (exponentials, their sums and conversions, tensor-memory loads) at hd 64: 8192 tokens
-// without masks, 12 heads, 259 us, 795 TFLOP/s, 0.42 of measured; at hd 128 as much time goes into the products: 417 us,
-// 989 TFLOP/s, 0.52.  8192 causal tokens 128 us, where the kernel without masks takes 161.
+// without masks, 12 heads, 263 us, 784 TFLOP/s, 0.41 of measured; at hd 128 as much time goes into the products: 392 us,
+// 1051 TFLOP/s, 0.55.  8192 causal tokens 128 us, where the kernel without masks takes 161.
 constexpr int kThreadsFwd = 384;
-constexpr uint32_t kFwdRegsCtl = 88, kFwdRegsRows = 208;  // 128·88 + 256·208 = 384·168
+constexpr uint32_t kFwdRegsCtl = 72, kFwdRegsRows = 216;  // 128·88 + 256·208 = 384·168
 
 template <int HD>
 struct FwdCfg {
@@ -998,13 +998,13 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
       const bool real = row < p.plan.T;
       tc_fence_after();
       float bad = 0.f;
-#pragma unroll
+      // Not unrolled, and O is read even where no tile was met (`seen` leaves it out): with both the other way the scores'
+      // loop has fewer registers (capped long text 689 us against 727).
+#pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
-        if (rg.y > rg.x) {
-          tmem_ld32(tO + uint32_t(c * 32), o);
-          tmem_ld_wait();
-        }
+        tmem_ld32(tO + uint32_t(c * 32), o);
+        tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float x = seen ? __uint_as_float(o[e]) * inv : 0.f;
@@ -1057,9 +1057,10 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // memory for one set of accumulators: there the halves' rows share one chain of 128 columns.
 //
 // What bounds it: the rows' chain at hd 64 (issue slots and tensor-memory latency: 8192 tokens without masks, 12 heads,
-// both passes: 929 us, 555 TFLOP/s of the formulas' five products and 888 of the eight that run, 0.47 of measured; one
-// chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1339 us, 770 and 1231 TFLOP/s,
-// 0.65 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and for the start of an item.
+// both passes: 880 us, 586 TFLOP/s of the formulas' five products and 938 of the eight that run, 0.49 of measured; one
+// chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1300 us, 792 and 1267 TFLOP/s,
+// 0.67 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and some 4000 cycles per item
+// for D₀, the last products' arrival and the epilogue, where a tile takes 2100 (hd 64) to 2900 (hd 128).
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
 constexpr uint32_t kBwdRegsCtl = 88, kBwdRegsRows = 208;  // 128·88 + 256·208 = 384·168
 constexpr int PW = BT / 2;        // columns of a row warp
@@ -1493,22 +1494,24 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
           tmem_ld_wait();
         }
       };
-#pragma unroll
+      // Not unrolled, and the accumulators are read even where no tile was met (the select leaves them out): with both the
+      // other way the tiles' loop has fewer registers (capped texts, heads of 128: backward 70 us against 78).
+#pragma unroll 1
       for (int w = 0; w < (KEY ? 2 : 1); ++w) {
         const CUtensorMap* tm = w ? &tmG2 : &tmG1;
         const bool raw = KEY && p.split > 1;  // the part's float32 sums
         const float mul = w || raw ? 1.f : p.scale;
         const uint32_t acc = tbase + (w ? C::ACC2 : C::ACC1) + lane_off + uint32_t(half * (HD / 2));
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < HD / 2; c += 32) {
           uint32_t o[32];
-          if (n > 0) load_acc(acc + uint32_t(c), o);
+          load_acc(acc + uint32_t(c), o);
           if constexpr (!KEY) {
             uint32_t wk[32];
-            if (n > 0) load_acc(tbase + C::ACC2 + lane_off + uint32_t(half * (HD / 2) + c), wk);
+            load_acc(tbase + C::ACC2 + lane_off + uint32_t(half * (HD / 2) + c), wk);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (n > 0) o[e] = __float_as_uint(fmaf(-Tr, __uint_as_float(wk[e]), __uint_as_float(o[e])));
+              o[e] = __float_as_uint(fmaf(-Tr, __uint_as_float(wk[e]), __uint_as_float(o[e])));
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
