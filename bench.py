@@ -62,7 +62,7 @@ def parse_args(argv=None):
     ap.add_argument("--recompute", action="store_true",
                     help="activation recompute: keep each layer's input only, redo its forward in the backward")
     ap.add_argument("--kernel", choices=["attention", "gemm", "layernorm", "gelu", "cross_entropy", "adamw", "fp8gemm",
-                                         "ce_fanout"],
+                                         "ce_fanout", "attention_masked", "rope_axes", "adamw8"],
                     default=None,
                     help="time one kernel family at the workload's sizes instead of the step (for profiling)")
     ap.add_argument("--sweep", action="store_true",
@@ -635,6 +635,40 @@ def run_kernel(args):
         print(json.dumps({"kernel": "attention", "workload": f"B{B} S{S} H{H}x{hd} causal bf16",
                           "fwd_us": fwd_us, "bwd_us": bwd_us,
                           "fwd_tflops": fl / fwd_us / 1e6, "bwd_tflops": 2 * fl / bwd_us / 1e6, "clocks": clocks}))
+    elif args.kernel == "attention_masked":
+        # the stack's batch as texts of uneven lengths packed end to end, causal
+        cfg = synth.BLOCK_CONFIGS[args.workload]
+        H, hd, T = cfg["H"], cfg["hd"], cfg["B"] * cfg["S"]
+        cuts = torch.randperm(T - 1, generator=g)[:3 * cfg["B"] - 1].add(1).sort().values.tolist()
+        off = torch.tensor([0] + cuts + [T], dtype=torch.int32, device=dev)
+        qkv = torch.randn(T, 3 * H * hd, generator=g).to(torch.bfloat16).to(dev)
+        dO = torch.randn(T, H * hd, generator=g).to(torch.bfloat16).to(dev)
+        o, dqkv = torch.empty_like(dO), torch.empty_like(qkv)
+        lse = torch.empty(H, T, dtype=torch.float32, device=dev)
+        plan, ws = xt.attention_plan_buffer(T, dev), xt.attention_masked_workspace(T, H, H, hd, dev)
+        q, k, v = qkv.split(H * hd, 1)
+        dq, dk, dv = dqkv.split(H * hd, 1)
+        plan_us = timed(lambda: xt.xt_attention_plan(plan, T, off.numel() - 1, off))
+        fwd_us = timed(lambda: xt.xt_attention_masked_fwd(q, k, v, o, lse, plan, H, H, hd))
+        bwd_us = timed(lambda: xt.xt_attention_masked_bwd(q, k, v, o, dO, lse, dq, dk, dv, plan, H, H, hd, ws=ws))
+        n = off.diff().double()
+        fl = 4 * hd * H * float((n * (n + 1) / 2).sum())   # QKᵀ and PV over what is seen; the backward 5 products
+        print(json.dumps({"kernel": "attention_masked", "workload": f"{off.numel() - 1} texts in {T} tokens, H{H}x{hd} bf16",
+                          "plan_us": plan_us, "fwd_us": fwd_us, "bwd_us": bwd_us, "fwd_tflops": fl / fwd_us / 1e6,
+                          "bwd_tflops": 2.5 * fl / bwd_us / 1e6, "clocks": clocks}))
+    elif args.kernel == "rope_axes":
+        # queries and keys of the stack's batch, three axes
+        cfg = synth.BLOCK_CONFIGS[args.workload]
+        H, hd, T = 2 * cfg["H"], cfg["hd"], cfg["B"] * cfg["S"]
+        x = torch.randn(T, H * hd, generator=g).to(torch.bfloat16).to(dev)
+        y = torch.empty_like(x)
+        pos = torch.randint(0, 4000, (3, T), generator=g, dtype=torch.int32).to(dev)
+        sec = [hd // 2 - 2 * (hd // 6), hd // 6, hd // 6]
+        fwd_us = timed(lambda: xt.xt_rope_axes_fwd(x, y, pos, sec, H, hd))
+        bwd_us = timed(lambda: xt.xt_rope_axes_bwd(x, y, pos, sec, H, hd))
+        nbytes = 2 * x.numel() * 2 + pos.numel() * 4
+        print(json.dumps({"kernel": "rope_axes", "rows": T, "heads": H, "hd": hd, "fwd_us": fwd_us, "bwd_us": bwd_us,
+                          "fwd_gbs": nbytes / fwd_us / 1e3, "bwd_gbs": nbytes / bwd_us / 1e3, "clocks": clocks}))
     elif args.kernel == "layernorm":
         # as the stack launches it: bf16 rows, float32 residual gradient accumulated, float32 dγ / dβ
         cfg = synth.BLOCK_CONFIGS[args.workload]
@@ -665,7 +699,7 @@ def run_kernel(args):
         bwd_us = timed(lambda: xt.xt_gelu_bwd(d, a, dx))
         print(json.dumps({"kernel": "gelu", "n": n, "fwd_us": fwd_us, "bwd_us": bwd_us,
                           "fwd_gbs": 4 * n / fwd_us / 1e3, "bwd_gbs": 6 * n / bwd_us / 1e3, "clocks": clocks}))
-    elif args.kernel == "adamw":
+    elif args.kernel in ("adamw", "adamw8"):
         # the optimizer step over the stack's parameter tensors (float32 masters, bf16 copies)
         cfg = synth.BLOCK_CONFIGS[args.workload]
         d, F, V, S, L = cfg["d"], cfg["F"], cfg["V"], cfg["S"], cfg["n_layers"]
@@ -680,13 +714,19 @@ def run_kernel(args):
         Vv = [torch.zeros_like(x) for x in P]
         SH = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in P]
         nrm = torch.zeros(1, dtype=torch.float32, device=dev)
-        ows = xt.adamw_workspace([x.numel() for x in P], dev)
+        numel = [x.numel() for x in P]
+        ows = (xt.adamw_workspace if args.kernel == "adamw" else xt.adamw8_workspace)(numel, dev)
         acfg = xt.adamw_config(1e-4, weight_decay=0.1, max_grad_norm=1.0, grad_scale=0.5, step=1)
-        us = timed(lambda: xt.xt_adamw_step(acfg, P, G, M, Vv, shadows=SH, norm_out=nrm, ws=ows))
-        n = sum(x.numel() for x in P)
-        nbytes = n * (4 + 16 + 12 + 2)   # norm pass reads g; update reads θ, g, m, v, writes θ, m, v, bf16 θ
+        n = sum(numel)
+        if args.kernel == "adamw":
+            us = timed(lambda: xt.xt_adamw_step(acfg, P, G, M, Vv, shadows=SH, norm_out=nrm, ws=ows))
+            nbytes = n * (4 + 16 + 12 + 2)   # norm pass reads g; update reads θ, g, m, v, writes θ, m, v, bf16 θ
+        else:
+            st = xt.adamw8_state(P)
+            us = timed(lambda: xt.xt_adamw8_step(acfg, P, G, *st, shadows=SH, norm_out=nrm, ws=ows))
+            nbytes = n * (4 + 10 + 6 + 2)    # the same with one byte for each of m and v
         peak = measured_peaks()[0].get("hbm_gbs", 6780.0)
-        print(json.dumps({"kernel": "adamw", "tensors": len(P), "params": n, "us": us,
+        print(json.dumps({"kernel": args.kernel, "tensors": len(P), "params": n, "us": us,
                           "gbs": nbytes / us / 1e3, "frac_of_measured_hbm": nbytes / us / 1e3 / peak,
                           "clocks": clocks}))
     elif args.kernel == "fp8gemm":
