@@ -20,9 +20,9 @@
 //
 // Memory-bound: 18 bytes per element (weight 8, gradient 4, codes 4, bf16 working copy 2) and 4 more
 // for the norm's pass.  A warp takes one block of 256 at a time: its lanes hold the block's values in
-// registers between the two maxima and the coding.  104.7 M weights with a bf16 working copy: update 358 us
-// (5.27 TB/s, 0.78 of the measured copy rate), with the norm's pass 462 us; decoding both moments 175 us
-// (1.05 GB, 5.99 TB/s).
+// registers between the two maxima and the coding.  104.7 M weights in 74 tensors with a bf16 working copy: update 353 us
+// (5.34 TB/s, 0.79 of the measured copy rate), with the norm's pass 492 us; decoding both moments 166 us
+// (1.05 GB, 6.31 TB/s, 0.93).  In the update a block's loads wait on one another's arithmetic (45 % of the issue slots).
 #include <cmath>
 
 #include "internal.cuh"
@@ -51,14 +51,13 @@ struct Table {
   int count;
 };
 
-__device__ __forceinline__ int tensor_of(const Table& tb, int t) {
-  int lo = 0, hi = tb.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tb.tile0[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+// The tensor of tile t, from that of an earlier tile.  A block's tiles only go forward, so this is one comparison for
+// most of them; a search from scratch put six dependent loads ahead of every tile's (74 tensors, 104.7 M weights:
+// step with norm 522 us so, 494 now).
+template <typename TB>
+__device__ __forceinline__ int tensor_of(const TB& tb, int t, int k) {
+  while (tb.tile0[k + 1] <= t) ++k;
+  return k;
 }
 
 __device__ __forceinline__ double warp_sum_f64(double v) {
@@ -85,11 +84,20 @@ __global__ void __launch_bounds__(kNormThreads, 3) sq8_kernel(const __grid_const
   const int tiles = tb.tile0[tb.count];
   double acc = 0.0;
   float hi = 0.f, lo = 0.f;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int k = tensor_of(tb, t);
-    const int64_t base = int64_t(t - tb.tile0[k]) * kNormTile;
-    const int64_t len = tb.n[k] - base < kNormTile ? tb.n[k] - base : kNormTile;
-    const float* g = tb.g[k] + base;
+  int first = 0, end = 0;  // tiles of the tensor at hand; its entry is read when it changes
+  int64_t n = 0;
+  const float* g0 = nullptr;
+  for (int t = blockIdx.x, k = 0; t < tiles; t += gridDim.x) {
+    if (t >= end) {
+      k = tensor_of(tb, t, k);
+      first = tb.tile0[k];
+      end = tb.tile0[k + 1];
+      n = tb.n[k];
+      g0 = tb.g[k];
+    }
+    const int64_t base = int64_t(t - first) * kNormTile;
+    const int64_t len = n - base < kNormTile ? n - base : kNormTile;
+    const float* g = g0 + base;
     float x[16];
     if (len == kNormTile && (reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
 #pragma unroll
@@ -312,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_consta
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = tb.tile0[tb.count];
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int k = tensor_of(tb, t);
+  for (int t = blockIdx.x, k = 0; t < tiles; t += gridDim.x) {
+    k = tensor_of(tb, t, k);
     const int64_t tile = int64_t(t - tb.tile0[k]) * kTile;
     float* p = tb.p[k];
     const float* g = tb.g[k];
@@ -353,13 +361,8 @@ struct DecodeTable {
 __global__ void __launch_bounds__(kThreads) decode8_kernel(const __grid_constant__ DecodeTable tb) {
   pdl_begin();
   const int tiles = tb.tile0[tb.count];
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    int k = 0, hi = tb.count - 1;
-    while (k < hi) {
-      const int mid = (k + hi + 1) >> 1;
-      if (tb.tile0[mid] <= t) k = mid;
-      else hi = mid - 1;
-    }
+  for (int t = blockIdx.x, k = 0; t < tiles; t += gridDim.x) {
+    k = tensor_of(tb, t, k);
     const int64_t base = int64_t(t - tb.tile0[k]) * kTile;
     const int8_t* m = tb.m[k] + base;
     const uint8_t* r = tb.r[k] + base;
@@ -568,7 +571,9 @@ int xt_adamw8_decode(int n, const int8_t* const* m_code, const uint8_t* const* r
       tb.vo[j] = v ? v[i] : nullptr;
     }
     if (tiles == 0) continue;
-    const int cap = num_sms() * 8;
+    // 104.7 M weights: 167 us with 64 blocks per SM (several waves even out what each of them waits for memory), 182
+    // with eight
+    const int cap = num_sms() * 64;
     launch(decode8_kernel, tiles < cap ? tiles : cap, kThreads, 0, s, tb);
     XT_TRY(check_launch("xt_adamw8_decode"));
   }
