@@ -21,8 +21,8 @@
 // Memory-bound: 18 bytes per element (weight 8, gradient 4, codes 4, bf16 working copy 2) and 4 more
 // for the norm's pass.  A warp takes one block of 256 at a time: its lanes hold the block's values in
 // registers between the two maxima and the coding.  104.7 M weights in 74 tensors with a bf16 working copy: update 353 us
-// (5.34 TB/s, 0.79 of the measured copy rate), with the norm's pass 492 us; decoding both moments 166 us
-// (1.05 GB, 6.31 TB/s, 0.93).  In the update a block's loads wait on one another's arithmetic (45 % of the issue slots).
+// (5.34 TB/s, 0.79 of the measured copy rate), with the norm's pass 435 us; decoding both moments 167 us
+// (1.05 GB, 6.27 TB/s, 0.92).  In the update a block's loads wait on one another's arithmetic (45 % of the issue slots).
 #include <cmath>
 
 #include "internal.cuh"
@@ -51,9 +51,21 @@ struct Table {
   int count;
 };
 
-// The tensor of tile t, from that of an earlier tile.  A block's tiles only go forward, so this is one comparison for
-// most of them; a search from scratch put six dependent loads ahead of every tile's (74 tensors, 104.7 M weights:
-// step with norm 522 us so, 494 now).
+// The table in shared memory.  Reads of the parameters at an index of its own wait for one another, several before
+// every tile's data where tensors are small (104.7 M weights in 74 tensors: step with norm 522 us with a search there,
+// 492 with the walk below, 435 with both).
+template <int THREADS>
+__device__ __forceinline__ void table_in(Table& to, const Table& from) {
+  constexpr int kWords = sizeof(Table) / 8;
+  static_assert(sizeof(Table) % 8 == 0, "words");
+#pragma unroll
+  for (int u = 0; u < (kWords + THREADS - 1) / THREADS; ++u) {
+    const int i = u * THREADS + threadIdx.x;
+    if (i < kWords) reinterpret_cast<uint64_t*>(&to)[i] = reinterpret_cast<const uint64_t*>(&from)[i];
+  }
+  __syncthreads();
+}
+// The tensor of tile t, from that of an earlier tile: a block's tiles only go forward.
 template <typename TB>
 __device__ __forceinline__ int tensor_of(const TB& tb, int t, int k) {
   while (tb.tile0[k + 1] <= t) ++k;
@@ -77,8 +89,10 @@ __device__ __forceinline__ void add_square(float& hi, float& lo, float x) {
 
 // Partial sums of g² of one group: one per CTA (the grid is fixed by the tile count and the device,
 // so the order of the sums is too).
-__global__ void __launch_bounds__(kNormThreads, 3) sq8_kernel(const __grid_constant__ Table tb,
+__global__ void __launch_bounds__(kNormThreads, 3) sq8_kernel(const __grid_constant__ Table table,
                                                              double* __restrict__ part) {
+  __shared__ Table tb;
+  table_in<kNormThreads>(tb, table);
   pdl_begin();
   __shared__ double sh[kNormThreads / 32];
   const int tiles = tb.tile0[tb.count];
@@ -295,7 +309,9 @@ __device__ __forceinline__ void step_block(float* p, const float* g, int8_t* mc,
 }
 
 template <typename TS>
-__global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_constant__ Table tb, const Hyper h) {
+__global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_constant__ Table table, const Hyper h) {
+  __shared__ Table tb;
+  table_in<kThreads>(tb, table);
   pdl_begin();
   __shared__ float sh_f;
   float f = h.scale;
@@ -536,8 +552,8 @@ int xt_adamw8_step(const xt_adamw_config* cfg, int n, float* const* param, const
     // a launch without tiles still reports the norm of tensors that are all empty
     if (tiles == 0 && (any || !norm_out || first + kMaxTensors < n)) continue;
     any = true;
-    // the blocks that fit at once (three per SM), each walking its tiles: 104.7 M weights 358 us, 393 with a grid of
-    // eight per SM; asking L2 for the next tile ahead of time made it 428
+    // the blocks that fit at once (three per SM), each walking its tiles: 104.7 M weights 353 us, 378 with a grid of
+    // six per SM; asking L2 for the next tile ahead of time made it 428
     const int cap = num_sms() * 3;
     const int grid = tiles < 1 ? 1 : tiles < cap ? tiles : cap;
     if (shadow && shadow_dtype == XT_BF16) launch(adamw8_kernel<bf16>, grid, kThreads, 0, s, tb, h);
