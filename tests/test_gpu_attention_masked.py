@@ -328,3 +328,30 @@ def test_long_text():
     c = Case(off=[0, 5000, 8100], H=2, Hkv=1, hd=128, cap=30.0, qstd=4.0)
     val, tol = c.reference()
     compare(c.run(), val, tol)
+
+
+def test_offsets_beyond_32_bits():
+    """The last of 1024 texts, whose elements lie behind 2^32, gives what it gives alone, bit for bit."""
+    T, n, H, hd = 1 << 20, 1024, 16, 128
+    d = H * hd
+    g = torch.Generator(device="cuda").manual_seed(5)
+    last = torch.randn(n, 4 * d, generator=g, device="cuda").to(torch.bfloat16)
+
+    def run(T):
+        qkvg = torch.zeros(T, 4 * d, dtype=torch.bfloat16, device="cuda")
+        qkvg[-n:] = last
+        q, k, v, do = qkvg.split(d, 1)
+        out = torch.full((T, 4 * d), 7.0, dtype=torch.bfloat16, device="cuda")
+        o, dq, dk, dv = out.split(d, 1)
+        lse = torch.full((H, T), 7.0, device="cuda")
+        plan = xt.attention_plan_buffer(T)
+        xt.xt_attention_plan(plan, T, T // n)
+        xt.xt_attention_masked_fwd(q, k, v, o, lse, plan, H, H, hd)
+        xt.xt_attention_masked_bwd(q, k, v, o, do, lse, dq, dk, dv, plan, H, H, hd)
+        torch.cuda.synchronize()
+        assert xt.device_errors() == 0
+        return out[-n:].clone(), lse[:, -n:].clone(), out[:n].clone()
+
+    alone, far = run(n), run(T)
+    assert torch.equal(alone[0], far[0]) and torch.equal(alone[1], far[1])
+    assert not bool(far[2].any())   # the first text is all zeros
