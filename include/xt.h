@@ -320,7 +320,8 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  * workspace holds D and lse by whole tiles (and partial sums where few shared key heads are split over the GPU).
  * Outputs, inputs, the plan and the workspace must not overlap (views of one buffer's columns do not).
  * Supported: dtype = XT_BF16, hd 64 or 128, row strides multiples of 8 elements, all pointers 16-byte
- * aligned, T < 2³⁰, n_docs < 2³⁰, cap ≤ 1024 (a larger one leaves bf16-sized scores as they are: use 0) (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
+ * aligned, T and n_docs < 2³⁰, cap ≤ 1024 (capped scores are resolved to 1.2e-4 there) and not so small
+ * that scale/cap overflows (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
  * device-side waits are bounded (XT_DEVERR_TIMEOUT).
  * ------------------------------------------------------------------------------- */
 typedef struct xt_attention_desc {

@@ -171,6 +171,9 @@ CASES = {
     "tail-outside": dict(off=[3, 200], H=2, T=333),
     "cap": dict(off=[0, 140, 270], H=2, cap=30.0, qstd=8.0),
     "cap-128": dict(off=[0, 140, 270], H=4, Hkv=2, hd=128, cap=50.0, qstd=8.0),
+    "one-key-head": dict(off=[0, 200, 333], H=12, Hkv=1),
+    "one-key-head-128": dict(off=[0, 77, 333], H=6, Hkv=1, hd=128, bias=True),
+    "uneven-parts": dict(off=list(range(0, 9729, 128)), H=10, Hkv=2),  # five heads of a group in parts of 2, 2 and 1
     "cap-large": dict(off=[0, 140, 270], H=2, cap=1000.0, qstd=8.0),
     "cap-small": dict(off=[0, 200], H=1, cap=0.5, qstd=1.0),
     "bias": dict(off=[0, 140, 470], H=3, bias=True),
@@ -355,3 +358,27 @@ def test_offsets_beyond_32_bits():
     alone, far = run(n), run(T)
     assert torch.equal(alone[0], far[0]) and torch.equal(alone[1], far[1])
     assert not bool(far[2].any())   # the first text is all zeros
+
+
+@pytest.mark.parametrize("hd,H,Hkv", [(64, 2, 2), (128, 2, 2), (64, 4, 1)])
+@pytest.mark.parametrize("T", [1, 31, 97, 200])
+def test_outputs_touch_nothing_else(T, hd, H, Hkv):
+    """Outputs inside a larger buffer: the columns beside and the rows behind them stay as they were."""
+    W, pad, rows = (2 * H + 2 * Hkv) * hd, 64, T + 70
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q, k, v, do = torch.randn(T, W, generator=g, device="cuda").to(torch.bfloat16).split([H * hd, Hkv * hd, Hkv * hd, H * hd], 1)
+    buf = torch.full((rows, W + 2 * pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, dq, dk, dv = buf[:T, pad:pad + W].split([H * hd, H * hd, Hkv * hd, Hkv * hd], 1)
+    lse = torch.empty(H, T, device="cuda")
+    plan = xt.attention_plan_buffer(T)
+    xt.xt_attention_plan(plan, T, 1)
+    xt.xt_attention_masked_fwd(q, k, v, o, lse, plan, H, Hkv, hd)
+    for outs, done in (((o,), [o]), ((dq, dk, dv), [o, dq, dk, dv])):
+        if len(outs) > 1:
+            xt.xt_attention_masked_bwd(q, k, v, o, do, lse, dq, dk, dv, plan, H, Hkv, hd)
+        mark = torch.zeros_like(buf, dtype=torch.bool)
+        for t in done:
+            c = (t.data_ptr() - buf.data_ptr()) // 2
+            mark[:T, c:c + t.shape[1]] = True
+        assert bool((buf[~mark] == 7.0).all())
+    assert xt.device_errors() == 0

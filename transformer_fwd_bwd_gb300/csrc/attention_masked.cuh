@@ -1062,7 +1062,8 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // 0.67 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and some 4000 cycles per item
 // for D₀, the last products' arrival and the epilogue, where a tile takes 2100 (hd 64) to 2900 (hd 128).
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
-constexpr uint32_t kBwdRegsCtl = 88, kBwdRegsRows = 208;  // 128·88 + 256·208 = 384·168
+constexpr uint32_t kBwdRegsCtl = 88, kBwdRegsRows = 208;  // 128·88 + 256·208 = 384·168; at 72 the query pass's issuer
+// spills at hd 128 (8192 unmasked tokens: 1383 us against 1300), where the forward's does not (above)
 constexpr int PW = BT / 2;        // columns of a row warp
 
 template <int HD, bool KEY>
