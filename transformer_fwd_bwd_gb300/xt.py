@@ -578,12 +578,13 @@ def _token_rows(T, hd, dtype, *pairs):
     """(pointer, row stride) of each [T, heads·hd] tensor, flattened."""
     out = []
     for t, heads in pairs:
-        if t.dim() != 2 or t.shape[0] != T or t.shape[1] != heads * hd or t.dtype != dtype:
-            raise ValueError(f"expected a [{T}, {heads * hd}] tensor of {dtype}")
-        st0, st1 = t.stride()
-        if st1 != 1:
+        cols = heads * hd
+        if t.shape != (T, cols) or t.dtype is not dtype or not t.is_cuda:
+            raise ValueError(f"expected a [{T}, {cols}] CUDA tensor of {dtype}")
+        ld, unit = t.stride()
+        if unit != 1:
             raise ValueError("unit column stride is needed")
-        out += [ptr(t, False), st0 if T > 1 else max(st0, -(-heads * hd // 8) * 8)]
+        out += (t.data_ptr(), ld if T > 1 else max(ld, -(-cols // 8) * 8))
     return out
 
 
@@ -594,9 +595,8 @@ def xt_attention_masked_fwd(q, k, v, o, lse, plan, H, Hkv, hd, scale=None, cap=0
     if lse.dtype != torch.float32 or lse.numel() != H * T:
         raise ValueError("lse must be float32 [H, T]")
     d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
-    q_, k_, v_, o_ = (_token_rows(T, hd, q.dtype, x) for x in ((q, H), (k, Hkv), (v, Hkv), (o, H)))
-    call("xt_attention_masked_fwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, *o_,
-         ptr(lse), stream(s))
+    call("xt_attention_masked_fwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(),
+         *_token_rows(T, hd, q.dtype, (q, H), (k, Hkv), (v, Hkv), (o, H)), ptr(lse), stream(s))
 
 
 def xt_attention_masked_bwd(q, k, v, o, d_o, lse, dq, dk, dv, plan, H, Hkv, hd, scale=None, cap=0.0, slopes=None,
@@ -608,10 +608,9 @@ def xt_attention_masked_bwd(q, k, v, o, d_o, lse, dq, dk, dv, plan, H, Hkv, hd, 
     d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
     if ws is None:
         ws = attention_masked_workspace(T, H, Hkv, hd, q.device)
-    q_, k_, v_, o_, do_, dq_, dk_, dv_ = (_token_rows(T, hd, q.dtype, x) for x in (
-        (q, H), (k, Hkv), (v, Hkv), (o, H), (d_o, H), (dq, H), (dk, Hkv), (dv, Hkv)))
-    call("xt_attention_masked_bwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *q_, *k_, *v_, *o_,
-         *do_, ptr(lse), *dq_, *dk_, *dv_, ptr(ws), ws.numel() * ws.element_size(), stream(s))
+    rows = _token_rows(T, hd, q.dtype, (q, H), (k, Hkv), (v, Hkv), (o, H), (d_o, H), (dq, H), (dk, Hkv), (dv, Hkv))
+    call("xt_attention_masked_bwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *rows[:10], ptr(lse),
+         *rows[10:], ptr(ws), ws.numel() * ws.element_size(), stream(s))
 
 
 def xt_softmax_bwd(d, y, dx, causal=0, q_len=0, acc=0, s=None):
