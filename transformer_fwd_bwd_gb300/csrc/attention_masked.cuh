@@ -165,14 +165,14 @@ struct Mma {
       tc_mma<kBf16>(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
     }
   }
-  // D [128 × HD] (+)= A B over N tokens: A bf16 in tensor memory, 64 tokens (32 columns) every `step` columns,
+  // D [128 × HD] (+)= A B over N tokens: A bf16 in tensor memory, GROUP tokens (two to a column) every `step` columns,
   // B's N rows from b on, MN-major
-  template <int N = BT>
+  template <int N = BT, int GROUP = 64>
   static __device__ __forceinline__ void tn(uint32_t d, uint32_t a, uint32_t step, uint32_t b, bool first) {
     constexpr uint32_t kIdesc = instr_desc_bf16(128, HD, false, true);
 #pragma unroll
     for (int kk = 0; kk < N / 16; ++kk)
-      tc_mma_ts(d, a + uint32_t(kk >> 2) * step + uint32_t(kk & 3) * 8, smem_desc(b + kk * 2048, TILE, 1024), kIdesc,
+      tc_mma_ts(d, a + uint32_t(kk / (GROUP / 16)) * step + uint32_t(kk % (GROUP / 16)) * 8, smem_desc(b + kk * 2048, TILE, 1024), kIdesc,
                 (!first || kk > 0) ? 1u : 0u);
   }
   static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int head, int tile) {
@@ -1049,6 +1049,13 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // D = D₀ + T,  dQ = scale·(Σ dS₀ K − T·Σ W K)  exactly.  It leaves −lse·log₂e and −D in the workspace, rows padded
 // to whole tiles, from where the key pass, which follows it, copies them in with each query tile.
 //
+// Rounding dS to bf16 puts as much error into dK and dQ as their own rounding (2.4e-3 of both against float64, 1.7e-3
+// without).  Where few elements carry a row, the total varies most: so an edge tile's dS, and short documents have no other tiles,
+// is multiplied as the sum of two bf16s, the rounded value and what the rounding left, which has room in the chunk's own
+// columns: their dK and dQ are as exact as float32 arithmetic rounded once, for 9 % of the backward where all tiles are
+// edges (23 packed texts: 102 us, 93 without) and 2 % in a long text.  One loop issues both terms: a second copy of
+// the products' code makes their issuer spill (8192 unmasked tokens at hd 128: 1574 us against 1317).
+//
 // A tile's time is the rows' chain of tensor-memory loads, exponentials, stores and barriers, several times the
 // work in it, so two chains run side by side: each half of a tile's 128 columns has its own MMA issuer, four row
 // warps (one per TMEM lane quadrant), S and dP buffers, accumulators and barriers; P and dS are elementwise, so
@@ -1057,9 +1064,9 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // memory for one set of accumulators: there the halves' rows share one chain of 128 columns.
 //
 // What bounds it: the rows' chain at hd 64 (issue slots and tensor-memory latency: 8192 tokens without masks, 12 heads,
-// both passes: 880 us, 586 TFLOP/s of the formulas' five products and 938 of the eight that run, 0.49 of measured; one
-// chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1300 us, 792 and 1267 TFLOP/s,
-// 0.67 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and some 4000 cycles per item
+// both passes: 900 us, 573 TFLOP/s of the formulas' five products and 917 of the eight that run, 0.48 of measured; one
+// chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1317 us, 782 and 1252 TFLOP/s,
+// 0.66 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and some 4000 cycles per item
 // for D₀, the last products' arrival and the epilogue, where a tile takes 2100 (hd 64) to 2900 (hd 128).
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
 constexpr uint32_t kBwdRegsCtl = 88, kBwdRegsRows = 208;  // 128·88 + 256·208 = 384·168; at 72 the query pass's issuer
@@ -1235,6 +1242,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         if (it.h < 0) break;
         const int n = (it.r0.y - it.r0.x) * it.b;
         if (n <= 0) continue;
+        int t = it.r0.x;
         if (!spin(smem_u32(&B.a_full), na & 1, p.wait_ns)) { ok = false; break; }
         ++na;
         tc_fence_after();
@@ -1254,7 +1262,11 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
           if (next && !issue_s(g + 1)) { ok = false; break; }
           if (!spin(smem_u32(&b.ds_full), g & 1, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
-          Mma<HD>::template tn<BT / CH>(acc1, tDP, PW, slot(g), j == 0);  // dK += dSᵀ Q, dQ += dS K
+          const int terms = t < it.r0.z || t >= it.r0.w ? 2 : 1;  // dS of an edge tile: with its remainders
+#pragma unroll 1
+          for (int r = 0; r < terms; ++r)  // dK += dSᵀ Q, dQ += dS K
+            Mma<HD>::template tn<BT / CH, 32>(acc1, tDP + uint32_t(16 * r), 32, slot(g), j == 0 && r == 0);
+          if (++t == it.r0.y) t = it.r0.x;
           tc_commit(smem_u32(&B.r_empty[g % RING]));
           if (next) {
             issue_dp(g + 1);
@@ -1404,7 +1416,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         auto form_ds = [&](auto masked) {
 #pragma unroll
           for (int c = 0; c < PW; c += 32) {
-            uint32_t d[32], pk[16];
+            uint32_t d[32], pk[16], rest[16];
             tmem_ld32(tDP + uint32_t(c), d);
             tmem_ld_wait();
 #pragma unroll
@@ -1439,8 +1451,17 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
               if constexpr (KEY || CAP) hide();
               pk[e >> 1] = pack_bf16(x[0], x[1]);
               pk[(e >> 1) + 1] = pack_bf16(x[2], x[3]);
+              if constexpr (decltype(masked)::value) {
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                  const uint32_t w = pk[(e + k) >> 1];
+                  rest[(e + k) >> 1] =
+                      pack_bf16(x[k] - __uint_as_float(w << 16), x[k + 1] - __uint_as_float(w & 0xFFFF0000u));
+                }
+              }
             }
-            tmem_st16(tDP + uint32_t(c / 2), pk);
+            tmem_st16(tDP + uint32_t(c), pk);
+            if constexpr (decltype(masked)::value) tmem_st16(tDP + uint32_t(c + 16), rest);
           }
         };
         if (edge) form_ds(std::true_type{});
