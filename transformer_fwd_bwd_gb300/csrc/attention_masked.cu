@@ -132,7 +132,8 @@ attnm::Params params(const xt_attention_desc* d, const void* plan) {
 // Items of the key pass per key tile and head: shared key heads leave few of them, each over the whole group
 // of query heads.  Where they are fewer than four per SM of a GB300 the group is cut into up to its heads, the
 // parts' float32 sums being joined by a second kernel (4 x 1023 tokens, 16 query and 4 key heads of 128:
-// backward 91 us, 103 without the cut, both with one bf16 of dS everywhere).  A constant SM count keeps the workspace's size a function of the problem alone.
+// backward 91 us, 103 without the cut, both with one bf16 of dS everywhere).  A constant SM count keeps the workspace's
+// size a function of the problem alone.
 int key_split(const xt_attention_desc* d) {
   constexpr int64_t kWanted = 4 * 152;
   const int64_t items = attn_plan::Layout(d->T).tiles * d->Hkv;
