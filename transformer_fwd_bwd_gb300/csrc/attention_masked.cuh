@@ -172,7 +172,8 @@ struct Mma {
     constexpr uint32_t kIdesc = instr_desc_bf16(128, HD, false, true);
 #pragma unroll
     for (int kk = 0; kk < N / 16; ++kk)
-      tc_mma_ts(d, a + uint32_t(kk / (GROUP / 16)) * step + uint32_t(kk % (GROUP / 16)) * 8, smem_desc(b + kk * 2048, TILE, 1024), kIdesc,
+      tc_mma_ts(d, a + uint32_t(kk / (GROUP / 16)) * step + uint32_t(kk % (GROUP / 16)) * 8,
+                smem_desc(b + kk * 2048, TILE, 1024), kIdesc,
                 (!first || kk > 0) ? 1u : 0u);
   }
   static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int head, int tile) {
@@ -1052,7 +1053,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // Rounding dS to bf16 puts as much error into dK and dQ as their own rounding (2.4e-3 of both against float64, 1.7e-3
 // without).  Where few elements carry a row, the total varies most: so an edge tile's dS, and short documents have no other tiles,
 // is multiplied as the sum of two bf16s, the rounded value and what the rounding left, which has room in the chunk's own
-// columns: their dK and dQ are as exact as float32 arithmetic rounded once, for 9 % of the backward where all tiles are
+// columns: their dK and dQ are as exact as float32 arithmetic rounded once, for 9 % of the backward where most tiles are
 // edges (23 packed texts: 102 us, 93 without) and 2 % in a long text.  One loop issues both terms: a second copy of
 // the products' code makes their issuer spill (8192 unmasked tokens at hd 128: 1574 us against 1317).
 //
