@@ -52,3 +52,20 @@ def test_scores_that_overflow_stay_in_their_document(hd, Hkv, causal):
     keep[90:200] = False
     compare_tokens(got, val, tol, keep)
     assert not bool(torch.isfinite(got["lse"][:, 90:200]).all())
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 1)], ids=["whole-groups", "split-group"])
+def test_plan_of_another_length_leaves_gradients_alone(H, Hkv):
+    """With a group of query heads in parts the parts' join writes nothing either."""
+    c = Case(off=[0, 300], H=H, Hkv=Hkv)
+    q, k, v = c.split(c.qkv)
+    got = c.run()
+    plan = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    xt.xt_attention_plan(plan, 260, 1)
+    d = [empty((300, n * 64), "bf16", fill=3.0) for n in (H, Hkv, Hkv)]
+    xt.xt_attention_masked_bwd(q, k, v, got["o"], c.do, got["lse"], *d, plan, H, Hkv, 64)
+    try:
+        assert xt.device_errors() == xt.XT_DEVERR_PLAN
+        assert all(bool((t == 3.0).all()) for t in d)
+    finally:
+        xt.clear_device_errors()

@@ -26,6 +26,7 @@ namespace {
 // dK and dV of a split key pass: the splits' sums added in order, scaled and rounded.
 __global__ void __launch_bounds__(256) attnm_join_kernel(const __grid_constant__ attnm::Params p, int width) {
   pdl_begin();
+  if (!attn_plan::valid(p.plan)) return;  // the passes have refused the plan: there are no sums
   const int64_t n = p.plan.T * width, per = n / 4;
   for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < 2 * per; v += int64_t(gridDim.x) * 256) {
     const bool is_v = v >= per;
