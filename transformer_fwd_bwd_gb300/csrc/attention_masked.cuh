@@ -579,14 +579,16 @@ struct Source {
     ++n;
     return true;
   }
-  // The next block's index; a request always ends before the block does.
-  __device__ __forceinline__ int take() {
+  // The next block's index (−1: none was left); a request always ends before the block does.  False when its reply did not
+  // come: whether a block was taken over is not known then, so the call must report it.
+  __device__ __forceinline__ bool take(int& next) {
     const uint32_t bar = smem_u32(&q->got);
     fence_proxy_async_smem();  // the last reply has been read
     mbar_expect_tx(bar, 16);
     take_block(smem_u32(&q->reply), bar);
-    if (!mbar_wait(bar, (n - 1) & 1)) return -1;
-    return taken_block(smem_u32(&q->reply));
+    if (!mbar_wait(bar, (n - 1) & 1)) return false;
+    next = taken_block(smem_u32(&q->reply));
+    return true;
   }
 };
 // Everybody else's: item n, false when the wait ran out.  All lanes of a warp, or one thread (WARP false).
@@ -742,7 +744,8 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
           Mma<HD>::load(sb + C::V + s * C::QT, &tmV, smem_u32(&B.v_full[s]), kh, j);
         }
         if (!ok || *abort_flag) { ok = false; break; }
-        const int next = src.take();
+        int next;
+        if (!src.take(next)) { ok = false; break; }
         if (next >= 0) it = describe<false, true>(p, next);
         else it.h = -1;
       }
@@ -1207,7 +1210,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
             }
           }
         if (!ok || *abort_flag) { ok = false; break; }
-        const int next = src.take();
+        int next;
+        if (!src.take(next)) { ok = false; break; }
         if (next >= 0) it = describe<KEY, false>(p, next);
         else it.h = -1;
       }
