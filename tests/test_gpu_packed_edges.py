@@ -69,3 +69,56 @@ def test_plan_of_another_length_leaves_gradients_alone(H, Hkv):
         assert all(bool((t == 3.0).all()) for t in d)
     finally:
         xt.clear_device_errors()
+
+
+@pytest.mark.parametrize("hd,Hkv", [(64, 2), (128, 2), (64, 1)])
+@pytest.mark.parametrize("y", [7.0, 8.0, -8.0, 10.0])
+def test_gradients_of_saturated_scores(y, hd, Hkv):
+    """Every score near y times the cap, where 1 − tanh² is 4e-6 to 8e-9 and the difference 1 − t·t of float32 numbers
+    is off by 2⁻²⁴.  As in Case.reference, but every error of dS is relative to the factor too:
+      dS    2⁻⁸ |dS| for its own rounding, 2⁻¹¹ |dS| for the factor's storage in 11 bits, 2(δ + 2⁻²⁰) |dS| for the error δ
+            of y in it (d ln(1 − t²)/dy = −2t) and its exponential,
+      W     the same factor beside D's correction;
+      dP    hd·2⁻²⁴ Σ|dO v| in float32, and what that adds up to in D."""
+    H, cap = 2, 1.0
+    off = [0, 3, 10, 40, 41, 140]
+    c = Case(off=off, H=H, Hkv=Hkv, hd=hd, cap=cap)
+    q, k, _ = c.split(c.qkv)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    near = lambda t, at: t.copy_(at + 0.05 * torch.randn(t.shape, generator=g, device="cuda"))  # noqa: E731
+    a = math.sqrt(abs(y) / math.sqrt(hd))
+    near(q, math.copysign(a, y))
+    near(k, a)
+    got = c.run()
+    q, k, v = (t.double().view(c.T, -1, hd) for t in c.split(c.qkv))
+    do, scale = c.do.double().view(c.T, H, hd), 1.0 / math.sqrt(hd)
+    val = {n: torch.zeros(c.T, m, hd, dtype=torch.float64, device="cuda") for n, m in (("dq", H), ("dk", Hkv))}
+    tol = {n: torch.zeros_like(t) for n, t in val.items()}
+    for b, e in zip(off, off[1:]):
+        at, see = slice(b, e), c.visible(e - b, 0)
+        for h in range(H):
+            kh = h // (H // Hkv)
+            Q, K, V, G = q[at, h], k[at, kh], v[at, kh], do[at, h]
+            x = Q @ K.T * scale / cap
+            delta = hd * 2.0 ** -24 * (Q.abs() @ K.abs().T) * scale / cap + 2.0 ** -22 * x.abs()
+            s = (cap * torch.tanh(x)).masked_fill(~see, -math.inf)
+            P = torch.softmax(s, 1)
+            slack = 1.0 / torch.cosh(x).square()
+            dP = G @ V.T
+            D = (P * dP).sum(1, keepdim=True)
+            dS = P * (dP - D) * slack
+            dPe = hd * 2.0 ** -24 * (G.abs() @ V.abs().T)
+            dPe = dPe + (P * dPe).sum(1, keepdim=True)
+            E = 2.0 ** -19 + 2 * (2.0 ** -21 * cap)   # float32 terms and the scores' resolution, as E of Case.reference
+            dSe = dS.abs() * (B8 + 2.0 ** -11 + 2 * (delta + 2.0 ** -20)) + P * slack * (E * (dP.abs() + D.abs()) + dPe)
+            o = P @ V
+            oerr = ((B8 + E) * P) @ V.abs() + B8 * o.abs()
+            dQe = dSe + 2 * B8 * P * slack * (G.abs() * oerr).sum(1, keepdim=True)
+            val["dq"][at, h] = scale * dS @ K
+            tol["dq"][at, h] = scale * dQe @ K.abs()
+            val["dk"][at, kh] += scale * dS.T @ Q
+            tol["dk"][at, kh] += scale * dSe.T @ Q.abs()
+    for n in val:
+        v64 = val[n].reshape(c.T, -1)
+        over = (got[n].double() - v64).abs() / (tol[n].reshape(c.T, -1) + B8 * v64.abs()).clamp_min(1e-30)
+        assert float(over.max()) <= 1.0, (n, float(over.max()))

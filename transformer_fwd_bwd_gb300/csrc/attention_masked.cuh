@@ -225,8 +225,15 @@ __device__ __forceinline__ void add_bias(uint32_t (&r)[N], float unit, float slo
 // column it would share a reciprocal with: it counts as beyond the cap.
 // 8192 causal tokens, 12 heads of 64, forward: 233 us (128 without a cap); the special-function unit alone takes 3 %
 // more than this mixture, the polynomial alone 4 %.
-template <int N>
-__device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
+//
+// `slack` (the backward's): 1 − tanh², times kSlack, as f16.  Beyond the cap 1 − t·t would be the rounding of t, so there it is
+// 4u(1 − u) of u = 1/(1 + e^{2y}), and 1 − u is e^{2y}·u where that is less than a half.  The power of two, which the
+// gradients' factors take back, keeps f16's normal range down to 1.9e-9 (|a/cap| of 10.4; 2⁻¹¹ of the value at most, half a
+// step, beside dS's own bf16 rounding of 2⁻⁸), for half the registers of float32; under that it is off by 9e-13.
+// (dS itself, of up to 1e34, stays in bf16's range.)
+constexpr float kSlack = 32768.f;
+template <int N, bool SLACK>
+__device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p, __half2 (&slack)[SLACK ? N / 2 : 1]) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < N; c += 2)
@@ -234,8 +241,16 @@ __device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
   const float most = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], 0.f) * p.capy;
   if (__any_sync(0xffffffffu, !(most <= 1.f))) {
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-      r[c] = __float_as_uint(fmaf(-2.f, rcp(1.f + ex2(__uint_as_float(r[c]) * p.capk)), 1.f));
+    for (int c = 0; c < N; c += 2) {
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float e = ex2(__uint_as_float(r[c + k]) * p.capk), u = rcp(1.f + e);
+        r[c + k] = __float_as_uint(fmaf(-2.f, u, 1.f));
+        if constexpr (SLACK) f[k] = 4.f * kSlack * u * (e < 1.f ? e * u : 1.f - u);
+      }
+      if constexpr (SLACK) slack[c / 2] = __floats2half2_rn(f[0], f[1]);
+    }
   } else {
     const uint64_t y2 = f32x2_pack(p.capy, p.capy), k2 = f32x2_pack(p.capk, p.capk), one2 = f32x2_pack(1.f, 1.f);
 #pragma unroll
@@ -255,6 +270,15 @@ __device__ __forceinline__ void tanh_cap(uint32_t (&r)[N], const Params& p) {
       f32x2_unpack(f32x2_mul(y, q), u, w);
       r[c] = __float_as_uint(u);
       r[c + 1] = __float_as_uint(w);
+      if constexpr (SLACK) {
+        const uint64_t all2 = f32x2_pack(kSlack, kSlack), neg2 = f32x2_pack(-kSlack, -kSlack);
+#pragma unroll
+        for (int k = c; k < c + 4; k += 2) {
+          const uint64_t t = pair(r[k], r[k + 1]);
+          f32x2_unpack(f32x2_fma(f32x2_mul(t, neg2), t, all2), u, w);
+          slack[k / 2] = __floats2half2_rn(u, w);
+        }
+      }
     }
   }
 }
@@ -355,7 +379,7 @@ __device__ __forceinline__ float pair_score(const Params& p, float dot, float sl
   if constexpr (CAP) {
     const float e = ex2(dot * p.capk), u = rcp(1.f + e);
     s = fmaf(-2.f * p.cap2, u, p.cap2);
-    slack = 4.f * u * (1.f - u);
+    slack = 4.f * u * (e < 1.f ? e * u : 1.f - u);
   }
   if constexpr (BIAS) s = fmaf(-slope2, fabsf(float(dist)), s);
   return s;
@@ -930,7 +954,10 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&b.s_free));
         }
-        if constexpr (CAP) tanh_cap(s, p);
+        if constexpr (CAP) {
+          __half2 none[1];
+          tanh_cap<128, false>(s, p, none);
+        }
         if constexpr (BIAS) add_bias(s, CAP ? p.cap2 : p.sc, slope2, j * BT - row, j < tile ? 1 : j > tile ? -1 : 0);
         if (j < rg.z || j >= rg.w) {
 #pragma unroll
@@ -1360,19 +1387,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
         const float unit = score_unit<CAP, BIAS>(p);
-        // 1 − tanh² ∈ [0, 1], as f16: half a step of 2⁻¹² beside dS's own bf16 rounding of 2⁻⁹, for half the registers
-        __half2 slack[CAP ? PW / 2 : 1];
-        if constexpr (CAP) {
-          tanh_cap(s, p);
-          const uint64_t one2 = f32x2_pack(1.f, 1.f), neg2 = f32x2_pack(-1.f, -1.f);
-#pragma unroll
-          for (int c = 0; c < PW; c += 2) {
-            const uint64_t y = pair(s[c], s[c + 1]);
-            float u, w;
-            f32x2_unpack(f32x2_fma(f32x2_mul(y, neg2), y, one2), u, w);
-            slack[c / 2] = __floats2half2_rn(u, w);
-          }
-        }
+        __half2 slack[CAP ? PW / 2 : 1];  // kSlack (1 − tanh²)
+        if constexpr (CAP) tanh_cap<PW, true>(s, p, slack);
         if constexpr (BIAS)
           add_bias(s, CAP ? p.cap2 : p.sc, slope2, t * BT + col0 - row, t < tile ? 1 : t > tile ? -1 : 0);
         const bool edge = t < rg.z || t >= rg.w;
@@ -1530,7 +1546,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       for (int w = 0; w < (KEY ? 2 : 1); ++w) {
         const CUtensorMap* tm = w ? &tmG2 : &tmG1;
         const bool raw = KEY && p.split > 1;  // the part's float32 sums
-        const float mul = w || raw ? 1.f : p.scale;
+        const float mul = w ? 1.f : (CAP ? 1.f / kSlack : 1.f) * (raw ? 1.f : p.scale);
         const uint32_t acc = tbase + (w ? C::ACC2 : C::ACC1) + lane_off + uint32_t(half * (HD / 2));
 #pragma unroll 1
         for (int c = 0; c < HD / 2; c += 32) {
