@@ -138,3 +138,41 @@ def test_short_documents_carry_what_the_rounding_of_ds_left(hd):
     for n in ("dq", "dk"):
         e = float((got[n].double() - val[n]).norm() / val[n].norm())
         assert e <= 2.0e-3, (n, e)
+
+
+def busy(stream):
+    """Some 20 ms of work on `stream`: what is queued behind it has not begun when the host goes on."""
+    with torch.cuda.stream(stream):
+        x = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+        for _ in range(30):
+            x = x @ x * 0.0
+    return x
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_workspaces_of_calls_on_another_stream(raw):
+    """ws = None and s = a busy stream: tensors that the current stream allocates after the call are its own."""
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if raw else side
+    T, H, hd = 2000, 2, 64
+    c = Case(off=[0, 700, T], H=H, hd=hd)
+    want, plan = c.run(), c.plan()
+    q, k, v = c.split(c.qkv)
+    d = torch.zeros_like(c.qkv)
+    g = torch.randn(4_000_000, device="cuda")
+    P = [[torch.ones_like(g)] for _ in range(2)]
+    st = [xt.adamw8_state(p) for p in P]
+    cfg = xt.adamw_config(1e-2, max_grad_norm=1.0, step=1)
+    xt.xt_adamw8_step(cfg, P[0], [g], *st[0])
+    nbytes = (xt.attention_masked_workspace(T, H, H, hd).numel(), xt.adamw8_workspace([g.numel()]).numel())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = busy(side)
+    xt.xt_attention_masked_bwd(q, k, v, want["o"], c.do, want["lse"], *c.split(d), plan, H, H, hd, s=s)
+    xt.xt_adamw8_step(cfg, P[1], [g], *st[1], s=s)
+    mine = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in nbytes * 4]
+    torch.cuda.synchronize()
+    assert xt.device_errors() == 0 and bool(torch.isfinite(held).all())
+    assert all(bool((t == 0x5A).all()) for t in mine)
+    assert all(torch.equal(a, want[n]) for a, n in zip(c.split(d), ("dq", "dk", "dv")))
+    assert torch.equal(P[0][0], P[1][0])

@@ -1,0 +1,51 @@
+"""The binding's and the library's host side at the edges of their contracts, without a GPU."""
+import contextlib
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def xt():
+    from transformer_fwd_bwd_gb300 import build
+    build.build()
+    from transformer_fwd_bwd_gb300 import xt as m
+    m.lib()
+    return m
+
+
+@pytest.mark.parametrize("make", ["workspace", "scratch"])
+def test_workspaces_are_made_under_the_stream_that_uses_them(xt, monkeypatch, make):
+    """Allocation and fill run under the call's stream, whatever form it is given in; without one under the current."""
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def under(s):
+        inside.append(s)
+        yield
+        inside.pop()
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+    for name in ("empty", "zeros"):
+        plain = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, plain=plain, **kw: seen.append(tuple(inside)) or plain(*a, **kw))
+    monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("handle", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    side = Stream(0x10)
+    for s, want in ((None, ()), (side, (side,)), (0x20, (("handle", 0x20),)), (0, ("default",))):
+        t = getattr(xt, make)(100, "cpu", s=s)
+        assert t.numel() == 100 and seen.pop() == want and not seen
+
+
+def test_every_call_gives_its_own_workspace_the_stream(xt):
+    """No binding that takes ws = None and s makes the workspace without s."""
+    import inspect
+    import re
+    made = re.findall(r"^ +ws = (\w+)\((.*)\)$", inspect.getsource(xt), re.M)
+    assert len(made) >= 18
+    for name, args in made:
+        assert re.search(r"(\bs=s|, s)$", args), (name, args)

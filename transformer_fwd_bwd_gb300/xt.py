@@ -8,6 +8,7 @@ library raises.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes as C
 import operator
 import os
@@ -286,9 +287,29 @@ def ws_bytes(name, *args) -> int:
     return int(out.value)
 
 
-def workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """Zero-filled scratch (the matmul workspace's flag words must start at zero)."""
-    return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+def _on(s):
+    """The context in which torch allocates and fills for stream `s` (what stream() takes).  A workspace that a call makes
+    for itself is freed when the call returns: allocated for another stream than the one that uses it, it could be given
+    away, or filled, while the kernels still run."""
+    if s is None:
+        return contextlib.nullcontext()
+    if not isinstance(s, torch.cuda.Stream):
+        handle = stream(s)
+        s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(s)
+
+
+def workspace(nbytes: int, device="cuda", s=None) -> torch.Tensor:
+    """Zero-filled scratch (the matmul workspace's flag words must start at zero) for calls on stream s (None: the
+    current one)."""
+    with _on(s):
+        return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+def scratch(nbytes: int, device="cuda", s=None) -> torch.Tensor:
+    """The same for workspaces whose contents on entry do not matter."""
+    with _on(s):
+        return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
 def gemm_set_schedule(mode: int):
@@ -371,7 +392,7 @@ def xt_scale_bwd(d, dx, alpha, acc=0, s=None):
 
 def xt_sum_fwd(x, out, ws=None, s=None):
     if ws is None:
-        ws = workspace(ws_bytes("xt_sum_workspace_size", x.numel()), x.device)
+        ws = workspace(ws_bytes("xt_sum_workspace_size", x.numel()), x.device, s=s)
     call("xt_sum_fwd", ptr(x), x.numel(), dt(x), ptr(out), ptr(ws), stream(s))
 
 
@@ -387,7 +408,7 @@ def xt_add_bias_fwd(x, bias, y, s=None):
 def xt_add_bias_bwd(d, dx, dbias, acc_dx=0, acc_dbias=0, ws=None, s=None):
     rows, cols = d.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_colsum_workspace_size", rows, cols), d.device)
+        ws = workspace(ws_bytes("xt_colsum_workspace_size", rows, cols), d.device, s=s)
     call("xt_add_bias_bwd", ptr(d), ptr(dx), ptr(dbias), rows, cols, dt(d), dt(dbias), ptr(ws), acc_dx,
          acc_dbias, stream(s))
 
@@ -433,7 +454,7 @@ def xt_rms_norm_fwd(x, gamma, y, inv_rms, eps, s=None):
 def xt_rms_norm_bwd(d, x, gamma, inv_rms, dx, dgamma, acc_dx=0, acc_param=0, ws=None, s=None):
     rows, cols = x.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_norm_bwd_workspace_size", rows, cols), x.device)
+        ws = workspace(ws_bytes("xt_norm_bwd_workspace_size", rows, cols), x.device, s=s)
     call("xt_rms_norm_bwd", ptr(d), ptr(x), ptr(gamma), ptr(inv_rms), ptr(dx), ptr(dgamma), rows, cols, dt(x),
          dt(dx) if dx is not None else dt(x), dt(dgamma) if dgamma is not None else dt(x), ptr(ws), acc_dx,
          acc_param, stream(s))
@@ -456,7 +477,7 @@ def xt_layernorm_fwd(x, gamma, beta, y, mean, rstd, eps, s=None):
 def xt_layernorm_bwd(d, x, gamma, mean, rstd, dx, dgamma, dbeta, acc_dx=0, acc_param=0, ws=None, s=None):
     rows, cols = x.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_norm_bwd_workspace_size", rows, cols), x.device)
+        ws = workspace(ws_bytes("xt_norm_bwd_workspace_size", rows, cols), x.device, s=s)
     pdt = dt(dgamma) if dgamma is not None else (dt(dbeta) if dbeta is not None else dt(x))
     call("xt_layernorm_bwd", ptr(d), ptr(x), ptr(gamma), ptr(mean), ptr(rstd), ptr(dx), ptr(dgamma), ptr(dbeta),
          rows, cols, dt(x), dt(dx) if dx is not None else dt(x), pdt, ptr(ws), acc_dx, acc_param, stream(s))
@@ -472,7 +493,7 @@ def xt_norm_bwd_dropout(norm, d, x, gamma, stat0, stat1, dx, dgamma, dbeta, g, p
                         acc_param=0, ws=None, s=None):
     rows, cols = x.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_norm_bwd_workspace_size", rows, cols), x.device)
+        ws = workspace(ws_bytes("xt_norm_bwd_workspace_size", rows, cols), x.device, s=s)
     pdt = dt(dgamma) if dgamma is not None else (dt(dbeta) if dbeta is not None else dt(x))
     call("xt_norm_bwd_dropout", norm, ptr(d), ptr(x), ptr(gamma), ptr(stat0), ptr(stat1), ptr(dx), ptr(dgamma),
          ptr(dbeta), ptr(g), rows, cols, dt(x), dt(dx), pdt, ptr(ws), acc_dx, acc_param, float(p),
@@ -538,7 +559,7 @@ def xt_attention_bwd(q, k, v, o, d_o, lse, dq, dk, dv, B, S, H, hd, causal=1, o_
     n = C.c_size_t(0)
     call("xt_attention_bwd_workspace_size", B, S, H, C.byref(n))
     if ws is None:
-        ws = torch.empty(max(1, n.value), dtype=torch.uint8, device=q.device)
+        ws = scratch(n.value, q.device, s)
     call("xt_attention_bwd", ptr(q, False), ptr(k, False), ptr(v, False), q.stride(0), ptr(o, False),
          ptr(o_lo, False), ptr(d_o, False), o.stride(0), ptr(lse), ptr(dq, False), ptr(dk, False), ptr(dv, False),
          dq.stride(0), ptr(ws), ws.numel(), B, S, H, hd, causal, dt(q), stream(s))
@@ -568,10 +589,10 @@ def _attention_desc(T, H, Hkv, hd, dtype, scale, cap, slopes):
     return AttentionDesc(int(T), H, Hkv, hd, dtype, float(scale or 0.0), float(cap), ptr(slopes))
 
 
-def attention_masked_workspace(T, H, Hkv, hd, device="cuda"):
-    """The backward's workspace."""
+def attention_masked_workspace(T, H, Hkv, hd, device="cuda", s=None):
+    """The backward's workspace (s: the stream that will use it; None: the current one)."""
     d = _attention_desc(T, H, Hkv, hd, XT_BF16, None, 0.0, None)
-    return torch.empty(ws_bytes("xt_attention_masked_bwd_workspace_size", C.byref(d)), dtype=torch.uint8, device=device)
+    return scratch(ws_bytes("xt_attention_masked_bwd_workspace_size", C.byref(d)), device, s)
 
 
 def _token_rows(T, hd, dtype, *pairs):
@@ -607,7 +628,7 @@ def xt_attention_masked_bwd(q, k, v, o, d_o, lse, dq, dk, dv, plan, H, Hkv, hd, 
         raise ValueError("lse must be float32 [H, T]")
     d = _attention_desc(T, H, Hkv, hd, dt(q), scale, cap, slopes)
     if ws is None:
-        ws = attention_masked_workspace(T, H, Hkv, hd, q.device)
+        ws = attention_masked_workspace(T, H, Hkv, hd, q.device, s=s)
     rows = _token_rows(T, hd, q.dtype, (q, H), (k, Hkv), (v, Hkv), (o, H), (d_o, H), (dq, H), (dk, Hkv), (dv, Hkv))
     call("xt_attention_masked_bwd", C.byref(d), ptr(plan), plan.numel() * plan.element_size(), *rows[:10], ptr(lse),
          *rows[10:], ptr(ws), ws.numel() * ws.element_size(), stream(s))
@@ -622,7 +643,7 @@ def xt_softmax_bwd(d, y, dx, causal=0, q_len=0, acc=0, s=None):
 def xt_cross_entropy_fwd(logits, targets, lse, loss, ws=None, s=None):
     rows, V = logits.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_cross_entropy_workspace_size", rows), logits.device)
+        ws = workspace(ws_bytes("xt_cross_entropy_workspace_size", rows), logits.device, s=s)
     call("xt_cross_entropy_fwd", ptr(logits), ptr(targets), ptr(lse), ptr(loss), rows, V, dt(logits), ptr(ws),
          stream(s))
 
@@ -631,7 +652,7 @@ def xt_cross_entropy_fwd_bwd(logits, targets, lse, loss, upstream, dlogits, ws=N
     """Forward and backward in one pass (dlogits may be logits)."""
     rows, V = logits.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_cross_entropy_workspace_size", rows), logits.device)
+        ws = workspace(ws_bytes("xt_cross_entropy_workspace_size", rows), logits.device, s=s)
     call("xt_cross_entropy_fwd_bwd", ptr(logits), ptr(targets), ptr(lse), ptr(loss), ptr(upstream), ptr(dlogits),
          rows, V, dt(logits), dt(dlogits), ptr(ws), stream(s))
 
@@ -642,7 +663,7 @@ def xt_cross_entropy_fanout_fwd_bwd(logits, targets, c_lin, c_sq, lse, loss, sum
     u the device scalar `upstream` (None: 1)."""
     rows, V = logits.shape
     if ws is None:
-        ws = workspace(ws_bytes("xt_cross_entropy_fanout_workspace_size", rows), logits.device)
+        ws = workspace(ws_bytes("xt_cross_entropy_fanout_workspace_size", rows), logits.device, s=s)
     call("xt_cross_entropy_fanout_fwd_bwd", ptr(logits), ptr(targets), float(c_lin), float(c_sq), ptr(upstream),
          ptr(lse), ptr(loss), ptr(sums), ptr(grad), int(acc), rows, V, dt(logits), ptr(ws), ws.numel(), stream(s))
 
@@ -686,7 +707,7 @@ def xt_embedding_bwd(ids, dh, dE, dP, S, acc=0, ws=None, s=None):
     V, d = dE.shape
     T = ids.numel()
     if ws is None:
-        ws = workspace(ws_bytes("xt_embedding_workspace_size", T), dh.device)
+        ws = workspace(ws_bytes("xt_embedding_workspace_size", T), dh.device, s=s)
     call("xt_embedding_bwd", ptr(ids), ptr(dh), ptr(dE), ptr(dP), T, S, d, V, dt(dh), dt(dE), ptr(ws), acc,
          stream(s))
 
@@ -711,9 +732,9 @@ def adamw_config(lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, max_grad
     return AdamWConfig(lr, beta1, beta2, eps, weight_decay, max_grad_norm, grad_scale, step)
 
 
-def adamw_workspace(numels, device="cuda"):
+def adamw_workspace(numels, device="cuda", s=None):
     arr = (C.c_int64 * max(1, len(numels)))(*numels)
-    return workspace(ws_bytes("xt_adamw_workspace_size", len(numels), arr), device)
+    return workspace(ws_bytes("xt_adamw_workspace_size", len(numels), arr), device, s)
 
 
 def xt_adamw_step(cfg, params, grads, m, v, shadows=None, norm_out=None, ws=None, s=None):
@@ -746,7 +767,7 @@ def xt_adamw_step(cfg, params, grads, m, v, shadows=None, norm_out=None, ws=None
         SH = (C.c_void_p * n)(*[(t.data_ptr() if t is not None else None) for t in shadows])
     N = (C.c_int64 * n)(*numel)
     if ws is None and (cfg.max_grad_norm > 0 or norm_out is not None):
-        ws = adamw_workspace(numel, params[0].device)
+        ws = adamw_workspace(numel, params[0].device, s=s)
     call("xt_adamw_step", C.byref(cfg), n, P, G, M, V, SH, sdt, N, ptr(norm_out), ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
 
@@ -767,9 +788,9 @@ def adamw8_state(params):
             [new(p, torch.float32, adamw8_scales(p.numel())) for p in params])
 
 
-def adamw8_workspace(numels, device="cuda"):
+def adamw8_workspace(numels, device="cuda", s=None):
     arr = (C.c_int64 * max(1, len(numels)))(*numels)
-    return workspace(ws_bytes("xt_adamw8_workspace_size", len(numels), arr), device)
+    return scratch(ws_bytes("xt_adamw8_workspace_size", len(numels), arr), device, s)
 
 
 # Lists of a hundred tensors are checked before every step: each property is read by one map over the list (with
@@ -818,7 +839,7 @@ def xt_adamw8_step(cfg, params, grads, m_code, r_code, m_scale, r_scale, shadows
             given = iter(sh)
             sh = (C.c_void_p * n)(*[next(given) if t is not None else None for t in shadows])
     if ws is None and n and (cfg.max_grad_norm > 0 or norm_out is not None):
-        ws = adamw8_workspace(numel, params[0].device)
+        ws = adamw8_workspace(numel, params[0].device, s=s)
     call("xt_adamw8_step", C.byref(cfg), n, *tables, sh, sdt, (C.c_int64 * max(1, n))(*numel), ptr(norm_out), ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
 
@@ -839,7 +860,7 @@ def xt_quantize_fp8(x, out, dequant, ws=None, s=None):
         raise ValueError("out must be uint8 with x's element count")
     n = x.numel()
     if ws is None:
-        ws = workspace(ws_bytes("xt_quantize_fp8_workspace_size", n), x.device)
+        ws = workspace(ws_bytes("xt_quantize_fp8_workspace_size", n), x.device, s=s)
     call("xt_quantize_fp8", ptr(x), n, dt(x), ptr(out), ptr(dequant), ptr(ws), ws.numel(), stream(s))
 
 
@@ -866,7 +887,7 @@ def matmul_workspace(desc, device="cuda"):
 def xt_matmul_fwd(desc, A, B, Cm, ws=None, s=None):
     n = ws_bytes("xt_matmul_workspace_size", C.byref(desc))
     if n and ws is None:
-        ws = workspace(n, Cm.device)
+        ws = workspace(n, Cm.device, s=s)
     call("xt_matmul_fwd", C.byref(desc), ptr(A, False), ptr(B, False), ptr(Cm, False), ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
 
@@ -875,7 +896,7 @@ def xt_matmul_gelu_fwd(desc, A, B, Cm, Y, ws=None, s=None):
     """Cm = alpha·op(A)@op(B) (bf16) and Y = gelu(Cm), from one GEMM."""
     n = ws_bytes("xt_matmul_workspace_size", C.byref(desc))
     if n and ws is None:
-        ws = workspace(n, Cm.device)
+        ws = workspace(n, Cm.device, s=s)
     call("xt_matmul_gelu_fwd", C.byref(desc), ptr(A, False), ptr(B, False), ptr(Cm, False), ptr(Y, False), ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
 
@@ -884,7 +905,7 @@ def xt_matmul_gelu_bwd(desc, A, B, X, Cm, ws=None, s=None):
     """Cm = (alpha·op(A)@op(B)) ∘ gelu'(X), X the saved pre-activation (Cm's layout)."""
     n = ws_bytes("xt_matmul_workspace_size", C.byref(desc))
     if n and ws is None:
-        ws = workspace(n, Cm.device)
+        ws = workspace(n, Cm.device, s=s)
     call("xt_matmul_gelu_bwd", C.byref(desc), ptr(A, False), ptr(B, False), ptr(X, False), ptr(Cm, False), ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
 
@@ -892,7 +913,7 @@ def xt_matmul_gelu_bwd(desc, A, B, X, Cm, ws=None, s=None):
 def xt_matmul_bwd(desc, A, B, dC, dA, dB, acc_a=0, acc_b=0, ws=None, s=None):
     n = ws_bytes("xt_matmul_bwd_workspace_size", C.byref(desc))
     if n and ws is None:
-        ws = workspace(n, dC.device)
+        ws = workspace(n, dC.device, s=s)
     call("xt_matmul_bwd", C.byref(desc), ptr(A, False), ptr(B, False), ptr(dC, False), ptr(dA, False),
          ptr(dB, False),
          dt(dA) if dA is not None else XT_F32, dt(dB) if dB is not None else XT_F32, acc_a, acc_b, ptr(ws),
