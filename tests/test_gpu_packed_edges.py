@@ -176,3 +176,26 @@ def test_workspaces_of_calls_on_another_stream(raw):
     assert all(bool((t == 0x5A).all()) for t in mine)
     assert all(torch.equal(a, want[n]) for a, n in zip(c.split(d), ("dq", "dk", "dv")))
     assert torch.equal(P[0][0], P[1][0])
+
+
+@pytest.mark.parametrize("shadow", [False, True], ids=["", "bf16-copy"])
+@pytest.mark.parametrize("eps", [1e-16, 1e-20, 1e-30, 1e-42])
+def test_adamw8_with_a_tiny_epsilon(eps, shadow):
+    """Second moments whose root matters beside ε: roots down to 1e-19 and an ε below float32's normal range.  First step, so
+    m' = (1 − β₁) g, v' = ((1 − β₂) g)·g; the update lr·m̂/(√v̂ + ε) carries 16·2⁻²⁴ of itself (m' 2 roundings, √v' 4, two
+    bias factors, root, quotient and sum), v' of at least 2⁻¹²⁶ being a normal number."""
+    g0 = np.concatenate([np.exp(np.linspace(math.log(6e-19), math.log(1e-15), 700)), np.zeros(100), [3e-5] * 224])
+    g0 = (g0 * np.where(np.arange(g0.size) % 3 == 1, -1, 1)).astype(np.float32)
+    p0 = np.where(np.arange(g0.size) < 700, 0.0, 0.5).astype(np.float32)
+    P, G = [torch.from_numpy(p0).cuda()], [torch.from_numpy(g0).cuda()]
+    S = [torch.zeros(p0.size, dtype=torch.bfloat16, device="cuda")] if shadow else None
+    b1, b2 = float(np.float32(0.9)), float(np.float32(0.95))
+    xt.xt_adamw8_step(xt.adamw_config(1e-3, beta1=0.9, beta2=0.95, eps=eps, weight_decay=0.1, step=1), P, G,
+                      *xt.adamw8_state(P), shadows=S)
+    g = g0.astype(np.float64)
+    m, v, e = (1 - b1) * g, (1 - b2) * g * g, float(np.float32(eps))
+    step = 1e-3 * (m / (1 - b1)) / (np.sqrt(v / (1 - b2)) + e)
+    got, want = P[0].double().cpu().numpy(), p0 * (1 - 1e-4) - step
+    # θ's own roundings: 3·2⁻²⁴ of its value (1 − lr·λ, the product, the sum)
+    assert np.all(np.abs(got - want) <= 16 * 2.0 ** -24 * np.abs(step) + 3 * 2.0 ** -24 * np.abs(want))
+    assert S is None or torch.equal(S[0], P[0].to(torch.bfloat16))
