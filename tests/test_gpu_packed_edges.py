@@ -199,3 +199,22 @@ def test_adamw8_with_a_tiny_epsilon(eps, shadow):
     # θ's own roundings: 3·2⁻²⁴ of its value (1 − lr·λ, the product, the sum)
     assert np.all(np.abs(got - want) <= 16 * 2.0 ** -24 * np.abs(step) + 3 * 2.0 ** -24 * np.abs(want))
     assert S is None or torch.equal(S[0], P[0].to(torch.bfloat16))
+
+
+def test_train_step_losses_on_a_busy_stream():
+    """The losses that train_step returns are copied on its stream, behind the forward that writes them."""
+    import synth
+    from transformer_fwd_bwd_gb300.block import NativeBlock
+    cfg = dict(synth.BLOCK_CONFIGS["gpt12"], B=1, S=64, d=64, H=1, hd=64, F=128, V=256, n_layers=1)
+    ids, tgt = (torch.from_numpy(a).cuda() for a in synth.block_tokens(cfg))
+    side, out = torch.cuda.Stream(), []
+    for s in (None, side):
+        nb = NativeBlock(cfg, device="cuda:0", training=True)
+        nb.load(synth.block_params(cfg))
+        nb.init_optimizer(lr=1e-2, state_bits=8)
+        torch.cuda.synchronize()
+        held = busy(side)
+        losses = nb.train_step([(ids, tgt), (ids.flip(0), tgt)], stream=s)
+        torch.cuda.synchronize()
+        out.append([float(x) for x in losses])
+    assert out[0] == out[1] and bool(torch.isfinite(held).all())

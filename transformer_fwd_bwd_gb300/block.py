@@ -233,7 +233,8 @@ class NativeBlock:
         losses = []
         for ids, targets in microbatches:
             self.forward(ids, targets, stream)
-            losses.append(self.loss.clone())
+            with xt.on_stream(stream):
+                losses.append(self.loss.clone())
             self.backward(ids, targets, stream)
         self.optimizer_step(len(microbatches), stream)
         return losses

@@ -287,7 +287,7 @@ def ws_bytes(name, *args) -> int:
     return int(out.value)
 
 
-def _on(s):
+def on_stream(s):
     """The context in which torch allocates and fills for stream `s` (what stream() takes).  A workspace that a call makes
     for itself is freed when the call returns: allocated for another stream than the one that uses it, it could be given
     away, or filled, while the kernels still run."""
@@ -302,13 +302,13 @@ def _on(s):
 def workspace(nbytes: int, device="cuda", s=None) -> torch.Tensor:
     """Zero-filled scratch (the matmul workspace's flag words must start at zero) for calls on stream s (None: the
     current one)."""
-    with _on(s):
+    with on_stream(s):
         return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
 def scratch(nbytes: int, device="cuda", s=None) -> torch.Tensor:
     """The same for workspaces whose contents on entry do not matter."""
-    with _on(s):
+    with on_stream(s):
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
