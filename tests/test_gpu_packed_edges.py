@@ -218,3 +218,14 @@ def test_train_step_losses_on_a_busy_stream():
         torch.cuda.synchronize()
         out.append([float(x) for x in losses])
     assert out[0] == out[1] and bool(torch.isfinite(held).all())
+
+
+def test_tape_rope_axes_refuses_columns_beside_the_heads():
+    """xt_rope_axes_fwd rotates the first H·hd columns; a node's value and gradient are whole tensors."""
+    from transformer_fwd_bwd_gb300 import tape
+    pos = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    x = torch.ones(8, 3 * 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        tape.rope_axes(tape.leaf(x), pos, [8, 24], 2, 64)
+    y = tape.rope_axes(tape.leaf(x), pos, [8, 24], 3, 64)
+    assert torch.equal(y.value, x)   # position 0

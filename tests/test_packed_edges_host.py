@@ -49,3 +49,11 @@ def test_every_call_gives_its_own_workspace_the_stream(xt):
     assert len(made) >= 18
     for name, args in made:
         assert re.search(r"(\bs=s|, s)$", args), (name, args)
+
+
+def test_tape_rope_axes_refuses_columns_beside_the_heads(xt):
+    from transformer_fwd_bwd_gb300 import tape
+    pos = torch.zeros(2, 8, dtype=torch.int32)
+    for x in (torch.ones(8, 192), torch.ones(8, 64), torch.ones(8, 2, 64)):
+        with pytest.raises(ValueError, match="H\\*hd"):
+            tape.rope_axes(tape.leaf(x), pos, [8, 24], 2, 64)

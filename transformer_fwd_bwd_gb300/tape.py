@@ -369,6 +369,8 @@ def attention(q: Var, k: Var, v: Var, causal: bool = True) -> Var:
 
 def rope_axes(x: Var, pos: torch.Tensor, sections, H: int, hd: int, base: float = 10000.0, per_axis: bool = False) -> Var:
     """Rotary positions over several axes on [T, H·hd] rows (pos int32 [axes, T], sections: pairs per axis)."""
+    if x.value.dim() != 2 or x.value.shape[1] != H * hd:  # wider rows would leave columns of y and dx unwritten
+        raise ValueError("x must be [T, H*hd]")
     y = _empty_like(x.value)
     xt.xt_rope_axes_fwd(x.value, y, pos, sections, H, hd, base, int(per_axis))
 
