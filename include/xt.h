@@ -503,7 +503,8 @@ int xt_gemm_set_schedule(int mode);
  * 256-row tiles), each CTA loading half of its B rows for both pairs.  0 = the time model's
  * choice (default; never the multicast form, which measured slower than the plain pairs on
  * the 12-layer stack's shapes), 1 = never, 2 = the plain pairs wherever allowed, 3 = the
- * multicast form wherever allowed (else as 2).  Every kernel accumulates in fp32 over the same K order; the
+ * multicast form wherever allowed (else as 2; XT_ERR_UNSUPPORTED where the process sees several GPUs or
+ * is one of several ranks, WORLD_SIZE > 1).  Every kernel accumulates in fp32 over the same K order; the
  * choice is deterministic for a given shape.  XT_ERR_INVALID_ARG otherwise. */
 int xt_gemm_set_pairing(int mode);
 /* Process-wide override of the GEMM tile width: 0 = the time model's choice (default), else

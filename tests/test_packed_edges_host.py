@@ -57,3 +57,16 @@ def test_tape_rope_axes_refuses_columns_beside_the_heads(xt):
     for x in (torch.ones(8, 192), torch.ones(8, 64), torch.ones(8, 2, 64)):
         with pytest.raises(ValueError, match="H\\*hd"):
             tape.rope_axes(tape.leaf(x), pos, [8, 24], 2, 64)
+
+
+def test_multicast_pairs_are_for_one_gpu(xt, monkeypatch):
+    try:
+        monkeypatch.setenv("WORLD_SIZE", "2")
+        assert xt.lib().xt_gemm_set_pairing(3) == xt.XT_ERR_UNSUPPORTED
+        assert b"one GPU" in xt.lib().xt_last_error()
+        assert [xt.lib().xt_gemm_set_pairing(m) for m in (1, 2, 0)] == [0, 0, 0]
+        monkeypatch.setenv("WORLD_SIZE", "1")
+        if torch.cuda.device_count() <= 1:
+            assert xt.lib().xt_gemm_set_pairing(3) == xt.XT_OK
+    finally:
+        xt.lib().xt_gemm_set_pairing(0)

@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -568,6 +569,14 @@ int xt_gemm_set_tile(int bn) {
 
 int xt_gemm_set_pairing(int mode) {
   XT_REQUIRE(mode >= 0 && mode <= 3, "xt_gemm_set_pairing: mode must be 0..3");
+  // a TMA load that is multicast to a cluster belongs to programs on one GPU alone
+  if (mode == 3) {
+    int gpus = 0;
+    if (cudaGetDeviceCount(&gpus) != cudaSuccess) cudaGetLastError();  // no GPU: nothing will run
+    const char* ranks = std::getenv("WORLD_SIZE");
+    if (gpus > 1 || (ranks && std::atoi(ranks) > 1))
+      return fail(XT_ERR_UNSUPPORTED, "xt_gemm_set_pairing: the multicast form is for programs on one GPU");
+  }
   gemm::g_pairing = mode;
   return XT_OK;
 }
