@@ -311,7 +311,8 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  * plan: xt_attention_plan_size(T) bytes, 16-byte aligned, a function of these arrays' values when the call
  * runs.  Offsets that fall or leave [0, T], lengths outside the span and negative prefixes set
  * XT_DEVERR_INDEX; no access depends on them.  A plan made for another T sets XT_DEVERR_PLAN and the
- * attention call writes nothing.
+ * attention call writes nothing.  Only T is checked: the backward must find the plan that its forward had, so a buffer is
+ * not filled for the next batch (of as many tokens) before the last one's backward has been queued on the stream.
  *
  * Layout: token t of q is row t (ld_q elements apart), its head h columns [h·hd, h·hd + hd); k, v likewise
  * with Hkv heads, o, d_o and dq as q, dk and dv as k.  lse: float32 [H][T].  scale = 0 means 1/√hd.
@@ -321,8 +322,9 @@ int xt_attention_bwd(const void* q, const void* k, const void* v, int64_t ld_qkv
  * Outputs, inputs, the plan and the workspace must not overlap (views of one buffer's columns do not).
  * Supported: dtype = XT_BF16, hd 64 or 128, row strides multiples of 8 elements, all pointers 16-byte
  * aligned, T and n_docs < 2³⁰, cap ≤ 1024 (capped scores are resolved to 1.2e-4 there) and not so small
- * that scale/cap overflows (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic;
- * device-side waits are bounded (XT_DEVERR_TIMEOUT).
+ * that scale/cap overflows (else XT_ERR_UNSUPPORTED / XT_ERR_ALIGNMENT / XT_ERR_INVALID_ARG).  Deterministic: equal
+ * calls give equal bits.  A document's last bits depend on where it lies in the row (its place among 128-token tiles)
+ * and, with a cap, on the values beside it (2⁻²³ of the cap).  Device-side waits are bounded (XT_DEVERR_TIMEOUT).
  * ------------------------------------------------------------------------------- */
 typedef struct xt_attention_desc {
   int64_t T;
@@ -597,7 +599,8 @@ int xt_adamw_step(const xt_adamw_config* cfg, int n, float* const* param, const 
  *   m_scale = max|m'|/127², c = sign(m')·rint(√(|m'|/m_scale)), r_scale = √(max v')/255²,
  *   c = rint(√(√v'/r_scale)), but at least 1 where v' > 0,
  * so the codes are defined to the last bit.  State of zeros (codes and scales) is the state before the first
- * step.  A block with a gradient that is not finite ends with scales that decode to NaN (its θ is NaN too).
+ * step.  A gradient that is not finite, or whose square is not (|g'| above 1.8e19/√(1−β₂)), leaves its block of 256 with
+ * scales that decode to NaN (θ of the element is NaN at once, of the block by the next step).
  * Arguments as for xt_adamw_step, with m_code, r_code, m_scale and r_scale HOST arrays of device pointers.
  * The workspace (xt_adamw8_workspace_size, 8-byte aligned) is needed when clipping or norm_out is
  * requested; its contents on entry do not matter.  Deterministic.

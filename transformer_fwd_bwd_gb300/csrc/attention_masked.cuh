@@ -220,15 +220,17 @@ __device__ __forceinline__ void add_bias(uint32_t (&r)[N], float unit, float slo
 // r[c] = tanh(scale·r[c]/cap) = 1 − 2/(1 + e^{2y}), one exponential and one reciprocal.  Where no element of the
 // warp's rows is beyond the cap the special-function unit and the multipliers share the work: of four columns two go
 // through y·p(y²), p of degree 6 fitted to tanh(y)/y over |y| ≤ 1 (least squares reweighted to equal extremes,
-// Lawson's method; error 9e-8), and two through exponentials and the reciprocal of the product of their
-// denominators, 1/a = b·1/(ab) (at most 8.4² there).  A NaN, which may stand in a masked column, must not reach the
-// column it would share a reciprocal with: it counts as beyond the cap.
+// Lawson's method; tanh(y) is off by 2.6e-8 at most, 3.0e-7 of itself near 0), and two through exponentials and the
+// reciprocal of the product of their denominators, 1/a = b·1/(ab) (at most 8.4² there).  A NaN, which may stand in a masked
+// column, must not reach the column it would share a reciprocal with: it counts as beyond the cap.  The choice is one for
+// the warp's 32 rows and all columns, hidden ones too, so the last bits of a capped score (2⁻²³ of the cap) depend on what
+// lies beside it, and the two directions may differ by as much.
 // 8192 causal tokens, 12 heads of 64, forward: 233 us (128 without a cap); the special-function unit alone takes 3 %
 // more than this mixture, the polynomial alone 4 %.
 //
 // `slack` (the backward's): 1 − tanh², times kSlack, as f16.  Beyond the cap 1 − t·t would be the rounding of t, so there it is
 // 4u(1 − u) of u = 1/(1 + e^{2y}), and 1 − u is e^{2y}·u where that is less than a half.  The power of two, which the
-// gradients' factors take back, keeps f16's normal range down to 1.9e-9 (|a/cap| of 10.4; 2⁻¹¹ of the value at most, half a
+// gradients' factors take back, keeps f16's normal range down to 1.9e-9 (|a/cap| of 10.7; 2⁻¹¹ of the value at most, half a
 // step, beside dS's own bf16 rounding of 2⁻⁸), for half the registers of float32; under that it is off by 9e-13.
 // (dS itself, of up to 1e34, stays in bf16's range.)
 constexpr float kSlack = 32768.f;
@@ -649,7 +651,7 @@ __device__ __forceinline__ void queue_init(Queue* q, int readers) {
 // without masks, 12 heads, 263 us, 784 TFLOP/s, 0.41 of measured; at hd 128 as much time goes into the products: 392 us,
 // 1051 TFLOP/s, 0.55.  8192 causal tokens 128 us, where the kernel without masks takes 161.
 constexpr int kThreadsFwd = 384;
-constexpr uint32_t kFwdRegsCtl = 72, kFwdRegsRows = 216;  // 128·88 + 256·208 = 384·168
+constexpr uint32_t kFwdRegsCtl = 72, kFwdRegsRows = 216;  // 128·72 + 256·216 = 384·168
 
 template <int HD>
 struct FwdCfg {
@@ -1086,9 +1088,9 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // Rounding dS to bf16 puts as much error into dK and dQ as their own rounding (2.4e-3 of both against float64, 1.7e-3
 // without).  Where few elements carry a row, the total varies most: so an edge tile's dS, and short documents have no other tiles,
 // is multiplied as the sum of two bf16s, the rounded value and what the rounding left, which has room in the chunk's own
-// columns: their dK and dQ are as exact as float32 arithmetic rounded once, for 9 % of the backward where most tiles are
-// edges (23 packed texts: 102 us, 93 without) and 2 % in a long text.  One loop issues both terms: a second copy of
-// the products' code makes their issuer spill (8192 unmasked tokens at hd 128: 1574 us against 1317).
+// columns: their dK and dQ (without a cap: 1 − tanh² has 11 bits) are as exact as float32 arithmetic rounded once, for 9 % of
+// the backward where most tiles are edges (23 packed texts: 102 us, 93 without) and 2 % in a long text.  One loop issues both
+// terms: a second copy of the products' code makes their issuer spill (8192 unmasked tokens at hd 128: 1574 us against 1317).
 //
 // A tile's time is the rows' chain of tensor-memory loads, exponentials, stores and barriers, several times the
 // work in it, so two chains run side by side: each half of a tile's 128 columns has its own MMA issuer, four row
@@ -1101,7 +1103,9 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
 // both passes: 900 us, 573 TFLOP/s of the formulas' five products and 917 of the eight that run, 0.48 of measured; one
 // chain of whole tiles instead of two took 8 % more), at hd 128 the products beside it (1317 us, 782 and 1252 TFLOP/s,
 // 0.66 of measured).  Packed short texts pay for the parts of tiles that their masks hide, and some 4000 cycles per item
-// for D₀, the last products' arrival and the epilogue, where a tile takes 2100 (hd 64) to 2900 (hd 128).
+// for D₀, the last products' arrival and the epilogue, where an unmasked tile takes 2100 (hd 64) to 2900 (hd 128): together
+// three quarters of the time of 23 packed texts and half that of 40 capped ones, the rest being what edge tiles (masks, two
+// terms of dS) and caps take on top.
 constexpr int kThreadsBwd = 384;  // warps 0 TMA, 1 (and 2) MMA, 4–7 and 8–11 the halves' rows
 constexpr uint32_t kBwdRegsCtl = 88, kBwdRegsRows = 208;  // 128·88 + 256·208 = 384·168; at 72 the query pass's issuer
 // spills at hd 128 (8192 unmasked tokens: 1383 us against 1300), where the forward's does not (above)

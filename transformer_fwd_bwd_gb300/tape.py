@@ -385,7 +385,8 @@ def rope_axes(x: Var, pos: torch.Tensor, sections, H: int, hd: int, base: float 
 def attention_masked(q: Var, k: Var, v: Var, plan: torch.Tensor, H: int, Hkv: int, hd: int, scale=None, cap: float = 0.0,
                      slopes=None) -> Var:
     """Fused attention over packed documents on bf16 rows: q [T, H·hd], k and v [T, Hkv·hd], plan from
-    xt_attention_plan (what each token sees); cap and slopes as in xt_attention_masked_fwd."""
+    xt_attention_plan (what each token sees), which backward() reads again: it is not to be made for another batch before
+    then; cap and slopes as in xt_attention_masked_fwd."""
     T = q.value.shape[0]
     o = _empty_like(q.value)
     lse = torch.empty((H, T), dtype=_F32, device=q.value.device)

@@ -578,7 +578,7 @@ def _ints(t, n, name):
 
 def xt_attention_plan(plan, T, n_docs, doc_off=None, doc_len=None, prefix=None, causal=1, s=None):
     """The plan of a batch of T tokens in n_docs documents: doc_off int32 [n_docs + 1] (None: equal spans),
-    doc_len and prefix int32 [n_docs] or None."""
+    doc_len and prefix int32 [n_docs] or None.  The backward reads the plan too: a buffer is filled anew only behind it."""
     call("xt_attention_plan", int(T), int(n_docs), _ints(doc_off, n_docs + 1, "doc_off"), _ints(doc_len, n_docs, "doc_len"),
          _ints(prefix, n_docs, "prefix"), int(causal), ptr(plan), plan.numel() * plan.element_size(), stream(s))
 
