@@ -237,7 +237,7 @@ int xt_rope_bwd(const void* d, void* dx, const float* table, int B, int S, int H
  * pairs i = 0 .. hd/2 − 1 belong to the axes in order.  θ = pos[axis(i)][t]·f_i with
  * f_i = base^(−2i/hd) (per_axis = 0), or base^(−k/sections[a]) for pair k of axis a (per_axis = 1);
  * the rotation and its backward are xt_rope_fwd's.  Angles are reduced exactly (integer arithmetic
- * modulo a turn), so any int32 position is as accurate as position 0.  Token t, head h lives at
+ * modulo a turn), so any int32 position is as accurate as position 0 (base >= 1).  Token t, head h lives at
  * x + t·ld_x + h·hd (y + t·ld_y + h·hd); x and y may be one buffer with one stride (in place), except
  * with acc = 1.  hd even and at most 256 (else XT_ERR_INVALID_ARG / XT_ERR_UNSUPPORTED). */
 int xt_rope_axes_fwd(const void* x, int64_t ld_x, void* y, int64_t ld_y, const int32_t* pos, int n_axes,
