@@ -257,17 +257,17 @@ def _logprobs_own(s):
     R, k = c["R"], c["top"]
     if "logp" not in s:  # the buffers that a program keeps over its steps
         new = lambda *shape, dt=F32: torch.empty(*shape, dtype=dt, device="cuda")  # noqa: E731
-        s["logp"], s["entropy"], s["lse"] = new(R), new(R), new(R)
+        s["logp"], s["entropy"], s["stats"] = new(R), new(R), new(R, 2)
         s["top_logp"], s["top_ids"] = (new(R, k), new(R, k, dt=torch.int32)) if k else (None, None)
         if c["train"]:
             s["dlogits"] = torch.empty_like(s["logits"])
-    xt.xt_token_logprobs_fwd(s["logits"], s["tokens"], s["logp"], s["entropy"], s["lse"], s["top_logp"], s["top_ids"],
-                             scale=c["scale"])
+    xt.xt_token_logprobs_fwd(s["logits"], s["tokens"], s["logp"], s["entropy"], s["stats"], s["top_logp"],
+                             s["top_ids"], scale=c["scale"])
     out = {"logp": s["logp"], "entropy": s["entropy"]}
     if k:
         out["top_logp"], out["top_ids"] = s["top_logp"], s["top_ids"]
     if c["train"]:
-        xt.xt_token_logprobs_bwd(s["logits"], s["tokens"], s["lse"], s["entropy"], s["d_logp"], s["d_entropy"],
+        xt.xt_token_logprobs_bwd(s["logits"], s["tokens"], s["stats"], s["entropy"], s["d_logp"], s["d_entropy"],
                                  s["dlogits"], scale=c["scale"])
         out["dlogits"] = s["dlogits"]
     return out
