@@ -62,7 +62,7 @@ typedef enum { XT_F32 = 0, XT_BF16 = 1 } xt_dtype;
 /* device error flag bits */
 #define XT_DEVERR_INDEX 1u   /* a token id or target outside [0, V) */
 #define XT_DEVERR_TIMEOUT 2u /* a bounded mbarrier wait in a GEMM gave up */
-#define XT_DEVERR_PLAN 4u    /* masked attention was given a plan that was not made for its T */
+#define XT_DEVERR_PLAN 4u    /* masked attention (or the sorted embedding gradient) was given a plan made for other sizes */
 
 const char* xt_last_error(void);
 const char* xt_version(void);
@@ -392,6 +392,33 @@ int xt_cross_entropy_bwd(const void* logits, const int32_t* targets, const float
                          int dt_grad, int acc, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * Log probabilities of given tokens, with each row's entropy and its most probable tokens: what a loss on the
+ * tokens' own probabilities (a policy gradient, a distillation, scoring) needs where the mean cross-entropy does
+ * not do.  Per row r, z = scale·x[r] (scale: 1 / temperature), p = softmax(z):
+ *   logp[r] = log p[tokens[r]],   entropy[r] = −Σ_v p_v log p_v,
+ *   top_logp[r][0..top), top_ids[r][0..top): the largest logits in falling order, equal ones by rising id, and
+ *   their log p (top ≤ 32 and ≤ V; 0: none, pointers ignored);
+ *   stats[r] = {max x, ln Σ exp(z − scale·max x)}, for the backward.
+ * Backward, from d_logp and d_entropy (float32 [rows]; either may be NULL: nought):
+ *   dx_v (+)= scale·(d_logp·([v = token] − p_v) − d_entropy·p_v·(log p_v + entropy)).
+ * A row whose d_logp and d_entropy are both 0 gets zeros whatever it holds (padding).
+ * entropy and stats may be NULL in the forward; the backward needs stats, and entropy where d_entropy is given.
+ * Logits of −∞ (banned tokens) have p = 0 and gradient 0; a row that holds a NaN or +∞, or nothing but −∞, has no
+ * distribution: NaN in all its values, −1 as its ids.  Any finite logits are allowed, those of the type's lowest
+ * value among them.  A token outside [0, V) sets XT_DEVERR_INDEX and makes logp and the gradient of its row NaN.
+ * Layout: row r of logits at logits + r·ld (ld ≥ V), dlogits likewise with ld_d; dlogits may be logits (one dtype
+ * and stride, acc = 0).  Any alignment of the element type; rows of aligned 16 bytes need no more than that.
+ * scale in [1e-6, 1e6].  Entropies are accurate to about 1e-6 absolute.  Deterministic.
+ * ------------------------------------------------------------------------------- */
+int xt_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens, float scale, int top, float* logp,
+                          float* entropy, float* stats, float* top_logp, int32_t* top_ids, int64_t rows, int64_t V,
+                          int dt, void* stream);
+int xt_token_logprobs_bwd(const void* logits, int64_t ld, const int32_t* tokens, const float* stats,
+                          const float* entropy, const float* d_logp, const float* d_entropy, float scale,
+                          void* dlogits, int64_t ld_d, int64_t rows, int64_t V, int dt, int dt_grad, int acc,
+                          void* stream);
+
+/* ---------------------------------------------------------------------------------
  * Inverted dropout with a counter-based mask ([DO] § RNG：counter-based, § dropout 节点的
  * backward): for flat element index i (uint64),
  *   key = seed ⊕ (i·0x9E3779B97F4A7C15), h = splitmix64(key), u = (h>>40)·2⁻²⁴ (float32),
@@ -448,6 +475,25 @@ int xt_embedding_fwd(const int32_t* ids, const void* E, const void* P, void* h, 
 int xt_embedding_bwd(const int32_t* ids, const void* dh, void* dE, void* dP, int64_t T, int S,
                      int64_t d, int64_t V, int dt_dh, int dt_grad, void* ws, int acc,
                      void* stream);
+
+/* Embedding lookup with a scale and its gradient by sorted tokens, for any number of tokens T < 2³⁰:
+ *   h[t] = scale·E[ids[t]],   dE[v] (+)= scale·Σ_{t: ids[t]=v} dh[t]   (float32 sums, a fixed order: deterministic).
+ * xt_embedding_plan sorts a batch's ids once into plan (xt_embedding_plan_size bytes, 16-byte aligned): every table
+ * that the batch looks up, and every backward of it, can use that plan.  With acc = 0 rows of dE that no token touches
+ * are zeroed.  An id outside [0, V) sets XT_DEVERR_INDEX, its row of h is NaN and its row of dh is left out.  A plan
+ * made for another T or V sets XT_DEVERR_PLAN and the backward writes nothing.  The workspace
+ * (xt_embedding_sorted_bwd_workspace_size, 16-byte aligned) holds the shares of ids whose tokens are summed in several
+ * pieces; its contents on entry do not matter.  dh, dE, the plan and the workspace must not overlap.  E and h, and dh
+ * and dE, may have different dtypes; rows are contiguous, any d (multiples of 8 in 16-byte aligned buffers run on
+ * 16-byte accesses). */
+int xt_embedding_lookup_fwd(const int32_t* ids, const void* E, void* h, int64_t T, int64_t d, int64_t V, float scale,
+                            int dt_e, int dt_h, void* stream);
+int xt_embedding_plan_size(int64_t T, size_t* bytes);
+int xt_embedding_plan(const int32_t* ids, int64_t T, int64_t V, void* plan, size_t plan_bytes, void* stream);
+int xt_embedding_sorted_bwd_workspace_size(int64_t T, int64_t d, size_t* bytes);
+int xt_embedding_sorted_bwd(const void* plan, size_t plan_bytes, const void* dh, void* dE, int64_t T, int64_t d,
+                            int64_t V, float scale, int dt_dh, int dt_grad, int acc, void* ws, size_t ws_bytes,
+                            void* stream);
 
 /* ---------------------------------------------------------------------------------
  * Matmul on the tensor cores ([AE] op table row matmul: C = A@B; dA = d@Bᵀ, dB = Aᵀ@d).

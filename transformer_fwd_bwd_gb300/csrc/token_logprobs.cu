@@ -1,0 +1,655 @@
+// Log probabilities of given tokens, the entropy of each row's distribution and its most probable tokens, with the
+// gradient of the first two.  Per row, with z = scale·x:
+//   M = max x,  S = Σ_v exp(z_v − scale·M),  log p_v = z_v − scale·M − ln S,
+//   logp = log p_token,  H = −Σ_v p_v log p_v = ln S − Σ_v p_v (z_v − scale·M),
+//   dx_v = scale·(dlogp·([v = token] − p_v) − dH·p_v·(log p_v + H)).
+//
+// Forward.  One pass over the logits.  A thread keeps the sums Σ 2^t and Σ t·2^t of its elements, t = x·scale·log2(e) − b,
+// against a base b of its own: the largest t of the first elements it saw, moved only where a later one lies more than
+// kHeadroom above it (2^t has room for that in float32, so that almost no element pays for a rescaling, and
+// Σ t·2^t / Σ 2^t loses at most kHeadroom·2⁻²⁴).  The threads' sums meet at the largest base.  What this path cannot hold (a largest logit beyond
+// 2⁻¹·FLT_MAX in t, below −1e30, or no finite sum) is done over by row_safe(), two passes with differences taken first.
+//
+// The most probable tokens cost one comparison per 16 bytes in that pass: each thread keeps its largest element (the
+// value and the vector it lies in).  The k-th largest of the threads' maxima bounds the k-th largest element from below,
+// and the elements above it lie with the k threads whose maxima reach it, so only those threads' vectors are read again
+// (from L2: k/256 of the row) and their elements at or above the bound are put in order.  Elements are ordered by
+// (value, lower index first) throughout, so that ties have one answer, and no step depends on the data's order.
+//
+// Bound by HBM: a logit is read once (backward: read and written).  Measured times stand beside the launches.
+#include <cfloat>
+
+#include "internal.cuh"
+
+namespace xt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTop = 32;          // a list lives in one warp, an entry per lane
+constexpr float kHeadroom = 8.f;     // log2 units
+constexpr float kLowest = -200.f;    // 2^kLowest is 0 in float32, and 0·kLowest stays 0 where 0·(−∞) would not
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// max that keeps NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// 16 bytes of logits: the float values and their maximum (NaN ignored).
+template <typename T> struct Chunk;
+template <> struct Chunk<float> {
+  static constexpr int W = 4;
+  __device__ __forceinline__ static void values(const uint4& q, float (&x)[4]) {
+    x[0] = __uint_as_float(q.x); x[1] = __uint_as_float(q.y); x[2] = __uint_as_float(q.z); x[3] = __uint_as_float(q.w);
+  }
+  __device__ __forceinline__ static float top(const uint4& q) {
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+};
+template <> struct Chunk<bf16> {
+  static constexpr int W = 8;
+  __device__ __forceinline__ static void values(const uint4& q, float (&x)[8]) { Vec<bf16>::unpack(q, x); }
+  __device__ __forceinline__ static float top(const uint4& q) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+// A row as 16-byte vectors: `head` elements before the first 16-byte boundary, `full` whole vectors, then the tail.
+// Vectors are numbered 0 (head), 1 .. full, full + 1 (tail); element e of whole vector j is head + (j − 1)·W + e.
+template <typename T>
+struct Row {
+  const T* x;
+  int64_t V;
+  int head;
+  int64_t full;
+  __device__ __forceinline__ Row(const T* p, int64_t V_) : x(p), V(V_) {
+    const int64_t h = int64_t((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int64_t(sizeof(T));
+    head = int(h < V ? h : V);
+    full = (V - head) / Chunk<T>::W;
+  }
+  __device__ __forceinline__ const T* vector(int64_t j) const { return x + head + (j - 1) * Chunk<T>::W; }
+  // first element of vector j and one past its last
+  __device__ __forceinline__ int64_t first(int64_t j) const { return j == 0 ? 0 : head + (j - 1) * Chunk<T>::W; }
+  __device__ __forceinline__ int64_t last(int64_t j) const {
+    return j == 0 ? head : j <= full ? head + j * Chunk<T>::W : V;
+  }
+};
+
+struct Sums {
+  float b;         // base of the exponents, log2 units
+  uint64_t s, w;   // Σ 2^t and Σ t·2^t, two partial sums each
+  float top;       // largest element
+  uint32_t at;     // the first vector that holds it
+};
+
+__device__ __forceinline__ void rebase(Sums& a, float nb) {
+  const float d = fmaxf(a.b - nb, kLowest), r = ex2(d);
+  float s0, s1, w0, w1;
+  f32x2_unpack(a.s, s0, s1);
+  f32x2_unpack(a.w, w0, w1);
+  a.w = f32x2_pack(r * fmaf(d, s0, w0), r * fmaf(d, s1, w1));
+  a.s = f32x2_pack(r * s0, r * s1);
+  a.b = nb;
+}
+
+template <int N>
+__device__ __forceinline__ void consume(Sums& a, const float (&x)[N], float top, uint32_t j, float c) {
+  const bool more = top > a.top;
+  a.top = more ? top : a.top;
+  a.at = more ? j : a.at;
+  if (top * c > a.b + kHeadroom) rebase(a, top * c);
+  const uint64_t cc = f32x2_pack(c, c), nb = f32x2_pack(-a.b, -a.b);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float t0, t1;
+    f32x2_unpack(f32x2_fma(f32x2_pack(x[i], x[i + 1]), cc, nb), t0, t1);
+    t0 = max_nan(t0, kLowest);
+    t1 = max_nan(t1, kLowest);
+    const uint64_t e = f32x2_pack(ex2(t0), ex2(t1));
+    a.s = f32x2_add(a.s, e);
+    a.w = f32x2_fma(e, f32x2_pack(t0, t1), a.w);
+  }
+}
+
+// ------------------------------------------------------------------------------ lists of the most probable
+// An element's place in the order: larger values first, among equal ones the lower number.  0 stands for none.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);  // −0 as +0
+  return v != v ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order(float v, uint32_t number) {
+  const uint32_t k = order_key(v);
+  return k ? (uint64_t(k) << 32) | uint32_t(~number) : 0ull;
+}
+
+// The warp's 32 entries in falling order (bitonic network).
+__device__ __forceinline__ uint64_t sort_warp(uint64_t v, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2) {
+      const uint64_t o = __shfl_xor_sync(0xffffffffu, v, j);
+      const bool up = (lane & k) != 0 && k < 32, lower = (lane & j) != 0;
+      v = (v > o) == (up == lower) ? v : o;
+    }
+  return v;
+}
+// The 32 largest of two lists in falling order, in falling order.
+__device__ __forceinline__ uint64_t merge_warp(uint64_t a, uint64_t b, int lane) {
+  b = __shfl_sync(0xffffffffu, b, 31 - lane);
+  uint64_t v = a > b ? a : b;
+#pragma unroll
+  for (int j = 16; j > 0; j /= 2) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, v, j);
+    v = (v > o) == ((lane & j) == 0) ? v : o;
+  }
+  return v;
+}
+__device__ __forceinline__ uint64_t insert_warp(uint64_t list, uint64_t c, int lane) {
+  const int pos = __popc(__ballot_sync(0xffffffffu, list > c));
+  const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+  return lane < pos ? list : lane == pos ? c : up;
+}
+
+// Puts the elements of vector j (held by this lane; none where j < 0) at or above `bound` into the warp's list.
+template <typename T>
+__device__ __forceinline__ uint64_t collect(uint64_t list, const Row<T>& row, int64_t j, uint64_t bound, int lane) {
+  constexpr int W = Chunk<T>::W;
+  float x[W];
+  int64_t e0 = 0;
+  int n = 0;
+  if (j >= 0) {
+    e0 = row.first(j);
+    n = int(row.last(j) - e0);
+    if (n == W && j > 0) {
+      Chunk<T>::values(*reinterpret_cast<const uint4*>(row.vector(j)), x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = i < n ? to_f(row.x[e0 + i]) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    uint64_t c = 0;
+    if (i < n && order(x[i], uint32_t(j)) >= bound) c = order(x[i], uint32_t(e0 + i));
+    uint32_t some = __ballot_sync(0xffffffffu, c != 0);
+    while (some) {
+      const int from = __ffs(some) - 1;
+      some &= some - 1;
+      list = insert_warp(list, __shfl_sync(0xffffffffu, c, from), lane);
+    }
+  }
+  return list;
+}
+
+struct Fwd {
+  const void* x;
+  int64_t ld, rows, V;
+  const int32_t* tokens;
+  float scale, c;   // c = scale·log2(e)
+  int top;
+  float *logp, *entropy, *stats, *top_logp;
+  int32_t* top_ids;
+  uint32_t* flag;
+};
+
+// The row's results from M, log2 Σ 2^(c(x − M)) and −Σ p·c(x − M) (log2 units): one thread.
+template <typename T>
+__device__ __forceinline__ void write_row(const Fwd& a, const T* x, int64_t r, float M, double log2s, double mean) {
+  const bool ok = isfinite(M) && isfinite(log2s) && isfinite(mean);
+  const float nan = __int_as_float(0x7fc00000);
+  const double ln2 = 0.69314718055994530942;
+  const int32_t t = a.tokens[r];
+  const bool valid = t >= 0 && t < a.V;
+  if (!valid) flag_error(a.flag, XT_DEVERR_INDEX);
+  const double z = valid ? (double(to_f(x[t])) - double(M)) * double(a.scale) : 0.0;
+  a.logp[r] = ok && valid ? float(z - log2s * ln2) : nan;
+  if (a.entropy) a.entropy[r] = ok ? float(fmax((log2s - mean) * ln2, 0.0)) : nan;
+  if (a.stats) {
+    a.stats[2 * r] = ok ? M : nan;
+    a.stats[2 * r + 1] = ok ? float(log2s * ln2) : nan;
+  }
+}
+// The list's entries: one lane each.
+template <typename T>
+__device__ __forceinline__ void write_top(const Fwd& a, const T* x, int64_t r, uint64_t list, int lane, float M,
+                                          double log2s) {
+  if (lane >= a.top) return;
+  const bool ok = isfinite(M) && isfinite(log2s);
+  const int32_t id = int32_t(~uint32_t(list));
+  const double z = ok ? (double(to_f(x[id])) - double(M)) * double(a.scale) - log2s * 0.69314718055994530942 : 0.0;
+  a.top_logp[r * a.top + lane] = ok ? float(z) : __int_as_float(0x7fc00000);
+  a.top_ids[r * a.top + lane] = ok ? id : -1;
+}
+
+// The sums of one row by one warp, differences taken before they are scaled, double sums: any finite logits.
+template <typename T>
+__device__ __noinline__ void row_safe(const T* x, int64_t V, float scale, int lane, float& M, double& log2s,
+                                      double& mean) {
+  float m = -INFINITY;
+  for (int64_t v = lane; v < V; v += 32) m = max_nan(m, to_f(x[v]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  double s = 0, w = 0;
+  for (int64_t v = lane; v < V; v += 32) {
+    const float t = max_nan(float((double(to_f(x[v])) - double(m)) * double(scale)) * kLog2e, kLowest);
+    const float e = exp2f(t);
+    s += double(e);
+    w += double(e) * double(t);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    w += __shfl_xor_sync(0xffffffffu, w, o);
+  }
+  M = m;
+  log2s = log2(s);
+  mean = w / s;
+}
+
+// Sums over the warp at its largest base.
+__device__ __forceinline__ void warp_join(float& b, float& s, float& w) {
+  const float B = warp_max(b), d = fmaxf(b - B, kLowest), r = ex2(d);
+  w = warp_sum(r * fmaf(d, s, w));
+  s = warp_sum(r * s);
+  b = B;
+}
+
+// WARP: a warp to a row (short rows); else a CTA, or with gridDim.x a multiple of the cluster size a cluster of CTAs
+// that share the row's vectors out in ranges and join in the first one's shared memory.
+template <typename T, bool TOP, bool WARP>
+__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ Fwd a) {
+  constexpr int W = Chunk<T>::W;
+  constexpr int kUnroll = 4;
+  constexpr int NT = WARP ? 32 : kThreads;  // threads that share the vectors
+  constexpr int kMaxCluster = 8;
+  __shared__ float part[3][kMaxCluster * kWarps];  // base, Σ, Σ t of every warp of the cluster (in its first CTA)
+  __shared__ float part_top[kMaxCluster * kWarps];
+  __shared__ uint64_t lists[TOP && !WARP ? kMaxCluster * kWarps : 1][TOP && !WARP ? 32 : 1];
+  __shared__ uint64_t chosen[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = WARP ? lane : int(threadIdx.x);
+  uint32_t rank = 0, cl = 1;
+  if (!WARP) {
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
+  }
+  pdl_begin();
+  const int64_t r = WARP ? int64_t(blockIdx.x) * kWarps + warp : int64_t(blockIdx.x) / cl;
+  if (WARP && r >= a.rows) return;
+  const T* x = static_cast<const T*>(a.x) + r * a.ld;
+  const Row<T> row(x, a.V);
+  // this CTA's whole vectors: (lo, hi], numbers 1 .. full
+  const int64_t lo = WARP ? 0 : row.full * rank / cl, hi = WARP ? row.full : row.full * (rank + 1) / cl;
+
+  Sums m{-1e30f, 0ull, 0ull, -INFINITY, uint32_t(lo + 1 + tid)};
+  bool any = lo + tid < hi;
+  const T* p = row.vector(lo + 1 + tid);
+  int64_t j = lo + 1 + tid;
+  for (; j + (kUnroll - 1) * NT <= hi; j += kUnroll * NT, p += kUnroll * NT * W) {
+    uint4 q[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) q[u] = load_stream(p + u * NT * W);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float v[W];
+      Chunk<T>::values(q[u], v);
+      consume<W>(m, v, Chunk<T>::top(q[u]), uint32_t(j + u * NT), a.c);
+    }
+  }
+  for (; j <= hi; j += NT, p += NT * W) {
+    const uint4 q = load_stream(p);
+    float v[W];
+    Chunk<T>::values(q, v);
+    consume<W>(m, v, Chunk<T>::top(q), uint32_t(j), a.c);
+  }
+  // the elements beside the whole vectors: the head with thread 0 of the first CTA, the tail with the last thread of
+  // the last one (whose vectors they follow, so that the first of equal values is kept)
+  const int64_t tail = row.full + 1;
+  const bool has_head = rank == 0 && tid == 0 && row.head > 0;
+  const bool has_tail = rank == cl - 1 && tid == NT - 1 && row.first(tail) < a.V;
+  if (has_head || has_tail) {
+    const int64_t k = has_head ? 0 : tail;
+    float v[W], top = -INFINITY;
+    const int64_t e0 = row.first(k);
+    const int n = int(row.last(k) - e0);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      v[i] = i < n ? to_f(x[e0 + i]) : -INFINITY;
+      top = fmaxf(top, v[i]);
+    }
+    if (!any || (has_head && top >= m.top)) {  // the head comes before what the thread has seen
+      m.top = -INFINITY;
+      m.at = uint32_t(k);
+    }
+    any = true;
+    consume<W>(m, v, top, uint32_t(k), a.c);
+  }
+
+  float b = m.b, s0, s1, w0, w1;
+  f32x2_unpack(m.s, s0, s1);
+  f32x2_unpack(m.w, w0, w1);
+  float s = s0 + s1, w = w0 + w1, M = warp_max(m.top);
+  warp_join(b, s, w);
+  uint64_t list = 0;
+  uint64_t best = TOP && any ? order(m.top, m.at) : 0ull;
+
+  if constexpr (WARP) {
+    double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
+    double mean = double(w / s) + (double(b) - double(M) * double(a.c));
+    if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
+    if (lane == 0) write_row(a, x, r, M, log2s, mean);
+    if constexpr (TOP) {
+      const uint64_t bound = __shfl_sync(0xffffffffu, sort_warp(best, lane), a.top - 1);
+      // vectors are few here: all of them are looked through
+      for (int64_t j0 = 0; j0 <= tail; j0 += 32) {
+        const int64_t jj = j0 + lane;
+        list = collect(list, row, jj <= tail ? jj : -1, bound, lane);
+      }
+      write_top(a, x, r, list, lane, M, log2s);
+    }
+    return;
+  }
+
+  // ---- the CTA's most probable elements
+  if constexpr (TOP) {
+    const uint64_t sorted = sort_warp(best, lane);
+    lists[warp][lane] = sorted;
+    __syncthreads();
+    if (warp == 0) {
+      uint64_t v = sorted;
+#pragma unroll 1
+      for (int k = 1; k < kWarps; ++k) v = merge_warp(v, lists[k][lane], lane);
+      chosen[lane] = v;
+    }
+    __syncthreads();
+    const uint64_t bound = chosen[a.top - 1];
+    // a warp to a chosen thread: its vectors are the number that its maximum lies in, modulo kThreads
+    for (int k = warp; k < a.top; k += kWarps) {
+      const uint64_t ch = chosen[k];
+      if (ch == 0) break;
+      const int64_t at = int64_t(~uint32_t(ch));
+      int owner;
+      if (at == 0) owner = 0;
+      else if (at == tail) owner = kThreads - 1;
+      else owner = int((at - 1 - lo) % kThreads);
+      for (int64_t j0 = lo + 1 + owner; j0 <= hi; j0 += int64_t(32) * kThreads) {
+        const int64_t jj = j0 + int64_t(lane) * kThreads;
+        list = collect(list, row, jj <= hi ? jj : -1, bound, lane);
+      }
+      if (owner == 0 && rank == 0 && row.head > 0) list = collect(list, row, lane == 0 ? 0 : -1, bound, lane);
+      if (owner == kThreads - 1 && rank == cl - 1 && row.first(tail) < a.V)
+        list = collect(list, row, lane == 0 ? tail : -1, bound, lane);
+    }
+    __syncthreads();  // lists are free again
+  }
+
+  // ---- the warps' sums and lists meet in the first CTA of the cluster
+  const int slot = int(rank) * kWarps + warp;
+  if (cl > 1) {
+    // every CTA of the cluster runs, and the first one's warps are past the lists of their own
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    auto at0 = [](const void* p) {
+      uint32_t d;
+      asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(d) : "r"(uint32_t(__cvta_generic_to_shared(p))));
+      return d;
+    };
+    if (lane == 0) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at0(&part[0][slot])), "f"(b) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at0(&part[1][slot])), "f"(s) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at0(&part[2][slot])), "f"(w) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at0(&part_top[slot])), "f"(M) : "memory");
+    }
+    if constexpr (TOP) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at0(&lists[slot][lane])), "l"(list) : "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (rank != 0) return;
+  } else {
+    if (lane == 0) {
+      part[0][slot] = b;
+      part[1][slot] = s;
+      part[2][slot] = w;
+      part_top[slot] = M;
+    }
+    if constexpr (TOP) lists[slot][lane] = list;
+    __syncthreads();
+  }
+  if (warp != 0) return;
+  const int n = int(cl) * kWarps;  // ≤ 64: two slots to a lane, joined in slot order by the shuffles' fixed tree
+  b = lane < n ? part[0][lane] : -1e30f;
+  s = lane < n ? part[1][lane] : 0.f;
+  w = lane < n ? part[2][lane] : 0.f;
+  M = lane < n ? part_top[lane] : -INFINITY;
+  if (lane + 32 < n) {
+    const float b2 = part[0][lane + 32], s2 = part[1][lane + 32], w2 = part[2][lane + 32];
+    const float B = fmaxf(b, b2), d1 = fmaxf(b - B, kLowest), d2 = fmaxf(b2 - B, kLowest);
+    w = ex2(d1) * fmaf(d1, s, w) + ex2(d2) * fmaf(d2, s2, w2);
+    s = ex2(d1) * s + ex2(d2) * s2;
+    b = B;
+    M = fmaxf(M, part_top[lane + 32]);
+  }
+  M = warp_max(M);
+  warp_join(b, s, w);
+  double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
+  double mean = double(w / s) + (double(b) - double(M) * double(a.c));
+  if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
+  if (lane == 0) write_row(a, x, r, M, log2s, mean);
+  if constexpr (TOP) {
+    list = lists[0][lane];
+#pragma unroll 1
+    for (int k = 1; k < n; ++k) list = merge_warp(list, lists[k][lane], lane);
+    write_top(a, x, r, list, lane, M, log2s);
+  }
+}
+
+// ------------------------------------------------------------------------------ backward
+
+struct Bwd {
+  const void* x;
+  int64_t ld;
+  const int32_t* tokens;
+  const float *stats, *entropy, *d_logp, *d_entropy;
+  float scale, c;
+  void* dx;
+  int64_t ld_d, rows, V;
+  int64_t segs;     // pieces of a row, kSegVectors vectors for each lane
+  int acc;
+  uint32_t* flag;
+};
+constexpr int kSegVectors = 4;
+
+// A warp to kSegVectors·32 vectors of a row: dx = p·(A + B·t) (+ scale·dlogp at the token), t = log2 p.
+template <typename T, typename TG>
+__global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(const __grid_constant__ Bwd a) {
+  constexpr int W = Chunk<T>::W;
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t r = unit / a.segs, seg = unit - r * a.segs;
+  if (r >= a.rows) return;
+  const T* x = static_cast<const T*>(a.x) + r * a.ld;
+  TG* dx = static_cast<TG*>(a.dx) + r * a.ld_d;
+  const Row<T> row(x, a.V);
+  const int64_t tail = row.full + 1;
+  const int64_t j0 = seg * (kSegVectors * 32);
+  // 16-byte stores where the gradient's vectors are aligned as the logits' are
+  const bool vec = ((reinterpret_cast<uintptr_t>(dx) + size_t(row.head) * sizeof(TG)) & 15) == 0;
+  uint4 q[kSegVectors];
+#pragma unroll
+  for (int u = 0; u < kSegVectors; ++u) {
+    const int64_t j = j0 + u * 32 + lane;
+    if (j >= 1 && j <= row.full) q[u] = *reinterpret_cast<const uint4*>(row.vector(j));
+  }
+  const float dl = a.d_logp ? __ldg(a.d_logp + r) : 0.f, dh = a.d_entropy ? __ldg(a.d_entropy + r) : 0.f;
+  const int32_t t = __ldg(a.tokens + r);
+  const bool valid = t >= 0 && t < a.V;
+  if (!valid && seg == 0 && lane == 0) flag_error(a.flag, XT_DEVERR_INDEX);
+  const bool none = dl == 0.f && dh == 0.f;  // zeros, whatever the row holds
+  const float M = __ldg(a.stats + 2 * r), L = __ldg(a.stats + 2 * r + 1) * kLog2e;
+  const float H = dh != 0.f ? __ldg(a.entropy + r) : 0.f;
+  const float A = valid ? -a.scale * fmaf(dh, H, dl) : __int_as_float(0x7fc00000);
+  const float B = -a.scale * dh * 0.6931471805599453f;
+  const float hit = a.scale * dl;
+#pragma unroll
+  for (int u = 0; u < kSegVectors; ++u) {
+    const int64_t j = j0 + u * 32 + lane;
+    if (j > tail) continue;
+    const int64_t e0 = row.first(j);
+    const int n = int(row.last(j) - e0);
+    const bool whole = j >= 1 && j <= row.full;
+    float v[W];
+    if (whole) {
+      Chunk<T>::values(q[u], v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = i < n ? to_f(x[e0 + i]) : 0.f;
+    }
+    const int64_t rel = int64_t(t) - e0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float y = max_nan(fmaf(v[i] - M, a.c, -L), kLowest);
+      float d = ex2(y) * fmaf(B, y, A);
+      d = rel == i ? d + hit : d;
+      v[i] = none ? 0.f : d;
+    }
+    TG* out = dx + e0;
+    if (whole && vec) {
+      constexpr int S = 16 / int(sizeof(TG)) < W ? 16 / int(sizeof(TG)) : W;  // elements to a store
+#pragma unroll
+      for (int k = 0; k < W; k += S) {
+        float o[S];
+        if (a.acc) {
+          if constexpr (S * sizeof(TG) == 16) Vec<TG>::load(out + k, o);
+          else
+#pragma unroll
+            for (int i = 0; i < S; ++i) o[i] = to_f(out[k + i]);
+#pragma unroll
+          for (int i = 0; i < S; ++i) o[i] += v[k + i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < S; ++i) o[i] = v[k + i];
+        }
+        if constexpr (S * sizeof(TG) == 16) Vec<TG>::store(out + k, o);
+        else
+#pragma unroll
+          for (int i = 0; i < S; ++i) out[k + i] = from_f<TG>(o[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < n) out[i] = from_f<TG>(a.acc ? to_f(out[i]) + v[i] : v[i]);
+    }
+  }
+}
+
+// Arguments that both calls check.
+int check_args(const char* fn, const void* x, int64_t ld, const int32_t* tokens, float scale, int64_t rows, int64_t V,
+               int dt) {
+  XT_REQUIRE(valid_dtype(dt), "%s: bad dtype", fn);
+  XT_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31) && V > 0 && V < (int64_t(1) << 30), "%s: bad sizes", fn);
+  XT_REQUIRE(ld >= V, "%s: row stride smaller than V", fn);
+  XT_REQUIRE(scale >= 1e-6f && scale <= 1e6f, "%s: scale must lie in [1e-6, 1e6]", fn);
+  if (rows == 0) return XT_OK;
+  XT_REQUIRE(x && tokens, "%s: NULL pointer", fn);
+  if (reinterpret_cast<uintptr_t>(x) % dtype_size(dt)) return fail(XT_ERR_ALIGNMENT, "%s: logits are not aligned to their type", fn);
+  return XT_OK;
+}
+
+}  // namespace
+}  // namespace xt
+
+using namespace xt;
+
+extern "C" {
+
+int xt_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens, float scale, int top, float* logp,
+                          float* entropy, float* stats, float* top_logp, int32_t* top_ids, int64_t rows, int64_t V,
+                          int dt, void* stream) {
+  const char* fn = "xt_token_logprobs_fwd";
+  XT_TRY(check_args(fn, logits, ld, tokens, scale, rows, V, dt));
+  XT_REQUIRE(top >= 0 && top <= V, "%s: top must lie in [0, V]", fn);
+  if (top > kMaxTop) return fail(XT_ERR_UNSUPPORTED, "%s: at most %d alternatives", fn, kMaxTop);
+  if (rows == 0) return XT_OK;
+  XT_REQUIRE(logp && (top == 0 || (top_logp && top_ids)), "%s: NULL pointer", fn);
+  Fwd a{logits, ld, rows, V, tokens, scale, scale * kLog2e, top, logp, entropy, stats, top_logp, top_ids, errflag()};
+  cudaStream_t s = as_stream(stream);
+  const int64_t bytes = V * int64_t(dtype_size(dt));
+  // Short rows go to a warp each; longer ones to a CTA, and where the rows are too few to fill the GPU to a cluster of
+  // CTAs, as long as each of them keeps 8 KB of the row.
+  const bool warp = bytes <= 4096;
+  int cl = 1;
+  while (!warp && cl < 8 && rows * cl * 2 <= int64_t(num_sms()) * 4 && bytes >= int64_t(cl) * 2 * 8192) cl *= 2;
+  const int64_t grid = warp ? ceil_div(rows, kWarps) : rows * cl;
+  if (grid >= (int64_t(1) << 31)) return fail(XT_ERR_UNSUPPORTED, "%s: too many rows", fn);
+#define XT_LOGPROBS(T_, TOP_)                                                                            \
+  do {                                                                                                   \
+    if (warp) launch(token_logprobs_kernel<T_, TOP_, true>, unsigned(grid), kThreads, 0, s, a);          \
+    else if (cl == 1) launch(token_logprobs_kernel<T_, TOP_, false>, unsigned(grid), kThreads, 0, s, a); \
+    else launch_clustered(token_logprobs_kernel<T_, TOP_, false>, unsigned(grid), kThreads, 0, s, cl, a); \
+  } while (0)
+  if (dt == XT_BF16) {
+    if (top) XT_LOGPROBS(bf16, true);
+    else XT_LOGPROBS(bf16, false);
+  } else {
+    if (top) XT_LOGPROBS(float, true);
+    else XT_LOGPROBS(float, false);
+  }
+#undef XT_LOGPROBS
+  return check_launch(fn);
+}
+
+int xt_token_logprobs_bwd(const void* logits, int64_t ld, const int32_t* tokens, const float* stats,
+                          const float* entropy, const float* d_logp, const float* d_entropy, float scale,
+                          void* dlogits, int64_t ld_d, int64_t rows, int64_t V, int dt, int dt_grad, int acc,
+                          void* stream) {
+  const char* fn = "xt_token_logprobs_bwd";
+  XT_TRY(check_args(fn, logits, ld, tokens, scale, rows, V, dt));
+  XT_REQUIRE(valid_dtype(dt_grad), "%s: bad gradient dtype", fn);
+  XT_REQUIRE(ld_d >= V, "%s: gradient's row stride smaller than V", fn);
+  XT_REQUIRE(acc == 0 || acc == 1, "%s: acc must be 0 or 1", fn);
+  if (rows == 0) return XT_OK;
+  XT_REQUIRE(stats && dlogits, "%s: NULL pointer", fn);
+  XT_REQUIRE(d_entropy == nullptr || entropy != nullptr, "%s: d_entropy needs the forward's entropy", fn);
+  XT_REQUIRE(logits != dlogits || (dt == dt_grad && ld == ld_d && !acc), "%s: in place needs one dtype and row stride, and acc = 0", fn);
+  if (reinterpret_cast<uintptr_t>(dlogits) % dtype_size(dt_grad))
+    return fail(XT_ERR_ALIGNMENT, "%s: dlogits are not aligned to their type", fn);
+  const int w = dt == XT_BF16 ? 8 : 4;
+  // whole vectors, the head and the tail (V/w + 2 numbers at most)
+  const int64_t segs = ceil_div(V / w + 2, kSegVectors * 32);
+  Bwd a{logits, ld, tokens, stats, entropy, d_logp, d_entropy, scale, scale * kLog2e, dlogits, ld_d, rows, V, segs, acc,
+        errflag()};
+  const int64_t grid = ceil_div(rows * segs, kWarps);
+  if (grid >= (int64_t(1) << 31)) return fail(XT_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  cudaStream_t s = as_stream(stream);
+  if (dt == XT_BF16) {
+    if (dt_grad == XT_BF16) launch(token_logprobs_bwd_kernel<bf16, bf16>, unsigned(grid), kThreads, 0, s, a);
+    else launch(token_logprobs_bwd_kernel<bf16, float>, unsigned(grid), kThreads, 0, s, a);
+  } else {
+    if (dt_grad == XT_BF16) launch(token_logprobs_bwd_kernel<float, bf16>, unsigned(grid), kThreads, 0, s, a);
+    else launch(token_logprobs_bwd_kernel<float, float>, unsigned(grid), kThreads, 0, s, a);
+  }
+  return check_launch(fn);
+}
+
+}  // extern "C"

@@ -149,6 +149,13 @@ _SIGS = {
     "xt_embedding_workspace_size": [_I64, _SZP],
     "xt_embedding_fwd": [_VP, _VP, _VP, _VP, _I64, _I, _I64, _I64, _I, _VP],
     "xt_embedding_bwd": [_VP, _VP, _VP, _VP, _I64, _I, _I64, _I64, _I, _I, _VP, _I, _VP],
+    "xt_token_logprobs_fwd": [_VP, _I64, _VP, _F, _I, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _VP],
+    "xt_token_logprobs_bwd": [_VP, _I64, _VP, _VP, _VP, _VP, _VP, _F, _VP, _I64, _I64, _I64, _I, _I, _I, _VP],
+    "xt_embedding_lookup_fwd": [_VP, _VP, _VP, _I64, _I64, _I64, _F, _I, _I, _VP],
+    "xt_embedding_plan_size": [_I64, _SZP],
+    "xt_embedding_plan": [_VP, _I64, _I64, _VP, C.c_size_t, _VP],
+    "xt_embedding_sorted_bwd_workspace_size": [_I64, _I64, _SZP],
+    "xt_embedding_sorted_bwd": [_VP, C.c_size_t, _VP, _VP, _I64, _I64, _I64, _F, _I, _I, _I, _VP, C.c_size_t, _VP],
     "xt_matmul_workspace_size": [C.POINTER(MatmulDesc), _SZP],
     "xt_gemm_set_schedule": [_I],
     "xt_gemm_set_pairing": [_I],
@@ -710,6 +717,92 @@ def xt_embedding_bwd(ids, dh, dE, dP, S, acc=0, ws=None, s=None):
         ws = workspace(ws_bytes("xt_embedding_workspace_size", T), dh.device, s=s)
     call("xt_embedding_bwd", ptr(ids), ptr(dh), ptr(dE), ptr(dP), T, S, d, V, dt(dh), dt(dE), ptr(ws), acc,
          stream(s))
+
+
+def _rows_of(x, name):
+    """Rows, columns and row stride of a [rows, cols] tensor with unit column stride."""
+    if x.dim() != 2 or (x.numel() and x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
+    rows, cols = x.shape
+    ld = x.stride(0) if rows > 1 else cols
+    return rows, cols, ld
+
+
+def _vector(t, shape, dtype, name):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+
+
+def xt_token_logprobs_fwd(logits, tokens, logp, entropy=None, stats=None, top_logp=None, top_ids=None, scale=1.0, s=None):
+    """log p of tokens[r] in row r of logits [rows, V] (rows may be strided), the rows' entropies, what the backward
+    needs (stats, float32 [rows, 2]) and the most probable tokens (top_logp float32, top_ids int32: [rows, top])."""
+    rows, V, ld = _rows_of(logits, "logits")
+    _vector(tokens, (rows,), torch.int32, "tokens")
+    _vector(logp, (rows,), torch.float32, "logp")
+    _vector(entropy, (rows,), torch.float32, "entropy")
+    _vector(stats, (rows, 2), torch.float32, "stats")
+    if (top_logp is None) != (top_ids is None):
+        raise ValueError("top_logp and top_ids go together")
+    top = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids must be [rows, top]")
+        top = top_ids.shape[1]
+        _vector(top_ids, (rows, top), torch.int32, "top_ids")
+        _vector(top_logp, (rows, top), torch.float32, "top_logp")
+    call("xt_token_logprobs_fwd", ptr(logits, False), ld, ptr(tokens), float(scale), top, ptr(logp), ptr(entropy),
+         ptr(stats), ptr(top_logp), ptr(top_ids), rows, V, dt(logits), stream(s))
+
+
+def xt_token_logprobs_bwd(logits, tokens, stats, entropy, d_logp, d_entropy, dlogits, scale=1.0, acc=0, s=None):
+    """Gradient of the logits from those of logp and entropy (either may be None; entropy only with d_entropy)."""
+    rows, V, ld = _rows_of(logits, "logits")
+    if tuple(dlogits.shape) != (rows, V):
+        raise ValueError("dlogits must have the logits' shape")
+    _, _, ld_d = _rows_of(dlogits, "dlogits")
+    _vector(tokens, (rows,), torch.int32, "tokens")
+    _vector(stats, (rows, 2), torch.float32, "stats")
+    for name, t in (("entropy", entropy), ("d_logp", d_logp), ("d_entropy", d_entropy)):
+        _vector(t, (rows,), torch.float32, name)
+    call("xt_token_logprobs_bwd", ptr(logits, False), ld, ptr(tokens), ptr(stats), ptr(entropy), ptr(d_logp),
+         ptr(d_entropy), float(scale), ptr(dlogits, False), ld_d, rows, V, dt(logits), dt(dlogits), int(acc), stream(s))
+
+
+def xt_embedding_lookup_fwd(ids, E, h, scale=1.0, s=None):
+    """h[t] = scale·E[ids[t]]; ids int32 of any shape, h its rows."""
+    V, d = E.shape
+    T = ids.numel()
+    if ids.dtype != torch.int32 or h.numel() != T * d or h.shape[-1] != d:
+        raise ValueError("ids must be int32 and h a row of E per id")
+    call("xt_embedding_lookup_fwd", ptr(ids), ptr(E), ptr(h), T, d, V, float(scale), dt(E), dt(h), stream(s))
+
+
+def embedding_plan_buffer(T, device="cuda"):
+    """Room for the plan of T tokens."""
+    return torch.empty(ws_bytes("xt_embedding_plan_size", int(T)), dtype=torch.uint8, device=device)
+
+
+def xt_embedding_plan(ids, V, plan, s=None):
+    """Sorts a batch's ids (int32) into plan, for xt_embedding_sorted_bwd."""
+    if ids.dtype != torch.int32:
+        raise ValueError("ids must be int32")
+    call("xt_embedding_plan", ptr(ids), ids.numel(), int(V), ptr(plan), plan.numel(), stream(s))
+
+
+def embedding_sorted_workspace(T, d, device="cuda", s=None):
+    return scratch(ws_bytes("xt_embedding_sorted_bwd_workspace_size", int(T), int(d)), device, s)
+
+
+def xt_embedding_sorted_bwd(plan, dh, dE, scale=1.0, acc=0, ws=None, s=None):
+    """dE [V, d] (+)= scale·the sums of dh's rows by token, with the plan of the batch's ids."""
+    V, d = dE.shape
+    if dh.shape[-1] != d:
+        raise ValueError("dh and dE need rows of one width")
+    T = dh.numel() // d
+    if ws is None:
+        ws = embedding_sorted_workspace(T, d, dE.device, s)
+    call("xt_embedding_sorted_bwd", ptr(plan), plan.numel(), ptr(dh), ptr(dE), T, d, V, float(scale), dt(dh), dt(dE),
+         int(acc), ptr(ws), ws.numel(), stream(s))
 
 
 def matmul_desc(M, N, K, *, trans_a=0, trans_b=0, lda=None, ldb=None, ldc=None, batch_outer=1, batch_inner=1,
