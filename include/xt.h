@@ -584,6 +584,29 @@ int xt_matmul_bwd(const xt_matmul_desc* desc, const void* A, const void* B, cons
                   void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * Gated feed-forward block, bf16, x [T, d], W_up = [Wg | Wu] [d, 2F], W_down [F, d] (the block stack's layout):
+ *   g = x Wg,  u = x Wu,  h = act(g)∘u,  y = h W_down        (act: silu, or the exact gelu)
+ *   dh = dy W_downᵀ,  dg = dh∘u∘act'(g),  du = dh∘act(g),  dx = dg Wgᵀ + du Wuᵀ,
+ *   dW_up = xᵀ [dg | du],  dW_down = hᵀ dy.
+ * Both projections, the activation and the product are one kernel; the backward forms dg and du in the epilogue of dh,
+ * which is never written.  Forward: gu ([T, 2F]: g and u rounded to bf16, what the backward reads) may be NULL, and y
+ * (then w_down too) where only h is wanted.  act is evaluated on the float32 g; h is rounded to bf16 once.
+ * Backward: dgu [T, 2F] bf16 is scratch that receives [dg | du]; dx (bf16), dw_up and dw_down (dt_grad) may be NULL.
+ * acc_dx, acc_dw: add to what is there.  T = 0: the weights' gradients are 0 (acc_dw = 0).
+ * d and F multiples of 8, all pointers 16-byte aligned (else XT_ERR_ALIGNMENT); dt = XT_BF16 (else
+ * XT_ERR_UNSUPPORTED).  ws: xt_gated_mlp_workspace_size bytes of matmul workspace (its first 4096 bytes zero before
+ * the first use; not shared by calls that can run at once), or NULL as for xt_matmul_fwd.  Outputs must not overlap
+ * inputs.  Deterministic; device-side waits are bounded (XT_DEVERR_TIMEOUT).
+ * ------------------------------------------------------------------------------- */
+enum { XT_GATE_SILU = 0, XT_GATE_GELU = 1 };
+int xt_gated_mlp_workspace_size(int64_t T, int64_t d, int64_t F, size_t* bytes);
+int xt_gated_mlp_fwd(const void* x, const void* w_up, const void* w_down, void* gu, void* h, void* y, int64_t T,
+                     int64_t d, int64_t F, int act, int dt, void* ws, size_t ws_bytes, void* stream);
+int xt_gated_mlp_bwd(const void* x, const void* w_up, const void* w_down, const void* gu, const void* h, const void* dy,
+                     void* dgu, void* dx, void* dw_up, void* dw_down, int64_t T, int64_t d, int64_t F, int act, int dt,
+                     int dt_grad, int acc_dx, int acc_dw, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
  * FP8 E4M3 ([BP] § Vad generiska ramverk kostar, item 4: an FP8 E4M3 tensor-core path in the
  * mixed-precision pipeline; the pages give no format details, so the OCP E4M3 format is used:
  * bias 7, 3 mantissa bits, subnormals m·2⁻⁹, largest finite 448, no infinities).

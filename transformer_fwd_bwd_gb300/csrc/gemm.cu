@@ -384,6 +384,57 @@ int run(const Problem& pb, cudaStream_t s) {
   return st;
 }
 
+int run_gated(const Problem& pb, cudaStream_t s) {
+  const bool fwd = pb.act == kGateFwdSilu || pb.act == kGateFwdGelu;
+  // Pairs of CTAs where their 256-row tiles fill half of the GPU (the paired product's rate is 1.15 of the single
+  // one's); single CTAs below that, with tiles of half the width where even those would leave most SMs idle.
+  const int nt = fwd ? 128 : 256;  // columns of a 256-wide tile
+  const int pairs = pair_capacity();
+  const int64_t pair_tiles = ceil_div(pb.M, 2 * BM) * ceil_div(pb.N, nt);
+  const int cg = pairs > 0 && pb.M > BM && 2 * pair_tiles >= pairs ? 2 : 1;
+  const int bn = cg == 1 && 2 * ceil_div(pb.M, BM) * ceil_div(pb.N, nt) <= num_sms() ? 128 : 256;
+  const int cols = fwd ? bn / 2 : bn;
+  CUtensorMap ta, tb, tc, tc2;
+  memset(&tc, 0, sizeof(tc));
+  memset(&tc2, 0, sizeof(tc2));
+  XT_TRY(make_operand_map(&ta, pb.A, kBf16, BM, k_atoms(cg)));
+  XT_TRY(make_operand_map(&tb, pb.B, kBf16, bn / cg, k_atoms(cg)));
+  if (fwd) XT_TRY(make_output_map(&tc, pb.C, true, pb.M, pb.N, pb.N, 1, 1, 0, 0));
+  if (pb.C2) XT_TRY(make_output_map(&tc2, pb.C2, true, pb.M, pb.N, 2 * pb.N, 2, 1, pb.N, 0));
+  Params p{};
+  p.M = int(pb.M);
+  p.N = int(pb.N);
+  p.K = int(pb.K);
+  p.num_m = int(ceil_div(pb.M, int64_t(BM) * cg));
+  p.num_n = int(ceil_div(pb.N, cols));
+  p.batch_inner = 1;
+  p.batches = 1;
+  p.splitk = 1;
+  p.tma_store = 1;
+  p.c_bf16 = 1;
+  p.alpha = 1.f;
+  p.act = pb.act;
+  p.aux = static_cast<const bf16*>(pb.aux);
+  p.ld_aux = 2 * pb.N;
+  p.gate = int(pb.N);
+  p.store_gu = fwd && pb.C2 ? 1 : 0;
+  p.flag = errflag();
+  p.wait_ns = wait_limit_ns();
+  const int64_t tiles = int64_t(p.num_m) * p.num_n;
+  if (tiles > int64_t(1) << 30) return fail(XT_ERR_UNSUPPORTED, "gated product: too many tiles");
+  const int units = cg == 2 ? pairs : num_sms();
+  const int grid = cg * int(tiles < units ? tiles : units);
+  const int shape[8] = {p.M, fwd ? 2 * p.N : p.N, p.K, 1, cg == 2 ? 1000 + bn : bn, 0, int(fwd), 0};
+  unsigned long long* ts = nullptr;
+  void* tok = nullptr;
+  const bool prof = gemm_profile_begin((fwd ? 4.0 : 2.0) * double(pb.M) * double(pb.N) * double(pb.K), shape, &ts, &tok) &&
+                    grid <= kProfGemmSlots;
+  p.prof_ts = prof ? ts : nullptr;
+  const int st = launch_gated(pb.act, bn, cg, ta, tb, tc, tc2, p, grid, s);
+  if (prof) gemm_profile_grids(tok, grid, 0);
+  return st;
+}
+
 }  // namespace gemm
 
 // ------------------------------------------------------------------------------ tf32 staging

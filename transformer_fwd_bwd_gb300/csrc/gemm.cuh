@@ -37,9 +37,11 @@ struct Problem {
   void* split_ws;  // room for K-split or stream-K partial tiles (may be null)
   size_t split_ws_bytes;
   uint32_t* sk_flags;  // kSkFlagBytes of stream-K flag words, zero between calls (null: no stream-K)
-  int act;         // GELU epilogue (see Params::act); 0 none
+  int act;         // GELU epilogue (see Params::act) or gated epilogue (kGateFwdSilu ..); 0 none
   void* C2;        // act 1: gelu(C), C's layout
   const void* aux; // act 2: the pre-activation, C's layout
+  // gated epilogues: C is [M, N] (forward: act(g)∘u; backward: none), B of the forward [K, 2N]; C2 (forward: may be null)
+  // and aux are [M, 2N], the gate's columns before the up projection's
 };
 
 // Tile width, K split and schedule chosen for a problem (see choose()).
@@ -74,6 +76,12 @@ int launch_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUten
 // bf16, BN 256, with the GELU epilogue `act` (1 or 2).
 int launch_bf16_act(int act, bool a_mn, bool b_mn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                     const CUtensorMap& tc2, const Params& p, int grid, cudaStream_t s);
+
+// The gated epilogues: BN 256 on CTA pairs (cg 2), BN 256 or 128 on single CTAs.
+int launch_gated(int act, int bn, int cg, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+                 const CUtensorMap& tc2, const Params& p, int grid, cudaStream_t s);
+// The products with a gated epilogue (Problem::act).
+int run_gated(const Problem& pb, cudaStream_t s);
 
 template <int KIND, int BN, bool A_MN, bool B_MN, int ACT = 0, int CG = 1, int MC = 1>
 int launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tc2,

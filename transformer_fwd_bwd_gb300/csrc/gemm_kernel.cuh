@@ -46,6 +46,10 @@ struct Params {
   int act;
   const bf16* aux;
   int64_t ld_aux;
+  // gated epilogues (kGateFwd.., bf16, whole tiles, one batch): the gate's columns of B (and of aux and of the C2 map's
+  // two batches) begin at 0, the up projection's at `gate`; store_gu: the forward also stores both projections
+  int gate;
+  int store_gu;
   uint32_t* flag;
   // Stream-K schedule (sk = 1): CTA c computes the k-block iterations [⌊c·I/G⌋, ⌊(c+1)·I/G⌋) of
   // the tiles × kb_tile iteration space (I = sk_iters ≥ G = gridDim.x ≤ the SMs), so every CTA
@@ -532,6 +536,47 @@ __device__ __forceinline__ void sk_fixup(uint32_t tacc, const Params& p, int fir
   }
 }
 
+// The gated feed-forward block's epilogues.
+//   kGateFwd*: B = [gate | up] (MN-major, `gate` columns each).  A BN-wide tile holds BN/2 columns of the gate's product
+//     and the BN/2 of the up projection beside them (paired CTAs: the even one stages the gate's columns of B, the odd one
+//     the others), so that a lane has both projections of its row: C = act(g)∘u, and g and u themselves as bf16 where
+//     Params::store_gu asks for them (the two batches of the C2 map).  act is evaluated on the float32 accumulators.
+//   kGateBwd*: the product is dh; g and u are read (bf16, aux) and dg = dh·u·act'(g), du = dh·act(g) stored (the two
+//     batches of the C2 map), so that dh never leaves the SM.
+constexpr int kGateFwdSilu = 3, kGateFwdGelu = 4, kGateBwdSilu = 5, kGateBwdGelu = 6;
+
+// act(g) and act'(g) of N values (silu: σ(g) by one exponential and one reciprocal; gelu: as gelu_batch).
+template <bool GELU, int N>
+__device__ __forceinline__ void gate_batch(const float (&g)[N], float (&a)[N], float (&da)[N]) {
+  if constexpr (GELU) {
+    float z[N], t[N], q[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      z[i] = fabsf(g[i]) * 0.70710678118654752f;
+      q[i] = erfc_poly(z[i], t[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = __expf(-z[i] * z[i]);
+      const float he = 0.5f * t[i] * e * __expf(q[i]);
+      const float cdf = g[i] <= 0.f ? he : 1.f - he;
+      a[i] = g[i] * cdf;
+      da[i] = fmaf(g[i], 0.39894228040143268f * e, cdf);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float sg = __fdividef(1.f, 1.f + __expf(-g[i]));
+      a[i] = g[i] * sg;
+      da[i] = fmaf(a[i], 1.f - sg, sg);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // ACT: the epilogue's GELU mode (Params::act), a template parameter so the plain GEMMs carry
 // none of its code.
 //
@@ -556,7 +601,12 @@ template <int KIND, int BN, bool A_MN, bool B_MN, int ACT = 0, int CG = 1, int M
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmC2, const Params p) {
-  static_assert(CG == 1 || (CG == 2 && ACT == 0 && BN % 32 == 0), "paired tiles: plain epilogue, BN / 2 whole atoms");
+  constexpr bool GATE_F = ACT == kGateFwdSilu || ACT == kGateFwdGelu, GATE_B = ACT == kGateBwdSilu || ACT == kGateBwdGelu;
+  constexpr int NT = GATE_F ? BN / 2 : BN;  // columns of the output in a tile
+  static_assert(CG == 1 || (CG == 2 && (ACT == 0 || GATE_F || GATE_B) && BN % 32 == 0),
+                "paired tiles: plain or gated epilogue, BN / 2 whole atoms");
+  static_assert(!(GATE_F || GATE_B) || (KIND == kBf16 && !A_MN && B_MN == GATE_F && BN % 128 == 0 && MC == 1),
+                "gated epilogues: x by rows, weights as stored");
   static_assert(MC == 1 || (MC == 2 && CG == 2 && BN == 256), "multicast pairs: 256-wide paired tiles");
   // The set-up below (barriers, tensor-map prefetch, TMEM) reads nothing a preceding kernel
   // writes, so it runs before the programmatic-launch wait.
@@ -603,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     if (p.tma_store) prefetch_tmap(&tmC);
-    if (ACT == 1) prefetch_tmap(&tmC2);
+    if (ACT == 1 || GATE_B || (GATE_F && p.store_gu)) prefetch_tmap(&tmC2);
   }
   if (warp == 1) {
     tmem_alloc_cg<CG>(smem_u32(tmem_slot), TCOLS);
@@ -633,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = p.num_m * p.num_n;
     const int r = t - (t / per) * per;
     if constexpr (CG == 2) ti.m0 = ti.m0 * 2 + rank * BM;
-    ti.n0 = (r / p.num_m) * BN;
+    ti.n0 = (r / p.num_m) * NT;
     if (p.causal == 1 && ti.n0 >= ti.m0 + BM) ti.skip = true;
     if (kb0 >= 0) {  // a stream-K piece
       ti.kb_begin = kb0;
@@ -695,6 +745,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               static_assert(!B_MN || BNH == 2 * ATOM, "MN-major B: one atom-wide box per pair");
               tma_load_4d_mc(b_s + pidx * (BK * 128), &tmB, fb_own, nb0 + pidx * ATOM, k0, ti.ozi, ti.ozo, mask);
+            }
+          } else if constexpr (GATE_F) {
+            constexpr int HALF = NT / ATOM;  // boxes of each projection
+#pragma unroll
+            for (int j = 0; j < BNH / ATOM; ++j) {
+              const int up = CG == 2 ? rank : j / HALF;
+              load(b_s + j * (BK * 128), &tmB, fb, up * p.gate + ti.n0 + (j % HALF) * ATOM, k0, ti.ozi, ti.ozo);
             }
           } else if constexpr (!B_MN) {
 #pragma unroll
@@ -827,6 +884,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ti.skip) continue;
       const int row = ti.m0 + q * 32 + lane;
       const bool empty_k = ti.kb_end <= ti.kb_begin;
+      // 32 gate (up = 0) or up columns of this lane's row of aux from x on; 0 outside
+      auto aux_row = [&](uint4 (&v)[4], int x, int up) {
+        const bf16* ap = p.aux + int64_t(row < p.M ? row : 0) * p.ld_aux + int64_t(up) * p.gate + x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = row < p.M && x + 8 * j < p.N ? __ldg(reinterpret_cast<const uint4*>(ap) + j) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      uint4 ga[4], ua[4];
+      if constexpr (GATE_B) {  // in flight while the product is finished
+        aux_row(ga, ti.n0, 0);
+        aux_row(ua, ti.n0, 1);
+      }
       // stream-K piece kind: 1 = a later part of the tile (partial to its slot), 2 = the tile's
       // first k-blocks with later parts in units unit + 1 .. sk_last (adds their partials)
       const int kind = kb0 > 0 ? 1 : (kb0 == 0 && kb1 < p.kb_tile) ? 2 : 0;
@@ -883,6 +952,141 @@ __global__ void __launch_bounds__(kThreads, 1)
         // then read the tile's full sum
         sk_fixup<BN, CG>(tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * BN), p, unit + 1, sk_last, rank,
                          q * 32 + lane);
+      }
+      if constexpr (GATE_F) {
+        // ---- 64 columns of the output at a time, staged as below: g, u (two batches of C2) and act(g)∘u
+        const int y = ti.m0 + q * 32;
+        auto put = [&](const CUtensorMap* tm, const float (&v)[64], int x, int z) {
+          const uint32_t row_addr = smem_u32(staging) + uint32_t((q * 2 + (chunk & 1)) * 4096 + lane * 128);
+          if (lane == 0) bulk_wait_read_1();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(row_addr + (uint32_t(j ^ (lane & 7)) << 4), pack_bf16(v[8 * j], v[8 * j + 1]),
+                         pack_bf16(v[8 * j + 2], v[8 * j + 3]), pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                         pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(tm, smem_u32(staging) + uint32_t((q * 2 + (chunk & 1)) * 4096), x, y, z, 0);
+            bulk_commit();
+          }
+          ++chunk;
+        };
+#pragma unroll 1
+        for (int c = 0; c < NT / 64; ++c) {
+          const int x = ti.n0 + c * 64;
+          uint32_t gr[64], ur[64];
+          const uint32_t at = tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * BN + c * 64);
+          __syncwarp();
+          tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(gr));
+          tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(gr + 32));
+          tmem_ld32(at + NT, *reinterpret_cast<uint32_t(*)[32]>(ur));
+          tmem_ld32(at + NT + 32, *reinterpret_cast<uint32_t(*)[32]>(ur + 32));
+          tmem_ld_wait();
+          if (c == NT / 64 - 1) {  // the accumulator is read: the next tile's products may start
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) release_acc(ab);
+          }
+          if (y >= p.M || x >= p.N) continue;
+          float g[64], u[64];
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            g[j] = __uint_as_float(gr[j]);
+            u[j] = __uint_as_float(ur[j]);
+          }
+          if (p.store_gu) {
+            put(&tmC2, g, x, 0);
+            put(&tmC2, u, x, 1);
+          }
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float gv[16], a[16], da[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) gv[e] = g[16 * h + e];
+            gate_batch<ACT == kGateFwdGelu>(gv, a, da);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) g[16 * h + e] = a[e] * u[16 * h + e];
+          }
+          put(&tmC, g, x, 0);
+        }
+        if (++ab == 2) { ab = 0; aphase ^= 1; }
+        continue;
+      }
+      if constexpr (GATE_B) {
+        // ---- 32 columns at a time: dh from the accumulator, g and u one piece ahead from memory; dg and du of two pieces
+        // staged in the warp's two buffers
+        const int y = ti.m0 + q * 32;
+        const uint32_t buf = smem_u32(staging) + uint32_t(q * 2 * 4096);
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          const int x = ti.n0 + c * 32;
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * BN + c * 32), r);
+          tmem_ld_wait();
+          if (c == BN / 32 - 1) {  // the accumulator is read: the next tile's products may start
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) release_acc(ab);
+          }
+          if (y >= p.M || x - (c & 1) * 32 >= p.N) continue;
+          uint4 gn[4], un[4];
+          if (c + 1 < BN / 32) {
+            aux_row(gn, x + 32, 0);
+            aux_row(un, x + 32, 1);
+          }
+          if ((c & 1) == 0) {
+            if (lane == 0) bulk_wait_read_0();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float g[16], u[16], a[16], da[16];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t[8];
+              Vec<bf16>::unpack(ga[2 * h + e], t);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) g[8 * e + k] = t[k];
+              Vec<bf16>::unpack(ua[2 * h + e], t);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) u[8 * e + k] = t[k];
+            }
+            gate_batch<ACT == kGateBwdGelu>(g, a, da);
+            uint32_t dg[8], du[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float d0 = __uint_as_float(r[16 * h + 2 * k]), d1 = __uint_as_float(r[16 * h + 2 * k + 1]);
+              dg[k] = pack_bf16(d0 * u[2 * k] * da[2 * k], d1 * u[2 * k + 1] * da[2 * k + 1]);
+              du[k] = pack_bf16(d0 * a[2 * k], d1 * a[2 * k + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = (c & 1) * 4 + 2 * h + e;
+              const uint32_t off = uint32_t(lane) * 128 + (uint32_t(j ^ (lane & 7)) << 4);
+              st_shared_v4(buf + off, dg[4 * e], dg[4 * e + 1], dg[4 * e + 2], dg[4 * e + 3]);
+              st_shared_v4(buf + 4096 + off, du[4 * e], du[4 * e + 1], du[4 * e + 2], du[4 * e + 3]);
+            }
+          }
+          if (c & 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_4d(&tmC2, buf, x - 32, y, 0, 0);
+              tma_store_4d(&tmC2, buf + 4096, x - 32, y, 1, 0);
+              bulk_commit();
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ga[j] = gn[j];
+            ua[j] = un[j];
+          }
+        }
+        if (++ab == 2) { ab = 0; aphase ^= 1; }
+        continue;
       }
       if (p.tma_store) {
         // ---- staged TMA stores: chunk = 32 rows × 128 bytes (32 fp32 or 64 bf16 columns)

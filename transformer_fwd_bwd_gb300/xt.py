@@ -23,6 +23,7 @@ XT_F32, XT_BF16 = 0, 1
 XT_DEVERR_INDEX, XT_DEVERR_TIMEOUT, XT_DEVERR_PLAN = 1, 2, 4
 XT_NORM_RMS, XT_NORM_LN = 0, 1
 XT_MLP_SWIGLU, XT_MLP_GELU = 0, 1
+XT_GATE_SILU, XT_GATE_GELU = 0, 1
 XT_ATTN_AUTO, XT_ATTN_COMPOSED, XT_ATTN_FUSED = 0, 1, 2
 
 
@@ -156,6 +157,10 @@ _SIGS = {
     "xt_embedding_plan": [_VP, _I64, _I64, _VP, C.c_size_t, _VP],
     "xt_embedding_sorted_bwd_workspace_size": [_I64, _I64, _SZP],
     "xt_embedding_sorted_bwd": [_VP, C.c_size_t, _VP, _VP, _I64, _I64, _I64, _F, _I, _I, _I, _VP, C.c_size_t, _VP],
+    "xt_gated_mlp_workspace_size": [_I64, _I64, _I64, _SZP],
+    "xt_gated_mlp_fwd": [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I, _I, _VP, C.c_size_t, _VP],
+    "xt_gated_mlp_bwd": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I, _I, _I, _I, _I, _VP,
+                         C.c_size_t, _VP],
     "xt_matmul_workspace_size": [C.POINTER(MatmulDesc), _SZP],
     "xt_gemm_set_schedule": [_I],
     "xt_gemm_set_pairing": [_I],
@@ -1011,3 +1016,53 @@ def xt_matmul_bwd(desc, A, B, dC, dA, dB, acc_a=0, acc_b=0, ws=None, s=None):
          ptr(dB, False),
          dt(dA) if dA is not None else XT_F32, dt(dB) if dB is not None else XT_F32, acc_a, acc_b, ptr(ws),
          ws.numel() if ws is not None else 0, stream(s))
+
+
+def gated_mlp_workspace(T, d, F, device="cuda", s=None):
+    return workspace(ws_bytes("xt_gated_mlp_workspace_size", int(T), int(d), int(F)), device, s)
+
+
+def _gated_shapes(x, w_up, w_down, **others):
+    """T, d, F of a gated block's tensors, all checked against each other."""
+    if x.dim() != 2 or w_up.dim() != 2 or w_up.shape[1] % 2:
+        raise ValueError("x must be [T, d] and w_up [d, 2F]")
+    T, d = x.shape
+    F = w_up.shape[1] // 2
+    shapes = dict(w_up=(d, 2 * F), w_down=(F, d), gu=(T, 2 * F), h=(T, F), y=(T, d), dy=(T, d), dgu=(T, 2 * F), dx=(T, d),
+                  dw_up=(d, 2 * F), dw_down=(F, d))
+    for name, t in dict(others, w_up=w_up, w_down=w_down).items():
+        if t is None:
+            continue
+        if tuple(t.shape) != shapes[name]:
+            raise ValueError(f"{name} must be {list(shapes[name])}")
+        if t.dtype != x.dtype and name not in ("dw_up", "dw_down"):
+            raise ValueError(f"{name} must have x's dtype")
+    return T, d, F
+
+
+def xt_gated_mlp_fwd(x, w_up, w_down, gu, h, y, act=XT_GATE_SILU, ws=None, s=None):
+    """h = act(x Wg)∘(x Wu), y = h w_down for x [T, d], w_up = [Wg | Wu] [d, 2F]; gu [T, 2F] keeps both projections for
+    the backward (None: not kept); y and w_down None: h alone."""
+    T, d, F = _gated_shapes(x, w_up, w_down, gu=gu, h=h, y=y)
+    if (y is None) != (w_down is None):
+        raise ValueError("y and w_down go together")
+    if ws is None and y is not None and T:
+        ws = gated_mlp_workspace(T, d, F, x.device, s)
+    call("xt_gated_mlp_fwd", ptr(x), ptr(w_up), ptr(w_down), ptr(gu), ptr(h), ptr(y), T, d, F, int(act), dt(x), ptr(ws),
+         ws.numel() if ws is not None else 0, stream(s))
+
+
+def xt_gated_mlp_bwd(x, w_up, w_down, gu, h, dy, dgu, dx, dw_up, dw_down, act=XT_GATE_SILU, acc_dx=0, acc_dw=0, ws=None,
+                     s=None):
+    """The gradients of xt_gated_mlp_fwd; dgu [T, 2F] is scratch (it receives the projections' gradients); dx, dw_up and
+    dw_down may be None."""
+    T, d, F = _gated_shapes(x, w_up, w_down, gu=gu, h=h, dy=dy, dgu=dgu, dx=dx, dw_up=dw_up, dw_down=dw_down)
+    kinds = {t.dtype for t in (dw_up, dw_down) if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("dw_up and dw_down must share a dtype")
+    some = dw_up if dw_up is not None else dw_down
+    if ws is None and T:
+        ws = gated_mlp_workspace(T, d, F, x.device, s)
+    call("xt_gated_mlp_bwd", ptr(x), ptr(w_up), ptr(w_down), ptr(gu), ptr(h), ptr(dy), ptr(dgu), ptr(dx), ptr(dw_up),
+         ptr(dw_down), T, d, F, int(act), dt(x), dt(some) if some is not None else XT_F32, int(acc_dx), int(acc_dw),
+         ptr(ws), ws.numel() if ws is not None else 0, stream(s))
