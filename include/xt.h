@@ -685,6 +685,34 @@ int xt_adamw8_decode(int n, const int8_t* const* m_code, const uint8_t* const* r
                      const float* const* r_scale, float* const* m, float* const* v, const int64_t* numel,
                      void* stream);
 
+/* The Muon step over n matrices W [rows[i], cols[i]] (float32 master weights), in place of AdamW for a model's hidden
+ * matrices; two-dimensional parameters such as embeddings, and vectors, stay with xt_adamw_step:
+ *   M ← μ M + s·G,   U = s·G + μ M (nesterov = 1; else U = M),   X = U / (‖U‖_F + ε),
+ *   steps times  X ← a X + (b A + c A²) X with A = X Xᵀ (Xᵀ X from the right where rows > cols),
+ *     a, b, c = 3.4445, −4.7750, 2.0315 (singular values go to about 1: 0.68 .. 1.21),
+ *   W ← W (1 − lr·λ) − lr·rms·√max(rows, cols)·X      (rms: the update's root mean square is about rms·lr).
+ * s = grad_scale, μ = momentum, λ = weight_decay.  momentum buffers M (float32) start at 0 and are updated in place with
+ * W; grad is read only; shadow as for xt_adamw_step.  Products are taken on f16 tensor cores from operands in two terms
+ * (22 bits), so X is as accurate as with float32 products.  A gradient of 0 with a momentum of 0 leaves X = 0; one that is
+ * not finite makes its own matrix NaN.  param, grad, momentum, shadow, rows and cols are HOST arrays; buffers are
+ * contiguous, of any alignment of float32 (multiples of 8 columns in 16-byte aligned buffers run on 16-byte accesses), and must
+ * not overlap.  At most 64 different shapes; matrices of one shape run as a batch.  Workspace: xt_muon_workspace_size
+ * bytes, 16-byte aligned, contents on entry do not matter; about 8 bytes per weight and 8·min(rows, cols)² per matrix.
+ * Deterministic.  Device-side waits are bounded (XT_DEVERR_TIMEOUT). */
+typedef struct xt_muon_config {
+  float lr, momentum, weight_decay;
+  float rms;        /* e.g. 0.2 */
+  float eps;        /* e.g. 1e-7 */
+  float grad_scale; /* applied to every gradient (1 / n_microbatches) */
+  int32_t nesterov; /* 0 or 1 */
+  int32_t steps;    /* 1 .. 20; usually 5 */
+} xt_muon_config;
+
+int xt_muon_workspace_size(int n, const int64_t* rows, const int64_t* cols, size_t* bytes);
+int xt_muon_step(const xt_muon_config* cfg, int n, float* const* param, const float* const* grad, float* const* momentum,
+                 void* const* shadow, int shadow_dtype, const int64_t* rows, const int64_t* cols, void* ws,
+                 size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------------
  * Native block stack ([BP] § Framåtgåendet; [DO] § dropout 接在哪（wiring）):
  *   h = E[ids] (+ P);  per layer l:  h += dropout(attn(norm1 h), seed ⊕ l ⊕ 0xA77),

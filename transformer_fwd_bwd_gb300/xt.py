@@ -51,6 +51,11 @@ class AdamWConfig(C.Structure):
                 ("step", C.c_int32)]
 
 
+class MuonConfig(C.Structure):
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("rms", C.c_float),
+                ("eps", C.c_float), ("grad_scale", C.c_float), ("nesterov", C.c_int32), ("steps", C.c_int32)]
+
+
 class AttentionDesc(C.Structure):
     _fields_ = [("T", C.c_int64), ("H", C.c_int32), ("Hkv", C.c_int32), ("hd", C.c_int32), ("dtype", C.c_int32),
                 ("scale", C.c_float), ("cap", C.c_float), ("slopes", C.c_void_p)]
@@ -178,6 +183,9 @@ _SIGS = {
     "xt_adamw8_step": [C.POINTER(AdamWConfig), _I, _PP, _PP, _PP, _PP, _PP, _PP, _PP, _I, C.POINTER(C.c_int64), _VP,
                        _VP, C.c_size_t, _VP],
     "xt_adamw8_decode": [_I, _PP, _PP, _PP, _PP, _PP, _PP, C.POINTER(C.c_int64), _VP],
+    "xt_muon_workspace_size": [_I, C.POINTER(C.c_int64), C.POINTER(C.c_int64), _SZP],
+    "xt_muon_step": [C.POINTER(MuonConfig), _I, _PP, _PP, _PP, _PP, _I, C.POINTER(C.c_int64), C.POINTER(C.c_int64), _VP,
+                     C.c_size_t, _VP],
     "xt_matmul_fwd": [C.POINTER(MatmulDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
     "xt_matmul_gelu_fwd": [C.POINTER(MatmulDesc), _VP, _VP, _VP, _VP, _VP, C.c_size_t, _VP],
     "xt_matmul_gelu_bwd": [C.POINTER(MatmulDesc), _VP, _VP, _VP, _VP, _VP, C.c_size_t, _VP],
@@ -912,6 +920,22 @@ def _table(tensors, dtype, numel, what="the parameters'"):
     return _addresses(map(_data_ptr, tensors))
 
 
+def _shadow_table(shadows, numel):
+    """Addresses and dtype of a list of working copies (entries, or the list, may be None)."""
+    if shadows is None:
+        return None, XT_F32
+    n = len(numel)
+    if len(shadows) != n:
+        raise ValueError("the lists must have the same length")
+    some = [t for t in shadows if t is not None]
+    sdt = dt(some[0]) if some else XT_F32
+    sh = _table(some, some[0].dtype if some else None, [k for t, k in zip(shadows, numel) if t is not None])
+    if len(some) < n:
+        given = iter(sh)
+        sh = (C.c_void_p * n)(*[next(given) if t is not None else None for t in shadows])
+    return sh, sdt
+
+
 def _adamw8_tables(numel, m_code, r_code, m_scale, r_scale):
     scales = [(k + 255) // 256 for k in numel]
     return (_table(m_code, torch.int8, numel), _table(r_code, torch.uint8, numel),
@@ -926,16 +950,7 @@ def xt_adamw8_step(cfg, params, grads, m_code, r_code, m_scale, r_scale, shadows
     n = len(numel)
     tables = (_table(params, torch.float32, numel), _table(grads, torch.float32, numel),
               *_adamw8_tables(numel, m_code, r_code, m_scale, r_scale))
-    sh, sdt = None, XT_F32
-    if shadows is not None:
-        if len(shadows) != n:
-            raise ValueError("the lists must have the same length")
-        some = [t for t in shadows if t is not None]
-        sdt = dt(some[0]) if some else XT_F32
-        sh = _table(some, some[0].dtype if some else None, [k for t, k in zip(shadows, numel) if t is not None])
-        if len(some) < n:
-            given = iter(sh)
-            sh = (C.c_void_p * n)(*[next(given) if t is not None else None for t in shadows])
+    sh, sdt = _shadow_table(shadows, numel)
     if ws is None and n and (cfg.max_grad_norm > 0 or norm_out is not None):
         ws = adamw8_workspace(numel, params[0].device, s=s)
     call("xt_adamw8_step", C.byref(cfg), n, *tables, sh, sdt, (C.c_int64 * max(1, n))(*numel), ptr(norm_out), ptr(ws),
@@ -949,6 +964,40 @@ def xt_adamw8_decode(m_code, r_code, m_scale, r_scale, m=None, v=None, s=None):
     out = [_table(lst, torch.float32, numel) if lst is not None else None for lst in (m, v)]
     call("xt_adamw8_decode", n, *_adamw8_tables(numel, m_code, r_code, m_scale, r_scale), *out,
          (C.c_int64 * max(1, n))(*numel), stream(s))
+
+
+def muon_config(lr, momentum=0.95, weight_decay=0.0, rms=0.2, eps=1e-7, grad_scale=1.0, nesterov=1, steps=5):
+    return MuonConfig(lr, momentum, weight_decay, rms, eps, grad_scale, nesterov, steps)
+
+
+def _sides(shapes):
+    n = max(1, len(shapes))
+    return (C.c_int64 * n)(*[r for r, _ in shapes]), (C.c_int64 * n)(*[c for _, c in shapes])
+
+
+def muon_workspace(shapes, device="cuda", s=None):
+    """A workspace of xt_muon_step for matrices of these (rows, cols)."""
+    return scratch(ws_bytes("xt_muon_workspace_size", len(shapes), *_sides(shapes)), device, s)
+
+
+def xt_muon_step(cfg, params, grads, momentum, shadows=None, ws=None, s=None):
+    """One Muon step over a list of float32 matrices (params and momentum updated in place); shadows as for
+    xt_adamw_step."""
+    shapes = [tuple(t.shape) for t in params]
+    if any(len(shape) != 2 for shape in shapes):
+        raise ValueError("params must be matrices")
+    for lst in (grads, momentum, shadows):
+        if lst is not None and (len(lst) != len(params) or
+                                any(t is not None and tuple(t.shape) != shape for t, shape in zip(lst, shapes))):
+            raise ValueError("the lists must have params' shapes")
+    numel = list(map(_numel, params))
+    n = len(numel)
+    tables = [_table(lst, torch.float32, numel) for lst in (params, grads, momentum)]
+    sh, sdt = _shadow_table(shadows, numel)
+    if ws is None and n:
+        ws = muon_workspace(shapes, params[0].device, s)
+    call("xt_muon_step", C.byref(cfg), n, *tables, sh, sdt, *_sides(shapes), ptr(ws), ws.numel() if ws is not None else 0,
+         stream(s))
 
 
 def xt_quantize_fp8(x, out, dequant, ws=None, s=None):
