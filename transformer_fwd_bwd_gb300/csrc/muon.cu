@@ -7,7 +7,8 @@
 // directions of small singular values: with every operand rounded to bf16 X comes out with a relative error of a few
 // 10⁻², to f16 of a few 10⁻³.  Here X, A and B = b A + c A² are held as two f16 terms each (value and remainder,
 // 22 bits, scaled by 2¹⁰ so that remainders stay normal numbers; singular values stay below 1.21, entries of B below
-// 16), and a product is three: hi·hi + hi·lo + lo·hi, float32 sums in tensor memory.  X is then good to a few 10⁻⁶,
+// 16), and a product is three: hi·lo + lo·hi + hi·hi, float32 sums in tensor memory.  The sums there are cut off, not
+// rounded, after every 16 elements of K: the small products come first, while the sum is small.  X is then good to a few 10⁻⁶,
 // as with float32 products, at three times the operations of a single f16 product.
 //
 // Work.  A and A² are symmetric: only the tiles on and above the diagonal are computed, the others written from them.
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
           const uint32_t p_s = smem_u32(smem + stage * kStageBytes), q_s = p_s + kOperandBytes;
           const int term = kb / g.k_blocks, k0 = (kb - term * g.k_blocks) * kBk;
-          const int zp = term == 2, zq = term == 1;  // hi·hi, hi·lo, lo·hi
+          const int zp = term == 1, zq = term == 0;  // hi·lo, lo·hi, hi·hi
 #pragma unroll
           for (int c = 0; c < kAtoms; ++c) {
             if (g.p_mn) tma_load_4d_pair(p_s + c * (kBk * 128), &g.tp, fb, m0 + c * kAtom, k0, w.batch, zp);

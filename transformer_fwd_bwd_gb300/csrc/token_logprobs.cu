@@ -18,6 +18,7 @@
 //
 // Bound by HBM: a logit is read once (backward: read and written).  Measured times stand beside the launches.
 #include <cfloat>
+#include <cstring>
 
 #include "internal.cuh"
 
@@ -173,35 +174,70 @@ __device__ __forceinline__ uint64_t insert_warp(uint64_t list, uint64_t c, int l
   return lane < pos ? list : lane == pos ? c : up;
 }
 
-// Puts the elements of vector j (held by this lane; none where j < 0) at or above `bound` into the warp's list.
+__device__ __forceinline__ float order_value(uint64_t o) {
+  const uint32_t k = uint32_t(o >> 32);
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// Puts the elements at or above `bound` of the lanes' vectors (number j; none where j < 0) into the warp's list: lanes
+// whose maximum reaches the bound hand their 16 bytes round.
 template <typename T>
 __device__ __forceinline__ uint64_t collect(uint64_t list, const Row<T>& row, int64_t j, uint64_t bound, int lane) {
   constexpr int W = Chunk<T>::W;
-  float x[W];
-  int64_t e0 = 0;
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
   int n = 0;
+  float top = -INFINITY;
   if (j >= 0) {
-    e0 = row.first(j);
-    n = int(row.last(j) - e0);
+    n = int(row.last(j) - row.first(j));
     if (n == W && j > 0) {
-      Chunk<T>::values(*reinterpret_cast<const uint4*>(row.vector(j)), x);
+      q = *reinterpret_cast<const uint4*>(row.vector(j));
+      top = Chunk<T>::top(q);
     } else {
+      T v[W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = i < n ? to_f(row.x[e0 + i]) : 0.f;
+      for (int i = 0; i < W; ++i) v[i] = i < n ? row.x[row.first(j) + i] : from_f<T>(-INFINITY);
+      memcpy(&q, v, 16);
+      top = Chunk<T>::top(q);
     }
   }
+  uint32_t some = __ballot_sync(0xffffffffu, n > 0 && order(top, uint32_t(j)) >= bound);
+  while (some) {
+    const int from = __ffs(some) - 1;
+    some &= some - 1;
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, q.x, from);
+    o.y = __shfl_sync(0xffffffffu, q.y, from);
+    o.z = __shfl_sync(0xffffffffu, q.z, from);
+    o.w = __shfl_sync(0xffffffffu, q.w, from);
+    const int count = __shfl_sync(0xffffffffu, n, from);
+    const uint32_t jj = uint32_t(__shfl_sync(0xffffffffu, int(j), from));
+    float v[W], mine = 0.f;
+    Chunk<T>::values(o, v);
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < W; ++i) mine = lane == i ? v[i] : mine;
     uint64_t c = 0;
-    if (i < n && order(x[i], uint32_t(j)) >= bound) c = order(x[i], uint32_t(e0 + i));
-    uint32_t some = __ballot_sync(0xffffffffu, c != 0);
-    while (some) {
-      const int from = __ffs(some) - 1;
-      some &= some - 1;
-      list = insert_warp(list, __shfl_sync(0xffffffffu, c, from), lane);
+    if (lane < count && order(mine, jj) >= bound) c = order(mine, uint32_t(row.first(jj) + lane));
+    uint32_t hits = __ballot_sync(0xffffffffu, c != 0);
+    while (hits) {
+      const int l = __ffs(hits) - 1;
+      hits &= hits - 1;
+      list = insert_warp(list, __shfl_sync(0xffffffffu, c, l), lane);
     }
   }
   return list;
+}
+
+// The largest entries of N warps' lists, in falling order, merged pair by pair; the result is warp 0's return value.
+template <int N>
+__device__ __forceinline__ uint64_t merge_lists(uint64_t (*lists)[32], uint64_t mine, int warp, int lane) {
+#pragma unroll
+  for (int s = 1; s < N; s *= 2) {
+    lists[warp][lane] = mine;
+    __syncthreads();
+    if (warp % (2 * s) == 0 && warp + s < N) mine = merge_warp(mine, lists[warp + s][lane], lane);
+    __syncthreads();
+  }
+  return mine;
 }
 
 struct Fwd {
@@ -215,16 +251,15 @@ struct Fwd {
   uint32_t* flag;
 };
 
-// The row's results from M, log2 Σ 2^(c(x − M)) and −Σ p·c(x − M) (log2 units): one thread.
-template <typename T>
-__device__ __forceinline__ void write_row(const Fwd& a, const T* x, int64_t r, float M, double log2s, double mean) {
+// The row's results from M, log2 Σ 2^(c(x − M)) and Σ p·c(x − M) (log2 units), by the lane that holds the row's token and
+// its logit.
+__device__ __forceinline__ void write_row(const Fwd& a, int64_t r, bool valid, float given, float M, double log2s,
+                                          double mean) {
   const bool ok = isfinite(M) && isfinite(log2s) && isfinite(mean);
   const float nan = __int_as_float(0x7fc00000);
   const double ln2 = 0.69314718055994530942;
-  const int32_t t = a.tokens[r];
-  const bool valid = t >= 0 && t < a.V;
   if (!valid) flag_error(a.flag, XT_DEVERR_INDEX);
-  const double z = valid ? (double(to_f(x[t])) - double(M)) * double(a.scale) : 0.0;
+  const double z = (double(given) - double(M)) * double(a.scale);
   a.logp[r] = ok && valid ? float(z - log2s * ln2) : nan;
   if (a.entropy) a.entropy[r] = ok ? float(fmax((log2s - mean) * ln2, 0.0)) : nan;
   if (a.stats) {
@@ -233,15 +268,12 @@ __device__ __forceinline__ void write_row(const Fwd& a, const T* x, int64_t r, f
   }
 }
 // The list's entries: one lane each.
-template <typename T>
-__device__ __forceinline__ void write_top(const Fwd& a, const T* x, int64_t r, uint64_t list, int lane, float M,
-                                          double log2s) {
+__device__ __forceinline__ void write_top(const Fwd& a, int64_t r, uint64_t list, int lane, float M, double log2s) {
   if (lane >= a.top) return;
   const bool ok = isfinite(M) && isfinite(log2s);
-  const int32_t id = int32_t(~uint32_t(list));
-  const double z = ok ? (double(to_f(x[id])) - double(M)) * double(a.scale) - log2s * 0.69314718055994530942 : 0.0;
+  const double z = (double(order_value(list)) - double(M)) * double(a.scale) - log2s * 0.69314718055994530942;
   a.top_logp[r * a.top + lane] = ok ? float(z) : __int_as_float(0x7fc00000);
-  a.top_ids[r * a.top + lane] = ok ? id : -1;
+  a.top_ids[r * a.top + lane] = ok ? int32_t(~uint32_t(list)) : -1;
 }
 
 // The sums of one row by one warp, differences taken before they are scaled, double sums: any finite logits.
@@ -280,14 +312,15 @@ __device__ __forceinline__ void warp_join(float& b, float& s, float& w) {
 // WARP: a warp to a row (short rows); else a CTA, or with gridDim.x a multiple of the cluster size a cluster of CTAs
 // that share the row's vectors out in ranges and join in the first one's shared memory.
 template <typename T, bool TOP, bool WARP>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ Fwd a) {
+__global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __grid_constant__ Fwd a) {
   constexpr int W = Chunk<T>::W;
   constexpr int kUnroll = 4;
   constexpr int NT = WARP ? 32 : kThreads;  // threads that share the vectors
   constexpr int kMaxCluster = 8;
   __shared__ float part[3][kMaxCluster * kWarps];  // base, Σ, Σ t of every warp of the cluster (in its first CTA)
   __shared__ float part_top[kMaxCluster * kWarps];
-  __shared__ uint64_t lists[TOP && !WARP ? kMaxCluster * kWarps : 1][TOP && !WARP ? 32 : 1];
+  __shared__ uint64_t lists[TOP && !WARP ? kWarps : 1][32];
+  __shared__ uint64_t cluster_lists[TOP && !WARP ? kMaxCluster : 1][32];  // of every CTA (in the first one)
   __shared__ uint64_t chosen[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tid = WARP ? lane : int(threadIdx.x);
@@ -296,11 +329,21 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
   }
+  // the other CTAs are running before anything is stored into the first one
+  if (!WARP && cl > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   pdl_begin();
   const int64_t r = WARP ? int64_t(blockIdx.x) * kWarps + warp : int64_t(blockIdx.x) / cl;
   if (WARP && r >= a.rows) return;
   const T* x = static_cast<const T*>(a.x) + r * a.ld;
   const Row<T> row(x, a.V);
+  // the token's logit, on its way while the row is read
+  int32_t token = -1;
+  float given = 0.f;
+  if (lane == 0 && (WARP || warp == 0)) {
+    token = __ldg(a.tokens + r);
+    if (token >= 0 && token < a.V) given = to_f(x[token]);
+  }
+  const bool valid = token >= 0 && token < a.V;
   // this CTA's whole vectors: (lo, hi], numbers 1 .. full
   const int64_t lo = WARP ? 0 : row.full * rank / cl, hi = WARP ? row.full : row.full * (rank + 1) / cl;
 
@@ -319,11 +362,18 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       consume<W>(m, v, Chunk<T>::top(q[u]), uint32_t(j + u * NT), a.c);
     }
   }
-  for (; j <= hi; j += NT, p += NT * W) {
-    const uint4 q = load_stream(p);
-    float v[W];
-    Chunk<T>::values(q, v);
-    consume<W>(m, v, Chunk<T>::top(q), uint32_t(j), a.c);
+  {  // what is left, all of it in flight at once
+    uint4 q[kUnroll - 1];
+#pragma unroll
+    for (int u = 0; u < kUnroll - 1; ++u)
+      if (j + u * NT <= hi) q[u] = load_stream(p + u * NT * W);
+#pragma unroll
+    for (int u = 0; u < kUnroll - 1; ++u) {
+      if (j + u * NT > hi) break;
+      float v[W];
+      Chunk<T>::values(q[u], v);
+      consume<W>(m, v, Chunk<T>::top(q[u]), uint32_t(j + u * NT), a.c);
+    }
   }
   // the elements beside the whole vectors: the head with thread 0 of the first CTA, the tail with the last thread of
   // the last one (whose vectors they follow, so that the first of equal values is kept)
@@ -360,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
     double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
     double mean = double(w / s) + (double(b) - double(M) * double(a.c));
     if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
-    if (lane == 0) write_row(a, x, r, M, log2s, mean);
+    if (lane == 0) write_row(a, r, valid, given, M, log2s, mean);
     if constexpr (TOP) {
       const uint64_t bound = __shfl_sync(0xffffffffu, sort_warp(best, lane), a.top - 1);
       // vectors are few here: all of them are looked through
@@ -368,22 +418,15 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
         const int64_t jj = j0 + lane;
         list = collect(list, row, jj <= tail ? jj : -1, bound, lane);
       }
-      write_top(a, x, r, list, lane, M, log2s);
+      write_top(a, r, list, lane, M, log2s);
     }
     return;
   }
 
   // ---- the CTA's most probable elements
   if constexpr (TOP) {
-    const uint64_t sorted = sort_warp(best, lane);
-    lists[warp][lane] = sorted;
-    __syncthreads();
-    if (warp == 0) {
-      uint64_t v = sorted;
-#pragma unroll 1
-      for (int k = 1; k < kWarps; ++k) v = merge_warp(v, lists[k][lane], lane);
-      chosen[lane] = v;
-    }
+    const uint64_t all = merge_lists<kWarps>(lists, sort_warp(best, lane), warp, lane);
+    if (warp == 0) chosen[lane] = all;
     __syncthreads();
     const uint64_t bound = chosen[a.top - 1];
     // a warp to a chosen thread: its vectors are the number that its maximum lies in, modulo kThreads
@@ -403,14 +446,13 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       if (owner == kThreads - 1 && rank == cl - 1 && row.first(tail) < a.V)
         list = collect(list, row, lane == 0 ? tail : -1, bound, lane);
     }
-    __syncthreads();  // lists are free again
+    list = merge_lists<kWarps>(lists, list, warp, lane);
   }
 
-  // ---- the warps' sums and lists meet in the first CTA of the cluster
+  // ---- the warps' sums and the CTAs' lists meet in the first CTA of the cluster
   const int slot = int(rank) * kWarps + warp;
   if (cl > 1) {
-    // every CTA of the cluster runs, and the first one's warps are past the lists of their own
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     auto at0 = [](const void* p) {
       uint32_t d;
       asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(d) : "r"(uint32_t(__cvta_generic_to_shared(p))));
@@ -422,9 +464,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at0(&part[2][slot])), "f"(w) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at0(&part_top[slot])), "f"(M) : "memory");
     }
-    if constexpr (TOP) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at0(&lists[slot][lane])), "l"(list) : "memory");
+    if constexpr (TOP)
+      if (warp == 0)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at0(&cluster_lists[rank][lane])), "l"(list) : "memory");
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     if (rank != 0) return;
+    if constexpr (TOP) list = merge_lists<kWarps>(lists, warp < int(cl) ? cluster_lists[warp][lane] : 0ull, warp, lane);
   } else {
     if (lane == 0) {
       part[0][slot] = b;
@@ -432,7 +477,6 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       part[2][slot] = w;
       part_top[slot] = M;
     }
-    if constexpr (TOP) lists[slot][lane] = list;
     __syncthreads();
   }
   if (warp != 0) return;
@@ -454,13 +498,8 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
   double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
   double mean = double(w / s) + (double(b) - double(M) * double(a.c));
   if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
-  if (lane == 0) write_row(a, x, r, M, log2s, mean);
-  if constexpr (TOP) {
-    list = lists[0][lane];
-#pragma unroll 1
-    for (int k = 1; k < n; ++k) list = merge_warp(list, lists[k][lane], lane);
-    write_top(a, x, r, list, lane, M, log2s);
-  }
+  if (lane == 0) write_row(a, r, valid, given, M, log2s, mean);
+  if constexpr (TOP) write_top(a, r, list, lane, M, log2s);
 }
 
 // ------------------------------------------------------------------------------ backward
@@ -473,34 +512,67 @@ struct Bwd {
   float scale, c;
   void* dx;
   int64_t ld_d, rows, V;
-  int64_t segs;     // pieces of a row, kSegVectors vectors for each lane
-  int acc;
+  int segs;         // pieces of a row, loops·kSegVectors vectors for each lane
+  int loops, acc;
   uint32_t* flag;
 };
 constexpr int kSegVectors = 4;
 
-// A warp to kSegVectors·32 vectors of a row: dx = p·(A + B·t) (+ scale·dlogp at the token), t = log2 p.
+// 16 bytes of gradients, or as many as W values make, from and to memory.
+template <typename TG, int W> struct Store {
+  static constexpr int S = 16 / int(sizeof(TG)) < W ? 16 / int(sizeof(TG)) : W;  // elements to an access
+  __device__ __forceinline__ static void add(const TG* p, float (&v)[W]) {
+#pragma unroll
+    for (int k = 0; k < W; k += S) {
+      float o[S];
+      if constexpr (S * sizeof(TG) == 16) Vec<TG>::load(p + k, o);
+      else
+#pragma unroll
+        for (int i = 0; i < S; ++i) o[i] = to_f(p[k + i]);
+#pragma unroll
+      for (int i = 0; i < S; ++i) v[k + i] += o[i];
+    }
+  }
+  __device__ __forceinline__ static void put(TG* p, const float (&v)[W]) {
+#pragma unroll
+    for (int k = 0; k < W; k += S) {
+      float o[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) o[i] = v[k + i];
+      if constexpr (S * sizeof(TG) == 16) Vec<TG>::store(p + k, o);
+      else
+#pragma unroll
+        for (int i = 0; i < S; ++i) p[k + i] = from_f<TG>(o[i]);
+    }
+  }
+};
+
+// A warp to loops·kSegVectors·32 vectors of a row: dx = p·(A + B·t) (+ scale·dlogp at the token), t = log2 p.
 template <typename T, typename TG>
-__global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(const __grid_constant__ Bwd a) {
+__global__ void __launch_bounds__(kThreads, 5) token_logprobs_bwd_kernel(const __grid_constant__ Bwd a) {
   constexpr int W = Chunk<T>::W;
   pdl_begin();
   const int lane = threadIdx.x & 31;
   const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t r = unit / a.segs, seg = unit - r * a.segs;
+  const int64_t r = unit / a.segs;
+  const int seg = int(unit - r * a.segs);
   if (r >= a.rows) return;
   const T* x = static_cast<const T*>(a.x) + r * a.ld;
   TG* dx = static_cast<TG*>(a.dx) + r * a.ld_d;
   const Row<T> row(x, a.V);
-  const int64_t tail = row.full + 1;
-  const int64_t j0 = seg * (kSegVectors * 32);
+  const int full = int(row.full);
+  int j0 = seg * a.loops * (kSegVectors * 32) + lane;
+  uint4 q[kSegVectors];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int u = 0; u < kSegVectors; ++u) {
+      const int j = j0 + u * 32;
+      if (j >= 1 && j <= full) q[u] = *reinterpret_cast<const uint4*>(row.vector(j));
+    }
+  };
+  fetch();
   // 16-byte stores where the gradient's vectors are aligned as the logits' are
   const bool vec = ((reinterpret_cast<uintptr_t>(dx) + size_t(row.head) * sizeof(TG)) & 15) == 0;
-  uint4 q[kSegVectors];
-#pragma unroll
-  for (int u = 0; u < kSegVectors; ++u) {
-    const int64_t j = j0 + u * 32 + lane;
-    if (j >= 1 && j <= row.full) q[u] = *reinterpret_cast<const uint4*>(row.vector(j));
-  }
   const float dl = a.d_logp ? __ldg(a.d_logp + r) : 0.f, dh = a.d_entropy ? __ldg(a.d_entropy + r) : 0.f;
   const int32_t t = __ldg(a.tokens + r);
   const bool valid = t >= 0 && t < a.V;
@@ -511,55 +583,49 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(const __gr
   const float A = valid ? -a.scale * fmaf(dh, H, dl) : __int_as_float(0x7fc00000);
   const float B = -a.scale * dh * 0.6931471805599453f;
   const float hit = a.scale * dl;
+  for (int loop = 0;;) {
 #pragma unroll
-  for (int u = 0; u < kSegVectors; ++u) {
-    const int64_t j = j0 + u * 32 + lane;
-    if (j > tail) continue;
-    const int64_t e0 = row.first(j);
-    const int n = int(row.last(j) - e0);
-    const bool whole = j >= 1 && j <= row.full;
-    float v[W];
-    if (whole) {
-      Chunk<T>::values(q[u], v);
-    } else {
+    for (int u = 0; u < kSegVectors; ++u) {
+      const int j = j0 + u * 32;
+      if (j > full + 1) continue;
+      const int e0 = int(row.first(j));
+      const int n = int(row.last(j)) - e0;
+      const bool whole = j >= 1 && j <= full;
+      float v[W];
+      if (whole) {
+        Chunk<T>::values(q[u], v);
+      } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = i < n ? to_f(x[e0 + i]) : 0.f;
-    }
-    const int64_t rel = int64_t(t) - e0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float y = max_nan(fmaf(v[i] - M, a.c, -L), kLowest);
-      float d = ex2(y) * fmaf(B, y, A);
-      d = rel == i ? d + hit : d;
-      v[i] = none ? 0.f : d;
-    }
-    TG* out = dx + e0;
-    if (whole && vec) {
-      constexpr int S = 16 / int(sizeof(TG)) < W ? 16 / int(sizeof(TG)) : W;  // elements to a store
-#pragma unroll
-      for (int k = 0; k < W; k += S) {
-        float o[S];
-        if (a.acc) {
-          if constexpr (S * sizeof(TG) == 16) Vec<TG>::load(out + k, o);
-          else
-#pragma unroll
-            for (int i = 0; i < S; ++i) o[i] = to_f(out[k + i]);
-#pragma unroll
-          for (int i = 0; i < S; ++i) o[i] += v[k + i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < S; ++i) o[i] = v[k + i];
-        }
-        if constexpr (S * sizeof(TG) == 16) Vec<TG>::store(out + k, o);
-        else
-#pragma unroll
-          for (int i = 0; i < S; ++i) out[k + i] = from_f<TG>(o[i]);
+        for (int i = 0; i < W; ++i) v[i] = i < n ? to_f(x[e0 + i]) : 0.f;
       }
-    } else {
+      if (none) {
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < n) out[i] = from_f<TG>(a.acc ? to_f(out[i]) + v[i] : v[i]);
+        for (int i = 0; i < W; ++i) v[i] = 0.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float y = max_nan(fmaf(v[i] - M, a.c, -L), kLowest);
+          v[i] = ex2(y) * fmaf(B, y, A);
+        }
+        if (uint32_t(t - e0) < uint32_t(W)) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[i] += t - e0 == i ? hit : 0.f;
+        }
+      }
+      TG* out = dx + e0;
+      if (whole && vec) {
+        if (a.acc) Store<TG, W>::add(out, v);
+        Store<TG, W>::put(out, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (i < n) out[i] = from_f<TG>(a.acc ? to_f(out[i]) + v[i] : v[i]);
+      }
     }
+    if (++loop == a.loops) break;
+    j0 += kSegVectors * 32;
+    if (j0 - lane > full + 1) break;
+    fetch();
   }
 }
 
@@ -635,9 +701,12 @@ int xt_token_logprobs_bwd(const void* logits, int64_t ld, const int32_t* tokens,
   if (reinterpret_cast<uintptr_t>(dlogits) % dtype_size(dt_grad))
     return fail(XT_ERR_ALIGNMENT, "%s: dlogits are not aligned to their type", fn);
   const int w = dt == XT_BF16 ? 8 : 4;
-  // whole vectors, the head and the tail (V/w + 2 numbers at most)
-  const int64_t segs = ceil_div(V / w + 2, kSegVectors * 32);
-  Bwd a{logits, ld, tokens, stats, entropy, d_logp, d_entropy, scale, scale * kLog2e, dlogits, ld_d, rows, V, segs, acc,
+  const int64_t vectors = V / w + 2;  // whole ones, the head and the tail
+  // as long pieces as leave 64 warps to an SM, so that a row's values are fetched seldom
+  int loops = 4;
+  while (loops > 1 && rows * ceil_div(vectors, kSegVectors * 32 * loops) < int64_t(num_sms()) * 64) loops /= 2;
+  const int64_t segs = ceil_div(vectors, kSegVectors * 32 * loops);
+  Bwd a{logits, ld, tokens, stats, entropy, d_logp, d_entropy, scale, scale * kLog2e, dlogits, ld_d, rows, V, int(segs), loops, acc,
         errflag()};
   const int64_t grid = ceil_div(rows * segs, kWarps);
   if (grid >= (int64_t(1) << 31)) return fail(XT_ERR_UNSUPPORTED, "%s: too many rows", fn);
