@@ -62,11 +62,23 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int kSortCluster = 8;
+constexpr int kBatch = 8;
 // counts of the CTA's warps, totals of every CTA of the cluster, scratch of the scan over digits
 constexpr int kSortSmem = (kSortWarps * kDigits + kSortCluster * kDigits + kSortWarps) * 4;
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The lanes whose digit (of `bits` bits) is this lane's, among those in `in`: a ballot per bit (about 27 instructions; the
+// instruction that compares all lanes' values is slower: 131072 tokens sorted in 73 us instead of 56).
+__device__ __forceinline__ uint32_t same_digit(uint32_t dg, bool in, int bits) {
+  uint32_t peers = __ballot_sync(0xffffffffu, in);
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t one = __ballot_sync(0xffffffffu, (dg >> b) & 1);
+    peers &= (dg >> b) & 1 ? one : ~one;
+  }
+  return peers;
 }
 
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const int32_t* __restrict__ ids, void* plan,
@@ -104,15 +116,22 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const int3
     for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) counts[i] = 0;
     __syncthreads();
     uint32_t* mine = counts + warp * kDigits;
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint64_t e = in ? item(i) : 0;
-      const uint32_t dg = in ? uint32_t(e >> shift) & mask : uint32_t(kDigits);
-      if (p == 0 && in && (e >> 32) == uint64_t(V)) flag_error(flag, XT_DEVERR_INDEX);
-      const uint32_t peers = __match_any_sync(0xffffffffu, dg);
-      if (in && lane == __ffs(peers) - 1) mine[dg] += __popc(peers);
-      __syncwarp();
+    // kBatch rounds of 32 tokens are fetched together
+    auto digit = [&](uint64_t e, bool in) { return in ? uint32_t(e >> shift) & mask : uint32_t(kDigits); };
+    for (int64_t b0 = lo; b0 < hi; b0 += kBatch * 32) {
+      uint64_t e[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) e[k] = b0 + k * 32 + lane < hi ? item(b0 + k * 32 + lane) : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (b0 + k * 32 >= hi) break;
+        const bool in = b0 + k * 32 + lane < hi;
+        const uint32_t dg = digit(e[k], in);
+        if (p == 0 && in && (e[k] >> 32) == uint64_t(V)) flag_error(flag, XT_DEVERR_INDEX);
+        const uint32_t peers = same_digit(dg, in, bits);
+        if (in && lane == __ffs(peers) - 1) mine[dg] += __popc(peers);
+        __syncwarp();
+      }
     }
     __syncthreads();
     // counts → prefix over the CTA's warps; the CTA's totals go to every CTA of the cluster
@@ -156,22 +175,86 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const int3
       for (int w = 0; w < kSortWarps; ++w) counts[w * kDigits + threadIdx.x] += base;
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint64_t e = in ? item(i) : 0;
-      const uint32_t dg = in ? uint32_t(e >> shift) & mask : uint32_t(kDigits);
-      const uint32_t peers = __match_any_sync(0xffffffffu, dg);
-      const uint32_t first = in ? mine[dg] : 0u;
-      __syncwarp();
-      if (in) {
-        dst[first + __popc(peers & ((1u << lane) - 1u))] = e;
-        if (lane == __ffs(peers) - 1) mine[dg] = first + __popc(peers);
+    for (int64_t b0 = lo; b0 < hi; b0 += kBatch * 32) {
+      uint64_t e[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) e[k] = b0 + k * 32 + lane < hi ? item(b0 + k * 32 + lane) : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (b0 + k * 32 >= hi) break;
+        const bool in = b0 + k * 32 + lane < hi;
+        const uint32_t dg = digit(e[k], in);
+        const uint32_t peers = same_digit(dg, in, bits);
+        const uint32_t first = in ? mine[dg] : 0u;
+        __syncwarp();
+        if (in) {
+          dst[first + __popc(peers & ((1u << lane) - 1u))] = e[k];
+          if (lane == __ffs(peers) - 1) mine[dg] = first + __popc(peers);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     // the moves are done, and no CTA still reads the totals, before the next digit (or, at the end, the exit)
     cluster_barrier();
+  }
+}
+
+// Few tokens: a token's place is the number of tokens before it in the order, counted against all of them, with nothing to
+// wait for between CTAs (37 tokens: 2.4 us, the sort 8.5).  T² comparisons and 4·T bytes of shared memory per CTA: at 8192
+// tokens no faster than the sort (13.2 against 12.7 us), and changing the SMs' split of shared memory cost as much again.
+constexpr int kRankTokens = 2048;
+constexpr int kRankThreads = 256;
+constexpr int kRankPer = 32;  // tokens of a CTA: kRankThreads / 32 warps share the comparisons of a token to a lane
+__global__ void __launch_bounds__(kRankThreads) embedding_rank_kernel(const int32_t* __restrict__ ids, void* plan, int T,
+                                                                      int64_t V, uint32_t* flag) {
+  extern __shared__ __align__(16) uint32_t keys[];  // ids of all tokens, those outside as V; padded with ~0
+  __shared__ int part[kRankThreads / 32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarpsHere = kRankThreads / 32;
+  pdl_begin();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<PlanHeader*>(plan) = PlanHeader{T, V};
+  const int padded = (T + 127) / 128 * 128;
+  for (int i0 = threadIdx.x; i0 < padded; i0 += 8 * kRankThreads) {
+    int32_t id[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) id[k] = i0 + k * kRankThreads < T ? __ldg(ids + i0 + k * kRankThreads) : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kRankThreads;
+      const bool ok = id[k] >= 0 && id[k] < V;
+      if (!ok && blockIdx.x == 0) flag_error(flag, XT_DEVERR_INDEX);
+      if (i < padded) keys[i] = i >= T ? 0xffffffffu : ok ? uint32_t(id[k]) : uint32_t(V);
+    }
+  }
+  __syncthreads();
+  const int t = int(blockIdx.x) * kRankPer + lane;
+  const uint32_t mine = t < T ? keys[t] : 0u;
+  // pieces of 128 tokens go round the warps; in those before the token's own an equal id counts
+  const int own = int(blockIdx.x) * kRankPer / 128;
+  int rank = 0;
+  for (int p = warp; p < padded / 128; p += kWarpsHere) {
+    const uint4* k4 = reinterpret_cast<const uint4*>(keys + p * 128);
+    if (p == own) {
+#pragma unroll 8
+      for (int i = 0; i < 128; ++i) {
+        const uint32_t k = keys[p * 128 + i];
+        rank += k < mine || (k == mine && p * 128 + i < t);
+      }
+    } else {
+      const uint32_t bound = p < own ? mine + 1u : mine;  // V < 2³¹: no wrap
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const uint4 k = k4[i];
+        rank += int(k.x < bound) + int(k.y < bound) + int(k.z < bound) + int(k.w < bound);
+      }
+    }
+  }
+  part[warp][lane] = rank;
+  __syncthreads();
+  if (warp == 0 && t < T) {
+#pragma unroll
+    for (int w = 1; w < kWarpsHere; ++w) rank += part[w][lane];
+    plan_entries(plan)[rank] = (uint64_t(mine) << 32) | uint32_t(t);
   }
 }
 
@@ -200,14 +283,41 @@ struct Grad {
   uint32_t* flag;
 };
 
-// A lane's 8 columns of a row: 8 neighbours, or 8 columns 32 apart where rows are not made of aligned 16 bytes.
+// A lane's 8 columns of a row: two groups of 4 neighbours 128 columns apart (so that a warp's float32 accesses fill whole
+// sectors: with 8 neighbours to a lane 131072 rows of 1024 took 251 us instead of 202), or 8 columns 32 apart where rows are not
+// made of aligned 16 bytes.
+template <typename T> struct V4;
+template <> struct V4<float> {
+  __device__ __forceinline__ static void load(const float* p, float* v) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+  __device__ __forceinline__ static void store(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <> struct V4<bf16> {
+  __device__ __forceinline__ static void load(const bf16* p, float* v) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ static void store(bf16* p, const float* v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+};
 template <typename T, bool VEC> struct Cols {
   __device__ __forceinline__ static void load(const T* row, int64_t c0, int64_t d, int lane, float (&v)[8]) {
     if constexpr (VEC) {
-      if (c0 + lane * 8 < d) V8<T>::load(row + c0 + lane * 8, v);
-      else
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const int64_t c = c0 + h * 128 + lane * 4;
+        if (c < d) V4<T>::load(row + c, v + 4 * h);
+        else
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * h + i] = 0.f;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = c0 + i * 32 + lane < d ? to_f(row[c0 + i * 32 + lane]) : 0.f;
@@ -215,7 +325,11 @@ template <typename T, bool VEC> struct Cols {
   }
   __device__ __forceinline__ static void store(T* row, int64_t c0, int64_t d, int lane, const float (&v)[8]) {
     if constexpr (VEC) {
-      if (c0 + lane * 8 < d) V8<T>::store(row + c0 + lane * 8, v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t c = c0 + h * 128 + lane * 4;
+        if (c < d) V4<T>::store(row + c, v + 4 * h);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -246,8 +360,9 @@ __device__ __forceinline__ bool plan_fits(const Grad& a) {
 }
 
 template <typename T, typename TG, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) embedding_grad_kernel(const __grid_constant__ Grad a) {
-  constexpr int U = sizeof(T) == 2 ? 8 : 4;  // rows in flight
+__global__ void __launch_bounds__(kWarps * 32, 4) embedding_grad_kernel(const __grid_constant__ Grad a) {
+  // rows in flight: two and four blocks per SM (131072 rows of 1024: 183 us; four rows 188, eight 215)
+  constexpr int U = 2;
   pdl_begin();
   if (!plan_fits(a)) return;
   const int lane = threadIdx.x & 31;
@@ -457,6 +572,11 @@ int xt_embedding_plan(const int32_t* ids, int64_t T, int64_t V, void* plan, size
              plan ? plan_bytes : size_t(0), plan_bytes_for(T));
   if (!aligned16(plan)) return fail(XT_ERR_ALIGNMENT, "%s: the plan must be 16-byte aligned", fn);
   XT_REQUIRE(T == 0 || ids, "%s: NULL pointer", fn);
+  if (T > 0 && T <= kRankTokens) {
+    launch(embedding_rank_kernel, unsigned(ceil_div(T, kRankPer)), kRankThreads, size_t((T + 127) / 128 * 512),
+           as_stream(stream), ids, plan, int(T), V, errflag());
+    return check_launch(fn);
+  }
   int bits = 1;
   while ((V >> bits) != 0) ++bits;  // ids 0 .. V − 1, and V for those outside
   const int passes = int(ceil_div(bits, kDigitBits));

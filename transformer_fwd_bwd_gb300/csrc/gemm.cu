@@ -244,9 +244,9 @@ __global__ void splitk_reduce(const float* __restrict__ part, int splits, int64_
   }
 }
 
-// An output as the epilogue's TMA stores see it: boxes of 32 rows × 128 bytes, 128-byte swizzle.
+// An output as the epilogue's TMA stores see it: boxes of 32 rows × 128 (or 64) bytes, swizzled over their width.
 static int make_output_map(CUtensorMap* tm, void* base, bool bf16, int64_t M, int64_t N, int64_t ldc, int bi, int bo,
-                           int64_t s_inner, int64_t s_outer) {
+                           int64_t s_inner, int64_t s_outer, int width = 128) {
   auto enc = encode_fn();
   if (!enc) return fail(XT_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const int64_t e = bf16 ? 2 : 4;
@@ -254,10 +254,11 @@ static int make_output_map(CUtensorMap* tm, void* base, bool bf16, int64_t M, in
   cuuint64_t dims[4] = {cuuint64_t(N), cuuint64_t(M), cuuint64_t(bi), cuuint64_t(bo)};
   cuuint64_t strides[3] = {cuuint64_t(row_bytes), cuuint64_t(bi > 1 ? s_inner * e : row_bytes),
                            cuuint64_t(bo > 1 ? s_outer * e : row_bytes)};
-  cuuint32_t box[4] = {uint32_t(128 / e), 32, 1, 1};
+  cuuint32_t box[4] = {uint32_t(width / e), 32, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(XT_ERR_CUDA, "cuTensorMapEncodeTiled (C) failed (%d)", int(r));
   return XT_OK;
@@ -400,7 +401,7 @@ int run_gated(const Problem& pb, cudaStream_t s) {
   XT_TRY(make_operand_map(&ta, pb.A, kBf16, BM, k_atoms(cg)));
   XT_TRY(make_operand_map(&tb, pb.B, kBf16, bn / cg, k_atoms(cg)));
   if (fwd) XT_TRY(make_output_map(&tc, pb.C, true, pb.M, pb.N, pb.N, 1, 1, 0, 0));
-  if (pb.C2) XT_TRY(make_output_map(&tc2, pb.C2, true, pb.M, pb.N, 2 * pb.N, 2, 1, pb.N, 0));
+  if (pb.C2) XT_TRY(make_output_map(&tc2, pb.C2, true, pb.M, pb.N, 2 * pb.N, 2, 1, pb.N, 0, fwd ? 128 : 64));
   Params p{};
   p.M = int(pb.M);
   p.N = int(pb.N);

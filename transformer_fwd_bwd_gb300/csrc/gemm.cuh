@@ -87,7 +87,7 @@ template <int KIND, int BN, bool A_MN, bool B_MN, int ACT = 0, int CG = 1, int M
 int launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tc2,
                const Params& p, int grid, cudaStream_t s) {
   auto k = gemm_kernel<KIND, BN, A_MN, B_MN, ACT, CG, MC>;
-  constexpr int smem = Cfg<KIND, BN, CG>::SMEM;
+  constexpr int smem = Cfg<KIND, BN, CG>::SMEM, threads = threads_of(ACT);
   static bool attr_set = false;  // per instantiation; idempotent if raced
   if (!attr_set) {
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -98,9 +98,9 @@ int launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& 
   }
   if constexpr (CG == 2) {
     if (grid % (CG * MC)) return fail(XT_ERR_INVALID_ARG, "gemm: clustered launch needs whole clusters");
-    launch_clustered(k, grid, kThreads, smem, s, CG * MC, ta, tb, tc, tc2, p);
+    launch_clustered(k, grid, threads, smem, s, CG * MC, ta, tb, tc, tc2, p);
   } else {
-    launch(k, grid, kThreads, smem, s, ta, tb, tc, tc2, p);
+    launch(k, grid, threads, smem, s, ta, tb, tc, tc2, p);
   }
   return check_launch("gemm kernel");
 }

@@ -204,6 +204,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {
   uint32_t v;
@@ -544,6 +549,10 @@ __device__ __forceinline__ void sk_fixup(uint32_t tacc, const Params& p, int fir
 //   kGateBwd*: the product is dh; g and u are read (bf16, aux) and dg = dh·u·act'(g), du = dh·act(g) stored (the two
 //     batches of the C2 map), so that dh never leaves the SM.
 constexpr int kGateFwdSilu = 3, kGateFwdGelu = 4, kGateBwdSilu = 5, kGateBwdGelu = 6;
+// The backward's epilogue runs some 25 (silu) to 40 (gelu) instructions for each of a tile's values: eight warps, two to a
+// scheduler (with four 12001 x 5464 x 2048 gelu took 433 us, 8192 x 2048 x 768 silu 56).
+__host__ __device__ constexpr int epilogue_warps(int act) { return act == kGateBwdSilu || act == kGateBwdGelu ? 8 : 4; }
+__host__ __device__ constexpr int threads_of(int act) { return 64 + 32 * epilogue_warps(act); }
 
 // act(g) and act'(g) of N values (silu: σ(g) by one exponential and one reciprocal; gelu: as gelu_batch).
 template <bool GELU, int N>
@@ -598,7 +607,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // barrier, which then counts two arrivals; the MMAs' commits free a stage in all four CTAs
 // (each empty barrier counts one commit per pair).
 template <int KIND, int BN, bool A_MN, bool B_MN, int ACT = 0, int CG = 1, int MC = 1>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(ACT), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmC2, const Params p) {
   constexpr bool GATE_F = ACT == kGateFwdSilu || ACT == kGateFwdGelu, GATE_B = ACT == kGateBwdSilu || ACT == kGateBwdGelu;
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), 4 * CG);
+      mbar_init(smem_u32(&tempty[b]), epilogue_warps(ACT) * CG);
     }
     mbar_init(smem_u32(mma_done), 1);
     *abort_flag = 0;
@@ -884,21 +893,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ti.skip) continue;
       const int row = ti.m0 + q * 32 + lane;
       const bool empty_k = ti.kb_end <= ti.kb_begin;
-      // 32 gate (up = 0) or up columns of this lane's row of aux from x on; 0 outside
-      auto aux_row = [&](uint4 (&v)[4], int x, int up) {
-        const bf16* ap = p.aux + int64_t(row < p.M ? row : 0) * p.ld_aux + int64_t(up) * p.gate + x;
+      // 32 gate (up = 0) or up columns of the warp's 32 rows of aux from x on, 0 outside: v[j] is 16 bytes of row
+      // 8·j + lane/4 (with a row to a lane every load touched 32 lines, and the loads took as long as the product:
+      // 8192 x 2048 x 768 57 us instead of 51, 12001 x 5464 x 2048 389 instead of 303; asking L2 for the next tile's lines ahead
+      // of time made it 330)
+      auto aux_rows = [&](uint4 (&v)[4], int x, int up) {
+        const int y0 = ti.m0 + q * 32 + (lane >> 2), xc = x + (lane & 3) * 8;
+        const bf16* ap = p.aux + int64_t(y0) * p.ld_aux + int64_t(up) * p.gate + xc;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[j] = row < p.M && x + 8 * j < p.N ? __ldg(reinterpret_cast<const uint4*>(ap) + j) : make_uint4(0u, 0u, 0u, 0u);
+          v[j] = y0 + 8 * j < p.M && xc < p.N ? __ldg(reinterpret_cast<const uint4*>(ap + int64_t(8 * j) * p.ld_aux))
+                                              : make_uint4(0u, 0u, 0u, 0u);
       };
-      uint4 ga[4], ua[4];
-      if constexpr (GATE_B) {  // in flight while the product is finished
-        aux_row(ga, ti.n0, 0);
-        aux_row(ua, ti.n0, 1);
+      // the backward's warps take half of the columns each
+      const int half0 = GATE_B ? ((warp - 2) >> 2) * (BN / 2) : 0;
+      uint4 ga[2][4], ua[2][4];
+      if constexpr (GATE_B) {  // two pieces in flight while the product is finished
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          aux_rows(ga[c], ti.n0 + half0 + c * 32, 0);
+          aux_rows(ua[c], ti.n0 + half0 + c * 32, 1);
+        }
       }
       // stream-K piece kind: 1 = a later part of the tile (partial to its slot), 2 = the tile's
       // first k-blocks with later parts in units unit + 1 .. sk_last (adds their partials)
-      const int kind = kb0 > 0 ? 1 : (kb0 == 0 && kb1 < p.kb_tile) ? 2 : 0;
+      // (the gated epilogues run whole tiles only)
+      const int kind = GATE_F || GATE_B ? 0 : kb0 > 0 ? 1 : (kb0 == 0 && kb1 < p.kb_tile) ? 2 : 0;
       if (!empty_k) {
         const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[ab]), aphase, p.wait_ns));
         if (!ok) {
@@ -1015,74 +1035,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if constexpr (GATE_B) {
-        // ---- 32 columns at a time: dh from the accumulator, g and u one piece ahead from memory; dg and du of two pieces
-        // staged in the warp's two buffers
+        // ---- 32 columns at a time: dh from the accumulator, g and u two pieces ahead from memory; dg and du staged in
+        // a box of 32 rows × 64 bytes each (64-byte swizzle).  8 columns in registers at a time: what is spilled goes to
+        // L2 and back here, beside 224 KB of shared memory (12 to 48 spilled registers: 8192 x 2048 x 768 79 us).
         const int y = ti.m0 + q * 32;
-        const uint32_t buf = smem_u32(staging) + uint32_t(q * 2 * 4096);
+        const uint32_t box = smem_u32(staging) + uint32_t((warp - 2) * 4096);
+        const uint32_t at = uint32_t(lane) * 64;
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          const int x = ti.n0 + c * 32;
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld32(tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * BN + c * 32), r);
-          tmem_ld_wait();
-          if (c == BN / 32 - 1) {  // the accumulator is read: the next tile's products may start
-            tc_fence_before();
+        for (int c2 = 0; c2 < BN / 64; c2 += 2) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const int c = c2 + o, x = ti.n0 + half0 + c * 32;
+            uint32_t r[32];
             __syncwarp();
-            if (lane == 0) release_acc(ab);
-          }
-          if (y >= p.M || x - (c & 1) * 32 >= p.N) continue;
-          uint4 gn[4], un[4];
-          if (c + 1 < BN / 32) {
-            aux_row(gn, x + 32, 0);
-            aux_row(un, x + 32, 1);
-          }
-          if ((c & 1) == 0) {
-            if (lane == 0) bulk_wait_read_0();
+            tmem_ld32(tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * BN + half0 + c * 32), r);
+            tmem_ld_wait();
+            if (c == BN / 64 - 1) {  // the accumulator is read: the next tile's products may start
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) release_acc(ab);
+            }
+            if (y >= p.M || x >= p.N) continue;
+            if (lane == 0) bulk_wait_read_0();  // the last piece's boxes have been read
             __syncwarp();
-          }
+            // g and u pass through the boxes, to this lane's row
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float g[16], u[16], a[16], da[16];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float t[8];
-              Vec<bf16>::unpack(ga[2 * h + e], t);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) g[8 * e + k] = t[k];
-              Vec<bf16>::unpack(ua[2 * h + e], t);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) u[8 * e + k] = t[k];
+            for (int j = 0; j < 4; ++j) {
+              const int rw = 8 * j + (lane >> 2);
+              const uint32_t to = box + uint32_t(rw) * 64 + (uint32_t((lane & 3) ^ ((rw >> 1) & 3)) << 4);
+              st_shared_v4(to, ga[o][j].x, ga[o][j].y, ga[o][j].z, ga[o][j].w);
+              st_shared_v4(to + 2048, ua[o][j].x, ua[o][j].y, ua[o][j].z, ua[o][j].w);
             }
-            gate_batch<ACT == kGateBwdGelu>(g, a, da);
-            uint32_t dg[8], du[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float d0 = __uint_as_float(r[16 * h + 2 * k]), d1 = __uint_as_float(r[16 * h + 2 * k + 1]);
-              dg[k] = pack_bf16(d0 * u[2 * k] * da[2 * k], d1 * u[2 * k + 1] * da[2 * k + 1]);
-              du[k] = pack_bf16(d0 * a[2 * k], d1 * a[2 * k + 1]);
+            __syncwarp();
+            if (c + 2 < BN / 64) {
+              aux_rows(ga[o], x + 64, 0);
+              aux_rows(ua[o], x + 64, 1);
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = (c & 1) * 4 + 2 * h + e;
-              const uint32_t off = uint32_t(lane) * 128 + (uint32_t(j ^ (lane & 7)) << 4);
-              st_shared_v4(buf + off, dg[4 * e], dg[4 * e + 1], dg[4 * e + 2], dg[4 * e + 3]);
-              st_shared_v4(buf + 4096 + off, du[4 * e], du[4 * e + 1], du[4 * e + 2], du[4 * e + 3]);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t off = at + (uint32_t(j ^ ((lane >> 1) & 3)) << 4);
+              float g[8], u[8], a[8], da[8];
+              Vec<bf16>::unpack(ld_shared_v4(box + off), g);
+              Vec<bf16>::unpack(ld_shared_v4(box + 2048 + off), u);
+              gate_batch<ACT == kGateBwdGelu>(g, a, da);
+              uint32_t dg[4], du[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float d0 = __uint_as_float(r[8 * j + 2 * k]), d1 = __uint_as_float(r[8 * j + 2 * k + 1]);
+                dg[k] = pack_bf16(d0 * u[2 * k] * da[2 * k], d1 * u[2 * k + 1] * da[2 * k + 1]);
+                du[k] = pack_bf16(d0 * a[2 * k], d1 * a[2 * k + 1]);
+              }
+              st_shared_v4(box + off, dg[0], dg[1], dg[2], dg[3]);
+              st_shared_v4(box + 2048 + off, du[0], du[1], du[2], du[3]);
             }
-          }
-          if (c & 1) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_4d(&tmC2, buf, x - 32, y, 0, 0);
-              tma_store_4d(&tmC2, buf + 4096, x - 32, y, 1, 0);
+              tma_store_4d(&tmC2, box, x, y, 0, 0);
+              tma_store_4d(&tmC2, box + 2048, x, y, 1, 0);
               bulk_commit();
             }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ga[j] = gn[j];
-            ua[j] = un[j];
           }
         }
         if (++ab == 2) { ab = 0; aphase ^= 1; }
