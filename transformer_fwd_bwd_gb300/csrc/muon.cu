@@ -45,9 +45,10 @@ constexpr int kAtom = 64, kAtoms = kBk / kAtom;
 constexpr int kOperandBytes = BM * kBk * 2;  // each CTA stages 128 rows of either operand
 constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStagingBytes = 4 * 2 * 4096;
+constexpr int kEpilogueWarps = 8;
+constexpr int kStagingBytes = kEpilogueWarps * 4096;
 constexpr int kSmem = 1024 + kStages * kStageBytes + kStagingBytes + 256;
-constexpr int kProductThreads = 192;
+constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
 
 // Matrices of one shape: C = alpha·P Q + beta·D as two f16 terms.
 struct Group {
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), 4 * kCg);
+      mbar_init(smem_u32(&tempty[b]), kEpilogueWarps * kCg);
     }
     mbar_init(smem_u32(mma_done), 1);
     *abort_flag = 0;
@@ -224,103 +225,122 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
     }
   } else {
     // -------------------------------------------------------------------- epilogue
-    const int q = warp & 3;  // TMEM lanes [32q, 32q + 32)
+    // Two warps to a quadrant of tensor memory's lanes, half of the columns each, 32 columns at a time: D's two terms
+    // come two pieces ahead, whole sectors to a load (row 8·j + lane/4, 16 bytes of 64), pass through the warp's two
+    // boxes (32 rows × 64 bytes, 64-byte swizzle) to the lanes' own rows, and the result leaves from the same boxes.
+    // (Four warps that read D with a row to a lane: 20 us for a single tile, 4.1 ms a step of the 12-layer stack.)
+    const int q = warp & 3, half0 = ((warp - 2) >> 2) * (kTile / 2);
     int ab = 0;
     uint32_t aphase = 0;
-    const uint32_t buf = smem_u32(staging) + uint32_t(q * 2 * 4096);
+    const uint32_t box = smem_u32(staging) + uint32_t((warp - 2) * 4096);
     const uint32_t tempty0 = smem_u32(&tempty[0]), tempty_at = mapa_shared(tempty0, 0);
     for (int t = unit; t < a.tiles; t += units) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
       const Place w = place_of(a, t);
       const Group& g = a.g[w.g];
-      const int y = w.m * kTile + rank * BM + q * 32, row = y + lane, n0 = w.n * kTile;
+      const int y = w.m * kTile + rank * BM + q * 32, row = y + lane, x0 = w.n * kTile + half0;
+      const int M = g.M, N = g.N, ld = g.ld;
       const bool with_d = g.d != nullptr;
-      const __half* d = with_d ? g.d + w.batch * g.d_batch + int64_t(row < g.M ? row : 0) * g.ld : nullptr;
-      // 32 columns of D's two terms in this lane's row; 0 outside (rows of D are padded to whole 16 bytes)
+      const float alpha = g.alpha, beta = g.beta;
+      const int dr = y + (lane >> 2), dc = (lane & 3) * 8;
+      const __half* d = with_d ? g.d + w.batch * g.d_batch + int64_t(dr) * ld + dc : nullptr;
+      const int64_t d_term = g.d_term;
       auto load_d = [&](uint4 (&hi)[4], uint4 (&lo)[4], int x) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool in = with_d && row < g.M && x + 8 * j < g.N;
-          hi[j] = in ? __ldg(reinterpret_cast<const uint4*>(d + x) + j) : make_uint4(0u, 0u, 0u, 0u);
-          lo[j] = in ? __ldg(reinterpret_cast<const uint4*>(d + g.d_term + x) + j) : make_uint4(0u, 0u, 0u, 0u);
+          const bool in = with_d && dr + 8 * j < M && x + dc < N;
+          const __half* p = d + int64_t(8 * j) * ld + x;
+          hi[j] = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+          lo[j] = in ? __ldg(reinterpret_cast<const uint4*>(p + d_term)) : make_uint4(0u, 0u, 0u, 0u);
         }
       };
-      uint4 hi[4], lo[4];
-      load_d(hi, lo, n0);
+      uint4 hi[2][4], lo[2][4];
+      load_d(hi[0], lo[0], x0);
+      load_d(hi[1], lo[1], x0 + 32);
       const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[ab]), aphase, a.wait_ns));
       if (!ok) {
         if (lane == 0) give_up();
         break;
       }
       tc_fence_after();
-      const bool mirror = g.sym && w.m != w.n;
+      const bool mirror = g.sym && w.m != w.n && row < M;
+      __half* cm = g.c + w.batch * g.c_batch + row;  // the mirrored element (x + k, row)
+      const int64_t c_term = g.c_term;
 #pragma unroll 1
-      for (int c = 0; c < kTile / 32; ++c) {
-        const int x = n0 + c * 32;
-        uint32_t r[32];
-        __syncwarp();
-        tmem_ld32(tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * kTile + c * 32), r);
-        tmem_ld_wait();
-        if (c == kTile / 32 - 1) {  // the accumulator is read: the next tile's products may start
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (rank) mbar_arrive_cluster(tempty_at + uint32_t(ab * 8));
-            else mbar_arrive(tempty0 + uint32_t(ab * 8));
-          }
-        }
-        if (y >= g.M || x - (c & 1) * 32 >= g.N) continue;
-        uint4 hn[4], ln[4];
-        if (c + 1 < kTile / 32) load_d(hn, ln, x + 32);
-        if ((c & 1) == 0) {
-          if (lane == 0) bulk_wait_read_0();
-          __syncwarp();
-        }
-        __half* cm = g.c + w.batch * g.c_batch + row;  // the mirrored element (x + k, row)
+      for (int c2 = 0; c2 < kTile / 64; c2 += 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t dh[4] = {hi[j].x, hi[j].y, hi[j].z, hi[j].w}, dl[4] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w};
-          uint32_t oh[4], ol[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 vh = __half22float2(*reinterpret_cast<const __half2*>(&dh[e]));
-            const float2 vl = __half22float2(*reinterpret_cast<const __half2*>(&dl[e]));
-            const float v0 = fmaf(g.beta, vh.x + vl.x, g.alpha * __uint_as_float(r[8 * j + 2 * e]));
-            const float v1 = fmaf(g.beta, vh.y + vl.y, g.alpha * __uint_as_float(r[8 * j + 2 * e + 1]));
-            const __half2 h = __floats2half2_rn(v0, v1);
-            const float2 back = __half22float2(h);
-            const __half2 l = __floats2half2_rn(v0 - back.x, v1 - back.y);
-            oh[e] = *reinterpret_cast<const uint32_t*>(&h);
-            ol[e] = *reinterpret_cast<const uint32_t*>(&l);
-            if (mirror && row < g.M) {
-              const int k = x + 8 * j + 2 * e;
-              if (k < g.N) {
-                cm[int64_t(k) * g.ld] = __low2half(h);
-                cm[int64_t(k) * g.ld + g.c_term] = __low2half(l);
-              }
-              if (k + 1 < g.N) {
-                cm[int64_t(k + 1) * g.ld] = __high2half(h);
-                cm[int64_t(k + 1) * g.ld + g.c_term] = __high2half(l);
-              }
+        for (int o = 0; o < 2; ++o) {
+          const int c = c2 + o, x = x0 + c * 32;
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(tbase + (uint32_t(q * 32) << 16) + uint32_t(ab * kTile + half0 + c * 32), r);
+          tmem_ld_wait();
+          if (c == kTile / 64 - 1) {  // the accumulator is read: the next tile's products may start
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank) mbar_arrive_cluster(tempty_at + uint32_t(ab * 8));
+              else mbar_arrive(tempty0 + uint32_t(ab * 8));
             }
           }
-          const uint32_t off = uint32_t(lane) * 128 + (uint32_t(((c & 1) * 4 + j) ^ (lane & 7)) << 4);
-          st_shared_v4(buf + off, oh[0], oh[1], oh[2], oh[3]);
-          st_shared_v4(buf + 4096 + off, ol[0], ol[1], ol[2], ol[3]);
-        }
-        if (c & 1) {
+          if (y >= M || x >= N) continue;
+          if (lane == 0) bulk_wait_read_0();  // the last piece's boxes have been read
+          __syncwarp();
+          if (with_d) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int rw = 8 * j + (lane >> 2);
+              const uint32_t to = box + uint32_t(rw) * 64 + (uint32_t((lane & 3) ^ ((rw >> 1) & 3)) << 4);
+              st_shared_v4(to, hi[o][j].x, hi[o][j].y, hi[o][j].z, hi[o][j].w);
+              st_shared_v4(to + 2048, lo[o][j].x, lo[o][j].y, lo[o][j].z, lo[o][j].w);
+            }
+            __syncwarp();
+            if (c + 2 < kTile / 64) load_d(hi[o], lo[o], x + 64);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = box + uint32_t(lane) * 64 + (uint32_t(j ^ ((lane >> 1) & 3)) << 4);
+            uint4 vh4 = make_uint4(0u, 0u, 0u, 0u), vl4 = vh4;
+            if (with_d) {
+              vh4 = ld_shared_v4(at);
+              vl4 = ld_shared_v4(at + 2048);
+            }
+            const uint32_t dh[4] = {vh4.x, vh4.y, vh4.z, vh4.w}, dl[4] = {vl4.x, vl4.y, vl4.z, vl4.w};
+            uint32_t oh[4], ol[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 vh = __half22float2(*reinterpret_cast<const __half2*>(&dh[e]));
+              const float2 vl = __half22float2(*reinterpret_cast<const __half2*>(&dl[e]));
+              const float v0 = fmaf(beta, vh.x + vl.x, alpha * __uint_as_float(r[8 * j + 2 * e]));
+              const float v1 = fmaf(beta, vh.y + vl.y, alpha * __uint_as_float(r[8 * j + 2 * e + 1]));
+              const __half2 h = __floats2half2_rn(v0, v1);
+              const float2 back = __half22float2(h);
+              const __half2 l = __floats2half2_rn(v0 - back.x, v1 - back.y);
+              oh[e] = *reinterpret_cast<const uint32_t*>(&h);
+              ol[e] = *reinterpret_cast<const uint32_t*>(&l);
+              if (mirror) {
+                const int k = x + 8 * j + 2 * e;
+                __half* m = cm + int64_t(k) * ld;
+                if (k < N) {
+                  m[0] = __low2half(h);
+                  m[c_term] = __low2half(l);
+                }
+                if (k + 1 < N) {
+                  m[ld] = __high2half(h);
+                  m[ld + c_term] = __high2half(l);
+                }
+              }
+            }
+            st_shared_v4(at, oh[0], oh[1], oh[2], oh[3]);
+            st_shared_v4(at + 2048, ol[0], ol[1], ol[2], ol[3]);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_4d(&g.tc, buf, x - 32, y, w.batch, 0);
-            tma_store_4d(&g.tc, buf + 4096, x - 32, y, w.batch, 1);
+            tma_store_4d(&g.tc, box, x, y, w.batch, 0);
+            tma_store_4d(&g.tc, box + 2048, x, y, w.batch, 1);
             bulk_commit();
           }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          hi[j] = hn[j];
-          lo[j] = ln[j];
         }
       }
       if (++ab == 2) { ab = 0; aphase ^= 1; }
@@ -574,7 +594,7 @@ int plan(Layout& l, const char* fn, int n, const int64_t* rows, const int64_t* c
   return XT_OK;
 }
 
-// A matrix batch [2 terms][count][rows][ld] as the product kernel reads (operand boxes) or stores it (32 × 64 boxes).
+// A matrix batch [2 terms][count][rows][ld] as the product kernel reads (boxes 64 wide) or stores it (32 × 32 boxes).
 int make_map(CUtensorMap* tm, __half* base, int64_t rows, int64_t cols, int64_t ld, int count, int64_t term, uint32_t bx,
              uint32_t by) {
   auto enc = encode_fn();
@@ -583,7 +603,8 @@ int make_map(CUtensorMap* tm, __half* base, int64_t rows, int64_t cols, int64_t 
   cuuint64_t strides[3] = {cuuint64_t(ld * 2), cuuint64_t(rows * ld * 2), cuuint64_t(term * 2)};
   cuuint32_t box[4] = {bx, by, 1, 1}, estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, bx == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(XT_ERR_CUDA, "cuTensorMapEncodeTiled (muon) failed (%d)", int(r));
   return XT_OK;
@@ -601,10 +622,10 @@ int products(const Layout& l, int first, int count, int which, int flip, __half*
     __half *A = ws + sh.a, *B = ws + sh.b;
     const bool tall = sh.rows > sh.cols;
     auto square = [&](CUtensorMap* tm, __half* p, uint32_t by) {
-      return make_map(tm, p, sh.k, sh.k, sh.ldk, sh.count, sh.a_term, kAtom, by);
+      return make_map(tm, p, sh.k, sh.k, sh.ldk, sh.count, sh.a_term, by == 32 ? 32 : kAtom, by);
     };
     auto matrix = [&](CUtensorMap* tm, __half* p, uint32_t by) {
-      return make_map(tm, p, sh.rows, sh.cols, sh.ld, sh.count, sh.x_term, kAtom, by);
+      return make_map(tm, p, sh.rows, sh.cols, sh.ld, sh.count, sh.x_term, by == 32 ? 32 : kAtom, by);
     };
     int64_t K;
     if (which == 0) {
