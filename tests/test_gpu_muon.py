@@ -103,6 +103,11 @@ def test_more_matrices_than_a_table():
     check([(24, 48)] * 150 + [(48, 24)] * 20, config())
 
 
+def test_wide_tiles():
+    """Enough matrices for 256 x 256 tiles, which pairs of CTAs share, in all three products."""
+    check([(300, 700)] * 14 + [(769, 264)] * 8 + [(256, 256)] * 5, config(), shadow="bf16")
+
+
 @pytest.mark.parametrize("kw", [dict(nesterov=0), dict(momentum=0.0), dict(steps=1), dict(steps=2), dict(steps=8),
                                 dict(weight_decay=0.0, grad_scale=1.0), dict(lr=0.0)])
 def test_settings(kw):

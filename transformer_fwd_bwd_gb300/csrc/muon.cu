@@ -38,8 +38,8 @@ constexpr int kMaxMatrices = 128;  // of an elementwise launch (its table travel
 
 // ------------------------------------------------------------------------------ products
 
-constexpr int kCg = 2;             // CTAs to a tile
-constexpr int kTile = BM * kCg;    // tile edge
+// A tile's edge is BM for each of the CG CTAs that share it: pairs of CTAs with 256 × 256 tiles, or single ones with
+// 128 × 128 where the others would leave most of the GPU idle (see products()).
 constexpr int kBk = 128;           // K elements per stage: two swizzle atoms
 constexpr int kAtom = 64, kAtoms = kBk / kAtom;
 constexpr int kOperandBytes = BM * kBk * 2;  // each CTA stages 128 rows of either operand
@@ -95,8 +95,10 @@ __device__ __forceinline__ Place place_of(const Products& a, int t) {
   return w;
 }
 
+template <int kCg>
 __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const __grid_constant__ Products a) {
-  const int rank = int(cluster_ctarank()) & 1;
+  constexpr int kTile = BM * kCg;
+  const int rank = kCg == 2 ? int(cluster_ctarank()) & 1 : 0;
   const int unit = int(blockIdx.x) / kCg, units = int(gridDim.x) / kCg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -133,7 +135,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
     tmem_relinquish_cg<kCg>();
   }
   tc_fence_before();
-  cluster_sync_all();
+  if constexpr (kCg == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   pdl_wait();
@@ -157,19 +160,23 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
           if (*abort_flag) break;
           if (!mbar_wait_spin(smem_u32(&empty[stage]), phase ^ 1, a.wait_ns)) { give_up(); break; }
           if (rank == 0) mbar_expect_tx(smem_u32(&full[stage]), kCg * kStageBytes);
-          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+          const uint32_t fb = kCg == 2 ? mapa_shared(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]);
+          auto load = [&](uint32_t dst, const CUtensorMap* tm, int c0, int c1, int z) {
+            if constexpr (kCg == 2) tma_load_4d_pair(dst, tm, fb, c0, c1, w.batch, z);
+            else tma_load_4d(dst, tm, fb, c0, c1, w.batch, z);
+          };
           const uint32_t p_s = smem_u32(smem + stage * kStageBytes), q_s = p_s + kOperandBytes;
           const int term = kb / g.k_blocks, k0 = (kb - term * g.k_blocks) * kBk;
           const int zp = term == 1, zq = term == 0;  // hi·lo, lo·hi, hi·hi
 #pragma unroll
           for (int c = 0; c < kAtoms; ++c) {
-            if (g.p_mn) tma_load_4d_pair(p_s + c * (kBk * 128), &g.tp, fb, m0 + c * kAtom, k0, w.batch, zp);
-            else tma_load_4d_pair(p_s + c * (BM * 128), &g.tp, fb, k0 + c * kAtom, m0, w.batch, zp);
+            if (g.p_mn) load(p_s + c * (kBk * 128), &g.tp, m0 + c * kAtom, k0, zp);
+            else load(p_s + c * (BM * 128), &g.tp, k0 + c * kAtom, m0, zp);
           }
 #pragma unroll
           for (int c = 0; c < kAtoms; ++c) {
-            if (g.q_mn) tma_load_4d_pair(q_s + c * (kBk * 128), &g.tq, fb, n0 + c * kAtom, k0, w.batch, zq);
-            else tma_load_4d_pair(q_s + c * (BM * 128), &g.tq, fb, k0 + c * kAtom, n0, w.batch, zq);
+            if (g.q_mn) load(q_s + c * (kBk * 128), &g.tq, n0 + c * kAtom, k0, zq);
+            else load(q_s + c * (BM * 128), &g.tq, k0 + c * kAtom, n0, zq);
           }
           ++issued;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
     int ab = 0;
     uint32_t aphase = 0;
     const uint32_t box = smem_u32(staging) + uint32_t((warp - 2) * 4096);
-    const uint32_t tempty0 = smem_u32(&tempty[0]), tempty_at = mapa_shared(tempty0, 0);
+    const uint32_t tempty0 = smem_u32(&tempty[0]), tempty_at = kCg == 2 ? mapa_shared(tempty0, 0) : tempty0;
     for (int t = unit; t < a.tiles; t += units) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
       const Place w = place_of(a, t);
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
   }
   __syncthreads();
   // neither CTA releases tensor memory or exits while the other may still signal its barriers or read its operands
-  cluster_sync_all();
+  if constexpr (kCg == 2) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<kCg>(tbase, 2 * kTile);
@@ -614,6 +621,16 @@ int make_map(CUtensorMap* tm, __half* base, int64_t rows, int64_t cols, int64_t 
 int products(const Layout& l, int first, int count, int which, int flip, __half* ws, cudaStream_t s) {
   Products a{};
   a.groups = count;
+  const int pairs = pair_capacity();
+  if (pairs < 1) return fail(XT_ERR_CUDA, "xt_muon_step: no CTA pair can be resident");
+  // 256 × 256 tiles where they fill half of the pairs
+  int64_t big = 0;
+  for (int i = 0; i < count; ++i) {
+    const Shape& sh = l.shape[first + i];
+    const int64_t nk = ceil_div(sh.k, 2 * BM);
+    big += sh.count * (which < 2 ? nk * (nk + 1) / 2 : ceil_div(sh.rows, 2 * BM) * ceil_div(sh.cols, 2 * BM));
+  }
+  const int cg = 2 * big >= pairs ? 2 : 1, tile = BM * cg;
   for (int i = 0; i < count; ++i) {
     const Shape& sh = l.shape[first + i];
     Group& g = a.g[i];
@@ -667,8 +684,8 @@ int products(const Layout& l, int first, int count, int which, int flip, __half*
     g.c_term = g.d_term = which < 2 ? sh.a_term : sh.x_term;
     g.c_batch = g.d_batch = int64_t(g.M) * g.ld;
     g.k_blocks = int(ceil_div(K, kBk));
-    g.num_m = int(ceil_div(g.M, kTile));
-    g.num_n = int(ceil_div(g.N, kTile));
+    g.num_m = int(ceil_div(g.M, tile));
+    g.num_n = int(ceil_div(g.N, tile));
     g.tile0 = a.tiles;
     const int64_t per = g.sym ? int64_t(g.num_m) * (g.num_m + 1) / 2 : int64_t(g.num_m) * g.num_n;
     if (a.tiles + per * sh.count >= (int64_t(1) << 30)) return fail(XT_ERR_UNSUPPORTED, "xt_muon_step: too many tiles");
@@ -677,17 +694,19 @@ int products(const Layout& l, int first, int count, int which, int flip, __half*
   }
   a.flag = errflag();
   a.wait_ns = wait_limit_ns();
-  const int units = pair_capacity();
-  if (units < 1) return fail(XT_ERR_CUDA, "xt_muon_step: no CTA pair can be resident");
   static std::atomic<uint64_t> set{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("xt_muon_step");
   if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
-    if (cudaFuncSetAttribute(muon_product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(muon_product_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(muon_product_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
       return check_launch("xt_muon_step: shared memory attribute");
     if (dev < 64) set.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  launch_clustered(muon_product_kernel, kCg * (a.tiles < units ? a.tiles : units), kProductThreads, kSmem, s, kCg, a);
+  if (cg == 2)
+    launch_clustered(muon_product_kernel<2>, 2 * (a.tiles < pairs ? a.tiles : pairs), kProductThreads, kSmem, s, 2, a);
+  else
+    launch(muon_product_kernel<1>, a.tiles < num_sms() ? a.tiles : num_sms(), kProductThreads, kSmem, s, a);
   return check_launch("xt_muon_step (product)");
 }
 
