@@ -170,18 +170,32 @@ class NativeBlock:
 
     # -------------------------------------------------------------------------- optimizer
 
-    def init_optimizer(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, max_grad_norm=1.0, state_bits=32):
+    def init_optimizer(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, max_grad_norm=1.0, state_bits=32,
+                       matrices="adamw", muon_lr=0.02, muon_momentum=0.95, muon_rms=0.2):
         """AdamW state ([BP] § Optimiser-tillståndet): float32 master weights (the parameters
         themselves when they are float32; for bf16 parameters a float32 copy, the bf16 tensors
         then being the working copy every step rewrites), first and second moments at zero, in
-        float32 or (state_bits=8) as 8-bit codes with a scale per 256 elements (xt_adamw8_step)."""
+        float32 or (state_bits=8) as 8-bit codes with a scale per 256 elements (xt_adamw8_step).
+
+        matrices="muon": the layers' weight matrices (Wqkv, Wo, Wup, Wdown) take xt_muon_step with muon_lr,
+        muon_momentum, muon_rms and weight_decay instead, and keep one float32 momentum each; embeddings, positions and
+        norms stay with AdamW, whose gradient norm and clipping then cover those alone (Muon's update has a norm of its
+        own, whatever the gradient's)."""
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
+        if matrices not in ("adamw", "muon"):
+            raise ValueError("matrices must be 'adamw' or 'muon'")
         if self.gdt != torch.float32:
             raise ValueError("the optimizer reads float32 gradients (grad_dtype='f32')")
         self.hyper = dict(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
                           max_grad_norm=max_grad_norm)
-        self._names = list(self.p)
+        self._muon = [k for k in self.p if matrices == "muon" and k.split(".")[-1] in ("Wqkv", "Wo", "Wup", "Wdown")]
+        self._names = [k for k in self.p if k not in set(self._muon)]
+        self.muon = dict(lr=muon_lr, momentum=muon_momentum, weight_decay=weight_decay, rms=muon_rms)
+        self.momentum = {k: torch.zeros(self.p[k].shape, dtype=torch.float32, device=self.device) for k in self._muon}
+        self._muon_ws = None
+        if self._muon:
+            self._muon_ws = xt.muon_workspace([tuple(self.p[k].shape) for k in self._muon], self.device)
         self.master = {k: (v if v.dtype == torch.float32 else v.float().contiguous()) for k, v in self.p.items()}
         self.state_bits = state_bits
         self.opt_step = 0
@@ -191,8 +205,8 @@ class NativeBlock:
             self.state8 = xt.adamw8_state([self.p[k] for k in self._names])
             self._opt_ws = xt.adamw8_workspace(numels, self.device)
             return
-        self.m = {k: torch.zeros(v.shape, dtype=torch.float32, device=self.device) for k, v in self.p.items()}
-        self.v = {k: torch.zeros(v.shape, dtype=torch.float32, device=self.device) for k, v in self.p.items()}
+        self.m, self.v = ({k: torch.zeros(self.p[k].shape, dtype=torch.float32, device=self.device) for k in self._names}
+                          for _ in range(2))
         self._opt_ws = xt.adamw_workspace(numels, self.device)
 
     def moments(self):
@@ -206,11 +220,17 @@ class NativeBlock:
         return m, v
 
     def optimizer_step(self, n_microbatches=1, stream=None):
-        """Clipped AdamW over every parameter with the gradients scaled by 1 / n_microbatches
-        (the buffers hold the sum over the microbatches); the gradient norm before clipping
-        lands in self.grad_norm."""
+        """Clipped AdamW over every parameter (with matrices="muon" Muon over the layers' matrices) with the gradients
+        scaled by 1 / n_microbatches (the buffers hold the sum over the microbatches); the gradient norm before
+        clipping lands in self.grad_norm."""
         self.opt_step += 1
         h = self.hyper
+        if self._muon:
+            mats = self._muon
+            xt.xt_muon_step(xt.muon_config(grad_scale=1.0 / n_microbatches, **self.muon), [self.master[k] for k in mats],
+                            [self.g[k] for k in mats], [self.momentum[k] for k in mats],
+                            shadows=[self.p[k] for k in mats] if self.dt != torch.float32 else None, ws=self._muon_ws,
+                            s=stream)
         cfg = xt.adamw_config(h["lr"], h["beta1"], h["beta2"], h["eps"], h["weight_decay"], h["max_grad_norm"],
                               1.0 / n_microbatches, self.opt_step)
         names = self._names

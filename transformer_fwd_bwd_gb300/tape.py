@@ -224,6 +224,48 @@ def gelu(x: Var) -> Var:
     return Var(y, [x], bw)
 
 
+def embedding(E: Var, ids: torch.Tensor, scale: float = 1.0) -> Var:
+    """scale·E[ids] as [tokens, d] rows (ids int32); the gradient by tokens sorted in the forward."""
+    V, d = E.value.shape
+    n = ids.numel()
+    h = torch.empty((n, d), dtype=E.value.dtype, device=E.value.device)
+    xt.xt_embedding_lookup_fwd(ids, E.value, h, scale=scale)
+    plan = xt.embedding_plan_buffer(n, E.value.device)
+    xt.xt_embedding_plan(ids, V, plan)
+
+    def bw(g, ps):
+        p, first = ps[0], ps[0].grad is None
+        if first:
+            p.grad = torch.empty(p.value.shape, dtype=p.grad_dtype, device=p.value.device)
+        xt.xt_embedding_sorted_bwd(plan, g, p.grad, scale=scale, acc=int(not first))
+    return Var(h, [E], bw)
+
+
+def gated_mlp(x: Var, w_up: Var, w_down: Var, act: int = xt.XT_GATE_SILU) -> Var:
+    """The gated feed-forward block on bf16 rows: (act(x Wg)∘(x Wu)) w_down with w_up = [Wg | Wu]."""
+    T, d = x.value.shape
+    F = w_down.value.shape[0]
+    new = lambda *s: torch.empty(s, dtype=x.value.dtype, device=x.value.device)  # noqa: E731
+    gu, h, y = new(T, 2 * F), new(T, F), new(T, d)
+    ws = xt.gated_mlp_workspace(T, d, F, x.value.device)
+    xt.xt_gated_mlp_fwd(x.value, w_up.value, w_down.value, gu, h, y, act=act, ws=ws)
+
+    def bw(g, ps):
+        px, pu, pd = ps
+        # the weights' gradients in their grad dtype, at once where both have the same
+        dx = new(T, d)
+        grads = [torch.empty(p.value.shape, dtype=p.grad_dtype, device=p.value.device) for p in (pu, pd)]
+        args = (px.value, pu.value, pd.value, gu, h, _as(g, y), new(T, 2 * F))
+        if grads[0].dtype == grads[1].dtype:
+            xt.xt_gated_mlp_bwd(*args, dx, *grads, act=act, ws=ws)
+        else:
+            xt.xt_gated_mlp_bwd(*args, dx, grads[0], None, act=act, ws=ws)
+            xt.xt_gated_mlp_bwd(*args, None, None, grads[1], act=act, ws=ws)
+        for p, t in zip(ps, (dx, *grads)):
+            push(p, t, owned=True)
+    return Var(y, [x, w_up, w_down], bw)
+
+
 def swiglu(gate: Var, up: Var) -> Var:
     y = _empty_like(gate.value)
     xt.xt_swiglu_fwd(gate.value, up.value, y)
@@ -300,6 +342,25 @@ def cross_entropy(x: Var, targets: torch.Tensor) -> Var:
         else:                # later push: accumulate in place (no intermediate buffer)
             xt.xt_cross_entropy_bwd(p.value, targets, lse, up, p.grad, acc=1)
     return Var(loss, [x], bw)
+
+
+def token_logprobs(x: Var, tokens: torch.Tensor, scale: float = 1.0):
+    """(log p of tokens[r] in row r of x [rows, V], the rows' entropies), two float32 Vars of one forward pass, for losses
+    of the tokens' own probabilities (p = softmax(scale·x)); each pushes its part of x's gradient."""
+    rows = x.value.shape[0]
+    logp, entropy = (torch.empty(rows, dtype=_F32, device=x.value.device) for _ in range(2))
+    stats = torch.empty((rows, 2), dtype=_F32, device=x.value.device)
+    xt.xt_token_logprobs_fwd(x.value, tokens, logp, entropy, stats, scale=scale)
+
+    def bw(which):
+        def run(g, ps):
+            p, first = ps[0], ps[0].grad is None
+            if first:
+                p.grad = torch.empty(p.value.shape, dtype=p.grad_dtype, device=p.value.device)
+            xt.xt_token_logprobs_bwd(p.value, tokens, stats, entropy, g if which == 0 else None,
+                                     g if which == 1 else None, p.grad, scale=scale, acc=int(not first))
+        return run
+    return Var(logp, [x], bw(0)), Var(entropy, [x], bw(1))
 
 
 def cross_entropy_fanout(x: Var, targets: torch.Tensor, c_lin: float, c_sq: float) -> Var:
