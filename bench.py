@@ -62,7 +62,8 @@ def parse_args(argv=None):
     ap.add_argument("--recompute", action="store_true",
                     help="activation recompute: keep each layer's input only, redo its forward in the backward")
     ap.add_argument("--kernel", choices=["attention", "gemm", "layernorm", "gelu", "cross_entropy", "adamw", "fp8gemm",
-                                         "ce_fanout", "attention_masked", "rope_axes", "adamw8"],
+                                         "ce_fanout", "attention_masked", "rope_axes", "adamw8", "token_logprobs",
+                                         "embedding_sorted", "gated_mlp", "muon"],
                     default=None,
                     help="time one kernel family at the workload's sizes instead of the step (for profiling)")
     ap.add_argument("--sweep", action="store_true",
@@ -669,6 +670,55 @@ def run_kernel(args):
         nbytes = 2 * x.numel() * 2 + pos.numel() * 4
         print(json.dumps({"kernel": "rope_axes", "rows": T, "heads": H, "hd": hd, "fwd_us": fwd_us, "bwd_us": bwd_us,
                           "fwd_gbs": nbytes / fwd_us / 1e3, "bwd_gbs": nbytes / bwd_us / 1e3, "clocks": clocks}))
+    elif args.kernel == "token_logprobs":
+        # the stack's logits: log probabilities and entropies of its tokens, and the gradient of both
+        cfg = synth.BLOCK_CONFIGS[args.workload]
+        R, V = cfg["B"] * cfg["S"], cfg["V"]
+        x = (2.0 * torch.randn(R, V, generator=g)).to(torch.bfloat16).to(dev)
+        tok = torch.randint(0, V, (R,), generator=g, dtype=torch.int32).to(dev)
+        lp, ent, st = (torch.empty(s_, dtype=torch.float32, device=dev) for s_ in ((R,), (R,), (R, 2)))
+        up, dx = torch.full((R,), 1.0 / R, device=dev), torch.empty_like(x)
+        fwd_us = timed(lambda: xt.xt_token_logprobs_fwd(x, tok, lp, ent, st))
+        bwd_us = timed(lambda: xt.xt_token_logprobs_bwd(x, tok, st, ent, up, up, dx))
+        print(json.dumps({"kernel": "token_logprobs", "rows": R, "V": V, "fwd_us": fwd_us, "bwd_us": bwd_us,
+                          "fwd_gbs": 2 * R * V / fwd_us / 1e3, "bwd_gbs": 4 * R * V / bwd_us / 1e3, "clocks": clocks}))
+    elif args.kernel == "embedding_sorted":
+        cfg = synth.BLOCK_CONFIGS[args.workload]
+        T, d, V = cfg["B"] * cfg["S"], cfg["d"], cfg["V"]
+        ids = torch.randint(0, V, (T,), generator=g, dtype=torch.int32).to(dev)
+        E = torch.randn(V, d, generator=g).to(torch.bfloat16).to(dev)
+        h, dE = torch.empty(T, d, dtype=torch.bfloat16, device=dev), torch.zeros(V, d, device=dev)
+        plan, ws = xt.embedding_plan_buffer(T, dev), xt.embedding_sorted_workspace(T, d, dev)
+        fwd_us = timed(lambda: xt.xt_embedding_lookup_fwd(ids, E, h, scale=d ** 0.5))
+        plan_us = timed(lambda: xt.xt_embedding_plan(ids, V, plan))
+        bwd_us = timed(lambda: xt.xt_embedding_sorted_bwd(plan, h, dE, scale=d ** 0.5, acc=1, ws=ws))
+        print(json.dumps({"kernel": "embedding_sorted", "tokens": T, "d": d, "V": V, "fwd_us": fwd_us, "plan_us": plan_us,
+                          "bwd_us": bwd_us, "clocks": clocks}))
+    elif args.kernel == "gated_mlp":
+        cfg = synth.BLOCK_CONFIGS[args.workload]
+        T, d, F = cfg["B"] * cfg["S"], cfg["d"], 8 * cfg["d"] // 3
+        mk = lambda *sh: torch.randn(*sh, generator=g).to(torch.bfloat16).to(dev)  # noqa: E731
+        x, wu, wd, dy = mk(T, d), mk(d, 2 * F), mk(F, d), mk(T, d)
+        e = lambda *sh: torch.empty(*sh, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        gu, h, y, dgu, dx = e(T, 2 * F), e(T, F), e(T, d), e(T, 2 * F), e(T, d)
+        dwu, dwd = torch.empty(d, 2 * F, device=dev), torch.empty(F, d, device=dev)
+        ws = xt.gated_mlp_workspace(T, d, F, dev)
+        fwd_us = timed(lambda: xt.xt_gated_mlp_fwd(x, wu, wd, gu, h, y, ws=ws))
+        bwd_us = timed(lambda: xt.xt_gated_mlp_bwd(x, wu, wd, gu, h, dy, dgu, dx, dwu, dwd, ws=ws))
+        print(json.dumps({"kernel": "gated_mlp", "tokens": T, "d": d, "F": F, "fwd_us": fwd_us, "bwd_us": bwd_us,
+                          "fwd_tflops": 6 * T * d * F / fwd_us / 1e6, "bwd_tflops": 12 * T * d * F / bwd_us / 1e6,
+                          "clocks": clocks}))
+    elif args.kernel == "muon":
+        cfg = synth.BLOCK_CONFIGS[args.workload]
+        d, F = cfg["d"], cfg["F"]
+        up = 2 * F if cfg["mlp"] == "swiglu" else F
+        shapes = [sh for _ in range(cfg["n_layers"]) for sh in ((d, 3 * d), (d, d), (d, up), (F, d))]
+        P, G, M = ([(0.02 * torch.randn(*sh, generator=g)).to(dev) for sh in shapes] for _ in range(3))
+        ws, mcfg = xt.muon_workspace(shapes, dev), xt.muon_config(0.02, weight_decay=0.1)
+        us = timed(lambda: xt.xt_muon_step(mcfg, P, G, M, ws=ws))
+        fl = sum(5 * (2 * a * a * b * 1.5 + a ** 3) for a, b in ((min(sh), max(sh)) for sh in shapes))
+        print(json.dumps({"kernel": "muon", "matrices": len(P), "params": sum(t.numel() for t in P), "us": us,
+                          "tflops": fl / us / 1e6, "clocks": clocks}))
     elif args.kernel == "layernorm":
         # as the stack launches it: bf16 rows, float32 residual gradient accumulated, float32 dγ / dβ
         cfg = synth.BLOCK_CONFIGS[args.workload]

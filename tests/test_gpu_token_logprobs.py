@@ -94,6 +94,12 @@ CASES = [  # R, V, dtype, top, scale, ld, offset (elements before the first row)
     (70, 50304, "bf16", 1, 1.0, None, 0),
     (400, 20011, "f32", 20, 0.7, None, 0),
     (700, 9999, "bf16", 8, 1.0, None, 0),
+    # many long rows
+    (700, 16385, "bf16", 20, 1.0, None, 0),
+    (1400, 16384, "bf16", 0, 1.0, None, 0),
+    (460, 20003, "f32", 32, 1.25, 20009, 3),
+    (1000, 33001, "bf16", 1, 1.0, 33007, 5),
+    (300, 50257, "bf16", 8, 1.0, None, 0),
     (2, 128256, "f32", 20, 1.0, None, 0),
     (5, 128256, "bf16", 20, 1.0, None, 0),
 ]
@@ -251,6 +257,33 @@ def test_banned_extreme_and_empty_rows(V, dtype):
     # a row far from nought: its exponent is formed from the difference to the maximum, no further error
     assert ((dx[good].double() - gw).abs() <= bound).all()
     assert (dx[0, 5:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_long_rows_of_every_kind(dtype):
+    """Many long rows, the odd ones among them: ties, rising, banned, empty, not finite; each row equal to the same row on
+    its own (which a cluster of CTAs takes) up to the sums' order."""
+    V, n = 17000, 500
+    x, tok = make(n, V, dtype, 21)
+    x[3] = 0.0
+    x[4] = (torch.arange(V, device="cuda") // 3).to(TD[dtype])
+    x[5, ::2] = -math.inf
+    x[6] = -math.inf
+    x[7, 99] = float("nan")
+    x[8, 100] = math.inf
+    x[9] = torch.finfo(TD[dtype]).min
+    x[10, 7] = 500.0
+    tok[5] = 1
+    out = forward(x, tok, 20)
+    for r in range(12):
+        one = forward(x[r:r + 1], tok[r:r + 1], 20)
+        assert torch.equal(out[4][r:r + 1], one[4])
+        for a, b in zip(out[:4], one[:4]):
+            both = torch.isnan(a[r:r + 1]) & torch.isnan(b) | (a[r:r + 1] == b)
+            assert (both | ((a[r:r + 1] - b).abs() <= 40 * tol_sum(V) + 4 * EPS * b.abs())).all()
+    good = [r for r in range(n) if r not in (5, 6, 7, 8, 9)]
+    check_forward(x[good], tok[good], 20, 1.0, tuple(o[good] for o in out))
+    assert xt.device_errors() == 0
 
 
 def test_tokens_outside_the_vocabulary():

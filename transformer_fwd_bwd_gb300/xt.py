@@ -265,9 +265,17 @@ def _check(code):
         raise XtError(code, lib().xt_last_error().decode(errors="replace"))
 
 
+_entry = {}  # entry points by name, bound on first use
+
+
 def call(name, *args):
     """Calls a libxt entry point with already-marshalled arguments; raises on failure."""
-    _check(getattr(lib(), name)(*args))
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(lib(), name)
+    code = f(*args)
+    if code != XT_OK:
+        _check(code)
 
 
 # ------------------------------------------------------------------------------ marshalling
@@ -742,7 +750,7 @@ def _rows_of(x, name):
 
 
 def _vector(t, shape, dtype, name):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
 
 
@@ -1071,28 +1079,27 @@ def gated_mlp_workspace(T, d, F, device="cuda", s=None):
     return workspace(ws_bytes("xt_gated_mlp_workspace_size", int(T), int(d), int(F)), device, s)
 
 
-def _gated_shapes(x, w_up, w_down, **others):
-    """T, d, F of a gated block's tensors, all checked against each other."""
+def _gated_shapes(x, w_up, w_down, pairs):
+    """T, d, F of a gated block's tensors; pairs: (name, tensor, rows of T, columns in (d, F)) to check against them."""
     if x.dim() != 2 or w_up.dim() != 2 or w_up.shape[1] % 2:
         raise ValueError("x must be [T, d] and w_up [d, 2F]")
     T, d = x.shape
     F = w_up.shape[1] // 2
-    shapes = dict(w_up=(d, 2 * F), w_down=(F, d), gu=(T, 2 * F), h=(T, F), y=(T, d), dy=(T, d), dgu=(T, 2 * F), dx=(T, d),
-                  dw_up=(d, 2 * F), dw_down=(F, d))
-    for name, t in dict(others, w_up=w_up, w_down=w_down).items():
-        if t is None:
-            continue
-        if tuple(t.shape) != shapes[name]:
-            raise ValueError(f"{name} must be {list(shapes[name])}")
-        if t.dtype != x.dtype and name not in ("dw_up", "dw_down"):
-            raise ValueError(f"{name} must have x's dtype")
+    kind = x.dtype
+    if w_up.shape[0] != d or w_up.dtype != kind:
+        raise ValueError("w_up must be [d, 2F] of x's dtype")
+    if w_down is not None and (w_down.shape != (F, d) or w_down.dtype != kind):
+        raise ValueError("w_down must be [F, d] of x's dtype")
+    for name, t, cols_d, cols_f in pairs:
+        if t is not None and (t.shape != (T, cols_d * d + cols_f * F) or t.dtype != kind):
+            raise ValueError(f"{name} must be [T, {'d' if cols_d else 'F' if cols_f == 1 else '2F'}] of x's dtype")
     return T, d, F
 
 
 def xt_gated_mlp_fwd(x, w_up, w_down, gu, h, y, act=XT_GATE_SILU, ws=None, s=None):
     """h = act(x Wg)∘(x Wu), y = h w_down for x [T, d], w_up = [Wg | Wu] [d, 2F]; gu [T, 2F] keeps both projections for
     the backward (None: not kept); y and w_down None: h alone."""
-    T, d, F = _gated_shapes(x, w_up, w_down, gu=gu, h=h, y=y)
+    T, d, F = _gated_shapes(x, w_up, w_down, (("gu", gu, 0, 2), ("h", h, 0, 1), ("y", y, 1, 0)))
     if (y is None) != (w_down is None):
         raise ValueError("y and w_down go together")
     if ws is None and y is not None and T:
@@ -1105,7 +1112,10 @@ def xt_gated_mlp_bwd(x, w_up, w_down, gu, h, dy, dgu, dx, dw_up, dw_down, act=XT
                      s=None):
     """The gradients of xt_gated_mlp_fwd; dgu [T, 2F] is scratch (it receives the projections' gradients); dx, dw_up and
     dw_down may be None."""
-    T, d, F = _gated_shapes(x, w_up, w_down, gu=gu, h=h, dy=dy, dgu=dgu, dx=dx, dw_up=dw_up, dw_down=dw_down)
+    T, d, F = _gated_shapes(x, w_up, w_down, (("gu", gu, 0, 2), ("h", h, 0, 1), ("dy", dy, 1, 0), ("dgu", dgu, 0, 2),
+                                              ("dx", dx, 1, 0)))
+    if (dw_up is not None and dw_up.shape != (d, 2 * F)) or (dw_down is not None and dw_down.shape != (F, d)):
+        raise ValueError("dw_up must be [d, 2F] and dw_down [F, d]")
     kinds = {t.dtype for t in (dw_up, dw_down) if t is not None}
     if len(kinds) > 1:
         raise ValueError("dw_up and dw_down must share a dtype")
