@@ -169,6 +169,32 @@ def test_ids_outside_the_vocabulary_and_no_tokens():
     assert (dE == 0.0).all() and xt.device_errors() == 0
 
 
+def test_far_rows():
+    """A table of more than 2^31 elements, ids of 22 bits (three digits of the sort)."""
+    V, d, T = 2200000, 1024, 3000
+    E = torch.empty(V, d, dtype=torch.bfloat16, device="cuda")
+    ids = draw_ids("uniform", T, V, 4)
+    ids[:5] = V - 1
+    ids[5] = 0
+    E[ids.long()] = rows(T, d, "bf16", 1)
+    h = empty((T, d), "bf16")
+    xt.xt_embedding_lookup_fwd(ids, E, h)
+    assert torch.equal(h, E[ids.long()])
+    plan = xt.embedding_plan_buffer(T)
+    xt.xt_embedding_plan(ids, V, plan)
+    check_plan(plan, ids, V)
+    E.fill_(7.0)
+    dh = rows(T, d, "bf16", 2)
+    xt.xt_embedding_sorted_bwd(plan, dh, E, acc=0)
+    used, at = torch.unique(ids.long(), return_inverse=True)
+    want = torch.zeros(used.numel(), d, dtype=torch.float64, device="cuda").index_add_(0, at, dh.double())
+    mag = torch.zeros_like(want).index_add_(0, at, dh.double().abs())
+    assert ((E[used].double() - want).abs() <= 12 * EPS * mag + half("bf16") * want.abs()).all()
+    E[used] = 0
+    assert not E.any()
+    assert xt.device_errors() == 0
+
+
 def test_plan_of_other_sizes_is_refused():
     V, d = 100, 16
     ids = draw_ids("uniform", 64, V, 1)

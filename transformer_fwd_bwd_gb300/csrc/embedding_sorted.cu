@@ -13,7 +13,9 @@
 // occurs, and no sum depends on timing.  With acc = 0 the rows that no token touches are zeroed in the same launch: a
 // warp to 32 rows, each lane looking its row up in the plan.
 //
-// Bound by HBM.  Measured times stand beside the launches.
+// Bound by HBM, few tokens by latency.  On one GB300 (bf16 rows, float32 gradient, us): lookup, plan, gradient of 8192 tokens x 768
+// over 50304 rows 5.4, 12.7, 13.3; of 131072 x 1024 over 128256 rows, written afresh, 65, 56, 183 (0.64 of the copy rate); of
+// 37 tokens 1.8, 2.4, 7.1.
 #include <atomic>
 
 #include "internal.cuh"

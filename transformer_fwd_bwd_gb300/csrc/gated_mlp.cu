@@ -4,7 +4,9 @@
 // runs both projections, the activation and the product, the backward's forms dg and du where dh is still in tensor
 // memory.  [dg | du] stands as Wg and Wu stand beside each other, so dx is one product over 2F and dW_up another.
 //
-// Bound by the tensor cores: 6·T·d·F operations forward, 12·T·d·F backward.  Measured times stand beside the calls.
+// Bound by the tensor cores: 6·T·d·F operations forward, 12·T·d·F backward.  On one GB300, T x d x F = 8192 x 768 x 2048 silu (us):
+// projections with activation 42 (1230 TFLOP/s), down 28, dh with its epilogue 51 (504: reads of g and u compete with the
+// operands'), dx 41, dW 44 and 27; 12001 x 2048 x 5464 gelu: 359 (1500 TFLOP/s), 172, 303 (886), 325, 309 and 194.
 #include "gemm.cuh"
 #include "internal.cuh"
 

@@ -16,7 +16,9 @@
 // matrices fill the GPU together: three launches per iteration whatever the list.
 //
 // The product kernel is warp-specialised as the GEMM is: TMA producer, MMA issuer (CTA pairs, 256 × 256 tiles,
-// tcgen05 kind::f16 on f16), four epilogue warps; bounded waits.  Tensor-bound; measured times stand beside the launches.
+// tcgen05 kind::f16 on f16; 128 × 128 ones of single CTAs for few matrices), eight epilogue warps; bounded waits.  Tensor-bound.
+// On one GB300, 48 matrices of a 12-layer stack of width 768 (us): A 184 (1418 TFLOP/s of the three products), B 73, X 273 (1430) per
+// step, the passes over 85 M weights 141, 174 and 169 (at HBM's rate): 3390 in all; four matrices of width 256 222.
 #include <cuda_fp16.h>
 
 #include <cmath>
