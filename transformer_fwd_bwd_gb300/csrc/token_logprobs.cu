@@ -10,14 +10,16 @@
 // Σ t·2^t / Σ 2^t loses at most kHeadroom·2⁻²⁴).  The threads' sums meet at the largest base.  What this path cannot hold (a largest logit beyond
 // 2⁻¹·FLT_MAX in t, below −1e30, or no finite sum) is done over by row_safe(), two passes with differences taken first.
 //
-// The most probable tokens cost one comparison per 16 bytes in that pass: each thread keeps its largest element (the
-// value and the vector it lies in).  The k-th largest of the threads' maxima bounds the k-th largest element from below,
-// and the elements above it lie with the k threads whose maxima reach it, so only those threads' vectors are read again
-// (from L2: k/256 of the row) and their elements at or above the bound are put in order.  Elements are ordered by
-// (value, lower index first) throughout, so that ties have one answer, and no step depends on the data's order.
+// The most probable tokens: a warp takes 512 neighbouring bytes at a time and one of its lanes in turn keeps the largest of
+// these groups' maxima (a maximum over the warp, one instruction).  The k-th largest of the lanes' maxima bounds the k-th
+// largest element from below, and the elements above it lie with the k lanes whose maxima reach it, so only those lanes'
+// groups are read again (whole lines; with a thread's own vectors, 4 KB apart, it was 40 % more bytes out of HBM at
+// 128256 logits and 20 alternatives), filtered by their vectors' maxima, and the few elements at or above the bound are put
+// in order.  Elements are ordered by (value, lower index first) throughout, so that ties have one answer, and no step
+// depends on timing.
 //
-// Bound by HBM: a logit is read once (backward: read and written).  On one GB300: 8192 x 50304 bf16 forward 145 us (5.7 TB/s),
-// backward 258 us (6.4 TB/s); 4096 x 128256 with 20 alternatives 238 us (4.4 TB/s: a quarter more instructions and five block
+// Bound by HBM: a logit is read once (backward: read and written).  On one GB300: 8192 x 50304 bf16 forward 142 us (5.8 TB/s),
+// backward 258 us (6.4 TB/s); 4096 x 128256 with 20 alternatives 215 us (4.9 TB/s: a quarter more instructions and five block
 // barriers at a row's end, during which its block loads nothing); 3 x 50257 with 5 alternatives 10 us.  Six blocks per SM of 40
 // registers with four vectors in flight: fewer blocks or more vectors were 2 to 10 % slower.
 #include <cfloat>
@@ -105,7 +107,7 @@ struct Sums {
   float b;         // base of the exponents, log2 units
   uint64_t s, w;   // Σ 2^t and Σ t·2^t, two partial sums each
   float top;       // largest element
-  uint32_t at;     // the first vector that holds it
+  uint32_t at;     // the first vector that holds it (where asked for)
 };
 
 __device__ __forceinline__ void rebase(Sums& a, float nb) {
@@ -118,11 +120,15 @@ __device__ __forceinline__ void rebase(Sums& a, float nb) {
   a.b = nb;
 }
 
-template <int N>
+template <bool AT, int N>
 __device__ __forceinline__ void consume(Sums& a, const float (&x)[N], float top, uint32_t j, float c) {
-  const bool more = top > a.top;
-  a.top = more ? top : a.top;
-  a.at = more ? j : a.at;
+  if constexpr (AT) {
+    const bool more = top > a.top;
+    a.top = more ? top : a.top;
+    a.at = more ? j : a.at;
+  } else {
+    a.top = fmaxf(a.top, top);
+  }
   if (top * c > a.b + kHeadroom) rebase(a, top * c);
   const uint64_t cc = f32x2_pack(c, c), nb = f32x2_pack(-a.b, -a.b);
 #pragma unroll
@@ -182,10 +188,11 @@ __device__ __forceinline__ float order_value(uint64_t o) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// Puts the elements at or above `bound` of the lanes' vectors (number j; none where j < 0) into the warp's list: lanes
-// whose maximum reaches the bound hand their 16 bytes round.
+// Puts the elements at or above `bound` of the lanes' vectors (number j; none where j < 0; `group`: the number that the bound
+// orders them by) into the warp's list: lanes whose maximum reaches the bound hand their 16 bytes round.
 template <typename T>
-__device__ __forceinline__ uint64_t collect(uint64_t list, const Row<T>& row, int64_t j, uint64_t bound, int lane) {
+__device__ __forceinline__ uint64_t collect(uint64_t list, const Row<T>& row, int64_t j, uint32_t group, uint64_t bound,
+                                            int lane) {
   constexpr int W = Chunk<T>::W;
   uint4 q = make_uint4(0u, 0u, 0u, 0u);
   int n = 0;
@@ -203,7 +210,7 @@ __device__ __forceinline__ uint64_t collect(uint64_t list, const Row<T>& row, in
       top = Chunk<T>::top(q);
     }
   }
-  uint32_t some = __ballot_sync(0xffffffffu, n > 0 && order(top, uint32_t(j)) >= bound);
+  uint32_t some = __ballot_sync(0xffffffffu, n > 0 && order(top, group) >= bound);
   while (some) {
     const int from = __ffs(some) - 1;
     some &= some - 1;
@@ -213,13 +220,13 @@ __device__ __forceinline__ uint64_t collect(uint64_t list, const Row<T>& row, in
     o.z = __shfl_sync(0xffffffffu, q.z, from);
     o.w = __shfl_sync(0xffffffffu, q.w, from);
     const int count = __shfl_sync(0xffffffffu, n, from);
-    const uint32_t jj = uint32_t(__shfl_sync(0xffffffffu, int(j), from));
+    const uint32_t jj = uint32_t(__shfl_sync(0xffffffffu, int(j), from)), gg = __shfl_sync(0xffffffffu, group, from);
     float v[W], mine = 0.f;
     Chunk<T>::values(o, v);
 #pragma unroll
     for (int i = 0; i < W; ++i) mine = lane == i ? v[i] : mine;
     uint64_t c = 0;
-    if (lane < count && order(mine, jj) >= bound) c = order(mine, uint32_t(row.first(jj) + lane));
+    if (lane < count && order(mine, gg) >= bound) c = order(mine, uint32_t(row.first(jj) + lane));
     uint32_t hits = __ballot_sync(0xffffffffu, c != 0);
     while (hits) {
       const int l = __ffs(hits) - 1;
@@ -352,30 +359,43 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
 
   Sums m{-1e30f, 0ull, 0ull, -INFINITY, uint32_t(lo + 1 + tid)};
   bool any = lo + tid < hi;
+  // Groups (a CTA's rows with alternatives): the 32 neighbouring vectors that a warp takes together, 512 bytes, numbered
+  // 1 + 8·turn + warp in the row's order.  Lane t keeps the largest of its warp's groups of turns t, t + 32, ...
+  constexpr bool GROUPS = TOP && !WARP;
+  uint32_t best_key = 0, best_group = 0, turn = 0;
+  auto take = [&](const uint4& q, int64_t j, bool in) {
+    const float top = Chunk<T>::top(q);
+    if constexpr (GROUPS) {
+      const uint32_t key = __reduce_max_sync(0xffffffffu, in ? order_key(top) : 0u);
+      if (lane == int(turn & 31) && key > best_key) {
+        best_key = key;
+        best_group = 1 + turn * kWarps + warp;
+      }
+      ++turn;
+    }
+    if (!in) return;
+    float v[W];
+    Chunk<T>::values(q, v);
+    consume<TOP && WARP>(m, v, top, uint32_t(j), a.c);
+  };
   const T* p = row.vector(lo + 1 + tid);
   int64_t j = lo + 1 + tid;
-  for (; j + (kUnroll - 1) * NT <= hi; j += kUnroll * NT, p += kUnroll * NT * W) {
+  for (; j - lane + 31 + (kUnroll - 1) * NT <= hi; j += kUnroll * NT, p += kUnroll * NT * W) {  // the same for the whole warp
     uint4 q[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) q[u] = load_stream(p + u * NT * W);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float v[W];
-      Chunk<T>::values(q[u], v);
-      consume<W>(m, v, Chunk<T>::top(q[u]), uint32_t(j + u * NT), a.c);
-    }
+    for (int u = 0; u < kUnroll; ++u) take(q[u], j + u * NT, true);
   }
   {  // what is left, all of it in flight at once
-    uint4 q[kUnroll - 1];
+    uint4 q[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll - 1; ++u)
+    for (int u = 0; u < kUnroll; ++u)
       if (j + u * NT <= hi) q[u] = load_stream(p + u * NT * W);
 #pragma unroll
-    for (int u = 0; u < kUnroll - 1; ++u) {
-      if (j + u * NT > hi) break;
-      float v[W];
-      Chunk<T>::values(q[u], v);
-      consume<W>(m, v, Chunk<T>::top(q[u]), uint32_t(j + u * NT), a.c);
+    for (int u = 0; u < kUnroll; ++u) {
+      if (j - lane + u * NT > hi) break;
+      take(q[u], j + u * NT, j + u * NT <= hi);
     }
   }
   // the elements beside the whole vectors: the head with thread 0 of the first CTA, the tail with the last thread of
@@ -393,12 +413,19 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
       v[i] = i < n ? to_f(x[e0 + i]) : -INFINITY;
       top = fmaxf(top, v[i]);
     }
-    if (!any || (has_head && top >= m.top)) {  // the head comes before what the thread has seen
+    if constexpr (GROUPS) {
+      // the head, group 0, comes before what the lane has seen, the tail after it
+      const uint32_t key = order_key(top), group = has_head ? 0u : ~0u - 1u;
+      if (key > best_key || (has_head && key == best_key)) {
+        best_key = key;
+        best_group = group;
+      }
+    } else if (!any || (has_head && top >= m.top)) {
       m.top = -INFINITY;
       m.at = uint32_t(k);
     }
     any = true;
-    consume<W>(m, v, top, uint32_t(k), a.c);
+    consume<TOP && WARP>(m, v, top, uint32_t(k), a.c);
   }
 
   float b = m.b, s0, s1, w0, w1;
@@ -407,7 +434,6 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
   float s = s0 + s1, w = w0 + w1, M = warp_max(m.top);
   warp_join(b, s, w);
   uint64_t list = 0;
-  uint64_t best = TOP && any ? order(m.top, m.at) : 0ull;
 
   if constexpr (WARP) {
     double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
@@ -415,11 +441,11 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
     if (lane == 0) write_row(a, r, valid, given, M, log2s, mean);
     if constexpr (TOP) {
-      const uint64_t bound = __shfl_sync(0xffffffffu, sort_warp(best, lane), a.top - 1);
+      const uint64_t bound = __shfl_sync(0xffffffffu, sort_warp(any ? order(m.top, m.at) : 0ull, lane), a.top - 1);
       // vectors are few here: all of them are looked through
       for (int64_t j0 = 0; j0 <= tail; j0 += 32) {
         const int64_t jj = j0 + lane;
-        list = collect(list, row, jj <= tail ? jj : -1, bound, lane);
+        list = collect(list, row, jj <= tail ? jj : -1, uint32_t(jj), bound, lane);
       }
       write_top(a, r, list, lane, M, log2s);
     }
@@ -428,26 +454,27 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
 
   // ---- the CTA's most probable elements
   if constexpr (TOP) {
+    const uint64_t best = best_key ? (uint64_t(best_key) << 32) | uint32_t(~best_group) : 0ull;
     const uint64_t all = merge_lists<kWarps>(lists, sort_warp(best, lane), warp, lane);
     if (warp == 0) chosen[lane] = all;
     __syncthreads();
     const uint64_t bound = chosen[a.top - 1];
-    // a warp to a chosen thread: its vectors are the number that its maximum lies in, modulo kThreads
+    // a warp to a chosen lane: all the groups that its maximum is taken over
     for (int k = warp; k < a.top; k += kWarps) {
       const uint64_t ch = chosen[k];
       if (ch == 0) break;
-      const int64_t at = int64_t(~uint32_t(ch));
-      int owner;
-      if (at == 0) owner = 0;
-      else if (at == tail) owner = kThreads - 1;
-      else owner = int((at - 1 - lo) % kThreads);
-      for (int64_t j0 = lo + 1 + owner; j0 <= hi; j0 += int64_t(32) * kThreads) {
-        const int64_t jj = j0 + int64_t(lane) * kThreads;
-        list = collect(list, row, jj <= hi ? jj : -1, bound, lane);
+      const uint32_t group = ~uint32_t(ch);
+      const bool head = group == 0, end = group == ~0u - 1u;
+      const int ow = head ? 0 : end ? kWarps - 1 : int((group - 1) % kWarps);
+      const uint32_t ol = head ? 0 : end ? 31 : (group - 1) / kWarps % 32;
+      for (int64_t t = ol;; t += 32) {
+        const int64_t j0 = lo + 1 + (t * kWarps + ow) * 32;
+        if (j0 > hi) break;
+        list = collect(list, row, j0 + lane <= hi ? j0 + lane : -1, uint32_t(1 + t * kWarps + ow), bound, lane);
       }
-      if (owner == 0 && rank == 0 && row.head > 0) list = collect(list, row, lane == 0 ? 0 : -1, bound, lane);
-      if (owner == kThreads - 1 && rank == cl - 1 && row.first(tail) < a.V)
-        list = collect(list, row, lane == 0 ? tail : -1, bound, lane);
+      if (ow == 0 && ol == 0 && rank == 0 && row.head > 0) list = collect(list, row, lane == 0 ? 0 : -1, 0u, bound, lane);
+      if (ow == kWarps - 1 && ol == 31 && rank == cl - 1 && row.first(tail) < a.V)
+        list = collect(list, row, lane == 0 ? tail : -1, ~0u - 1u, bound, lane);
     }
     list = merge_lists<kWarps>(lists, list, warp, lane);
   }
