@@ -75,6 +75,8 @@ CASES = [  # T, d, F, act, dtype of the weights' gradients
     (4097, 136, 2056, 1, "f32"),
     (8192, 768, 2048, 0, "f32"),
     (5000, 1032, 2504, 1, "bf16"),
+    (100, 64, 20488, 0, "bf16"),   # one row of tiles, wide single-CTA ones
+    (128, 200, 10248, 1, "f32"),
 ]
 
 

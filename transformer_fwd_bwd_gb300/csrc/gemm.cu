@@ -392,7 +392,7 @@ int run_gated(const Problem& pb, cudaStream_t s) {
   const int nt = fwd ? 128 : 256;  // columns of a 256-wide tile
   const int pairs = pair_capacity();
   const int64_t pair_tiles = ceil_div(pb.M, 2 * BM) * ceil_div(pb.N, nt);
-  const int cg = pairs > 0 && pb.M > BM && 2 * pair_tiles >= pairs ? 2 : 1;
+  const int cg = g_pairing != 1 && pairs > 0 && pb.M > BM && 2 * pair_tiles >= pairs ? 2 : 1;
   const int bn = cg == 1 && 2 * ceil_div(pb.M, BM) * ceil_div(pb.N, nt) <= num_sms() ? 128 : 256;
   const int cols = fwd ? bn / 2 : bn;
   CUtensorMap ta, tb, tc, tc2;

@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
-    if (p.tma_store) prefetch_tmap(&tmC);
+    if (p.tma_store && !GATE_B) prefetch_tmap(&tmC);  // (dg and du leave by C2's map)
     if (ACT == 1 || GATE_B || (GATE_F && p.store_gu)) prefetch_tmap(&tmC2);
   }
   if (warp == 1) {
