@@ -1,8 +1,9 @@
 // Embedding lookup with a scale, and its gradient by sorted tokens:
 //   h[t] = scale·E[ids[t]],   dE[v] (+)= scale·Σ_{t: ids[t] = v} dh[t], t ascending.
 //
-// xt_embedding_plan sorts the tokens by id, those of one id by t: a stable radix sort, least significant digit first,
-// by one cluster of CTAs (hardware barriers, no waiting on memory), every digit of up to 9 bits two sweeps over the
+// xt_embedding_plan sorts the tokens by id, those of one id by t: up to kRankTokens of them by counting (below), more by
+// a stable radix sort, least significant digit first,
+// by one cluster of CTAs (hardware barriers, no waiting on memory; 16 CTAs for many tokens: 131072 in 35 us where 8 take 56), every digit of up to 9 bits two sweeps over the
 // cluster's tokens: counts of each warp, their prefix over warps, CTAs and digits, then the moves.  One launch; 16 bits
 // of id take two digits.
 //
@@ -14,7 +15,7 @@
 // warp to 32 rows, each lane looking its row up in the plan.
 //
 // Bound by HBM, few tokens by latency.  On one GB300 (bf16 rows, float32 gradient, us): lookup, plan, gradient of 8192 tokens x 768
-// over 50304 rows 5.4, 12.7, 13.3; of 131072 x 1024 over 128256 rows, written afresh, 65, 56, 183 (0.64 of the copy rate); of
+// over 50304 rows 5.4, 12.8, 13.2; of 131072 x 1024 over 128256 rows, written afresh, 65, 35, 176 (0.67 of the copy rate); of
 // 37 tokens 1.8, 2.4, 7.1.
 #include <atomic>
 
@@ -73,7 +74,7 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // The lanes whose digit (of `bits` bits) is this lane's, among those in `in`: a ballot per bit (about 27 instructions; the
-// instruction that compares all lanes' values is slower: 131072 tokens sorted in 73 us instead of 56).
+// instruction that compares all lanes' values is slower: 131072 tokens sorted by 8 CTAs in 73 us instead of 56).
 __device__ __forceinline__ uint32_t same_digit(uint32_t dg, bool in, int bits) {
   uint32_t peers = __ballot_sync(0xffffffffu, in);
   for (int b = 0; b < bits; ++b) {
