@@ -94,6 +94,13 @@ CASES = [  # R, V, dtype, top, scale, ld, offset (elements before the first row)
     (70, 50304, "bf16", 1, 1.0, None, 0),
     (400, 20011, "f32", 20, 0.7, None, 0),
     (700, 9999, "bf16", 8, 1.0, None, 0),
+    # rows between a warp's and a CTA's, few and many
+    (1300, 2500, "bf16", 32, 1.0, None, 0),
+    (1300, 4001, "f32", 20, 1.0, 4003, 1),
+    (1250, 8191, "bf16", 32, 1.25, None, 3),
+    (20, 4000, "bf16", 20, 1.0, None, 0),
+    (20, 8000, "bf16", 32, 1.0, None, 0),
+    (1300, 70, "bf16", 32, 1.0, None, 0),
     # many long rows
     (700, 16385, "bf16", 20, 1.0, None, 0),
     (1400, 16384, "bf16", 0, 1.0, None, 0),
@@ -197,14 +204,16 @@ def test_gradient_against_differences():
     assert ((dx.double() - w32).abs() <= tol + EPS * w32.abs()).all()
 
 
-@pytest.mark.parametrize("V", [257, 5001, 50257])
+@pytest.mark.parametrize("V", [257, 2047, 5001, 50257])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_ties_and_order(V, dtype):
+@pytest.mark.parametrize("times", [1, 220])
+def test_ties_and_order(V, dtype, times):
     """Equal logits by rising id, whichever threads hold them; rows that rise, fall and are constant."""
     rows = [torch.zeros(V), torch.arange(V) // 3, -(torch.arange(V) // 5), (torch.arange(V) * 7919) % 13,
             torch.where(torch.arange(V) % 256 == 3, 1.0, 0.0), torch.tensor([0.0, -0.0]).repeat(V)[:V]]
-    x = torch.stack([r.float() for r in rows]).to(TD[dtype]).cuda()
-    tok = torch.arange(len(rows), device="cuda").to(torch.int32)
+    # enough copies that other kernels take the rows
+    x = torch.stack([r.float() for r in rows]).to(TD[dtype]).cuda().repeat(times if V < 10000 else 1, 1)
+    tok = (torch.arange(x.shape[0], device="cuda") % V).to(torch.int32)
     out = forward(x, tok, 32)
     check_forward(x, tok, 32, 1.0, out)
 

@@ -107,7 +107,6 @@ struct Sums {
   float b;         // base of the exponents, log2 units
   uint64_t s, w;   // Σ 2^t and Σ t·2^t, two partial sums each
   float top;       // largest element
-  uint32_t at;     // the first vector that holds it (where asked for)
 };
 
 __device__ __forceinline__ void rebase(Sums& a, float nb) {
@@ -120,15 +119,9 @@ __device__ __forceinline__ void rebase(Sums& a, float nb) {
   a.b = nb;
 }
 
-template <bool AT, int N>
-__device__ __forceinline__ void consume(Sums& a, const float (&x)[N], float top, uint32_t j, float c) {
-  if constexpr (AT) {
-    const bool more = top > a.top;
-    a.top = more ? top : a.top;
-    a.at = more ? j : a.at;
-  } else {
-    a.top = fmaxf(a.top, top);
-  }
+template <int N>
+__device__ __forceinline__ void consume(Sums& a, const float (&x)[N], float top, float c) {
+  a.top = fmaxf(a.top, top);
   if (top * c > a.b + kHeadroom) rebase(a, top * c);
   const uint64_t cc = f32x2_pack(c, c), nb = f32x2_pack(-a.b, -a.b);
 #pragma unroll
@@ -357,13 +350,18 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
   // this CTA's whole vectors: (lo, hi], numbers 1 .. full
   const int64_t lo = WARP ? 0 : row.full * rank / cl, hi = WARP ? row.full : row.full * (rank + 1) / cl;
 
-  Sums m{-1e30f, 0ull, 0ull, -INFINITY, uint32_t(lo + 1 + tid)};
-  bool any = lo + tid < hi;
+  Sums m{-1e30f, 0ull, 0ull, -INFINITY};
   // Groups (a CTA's rows with alternatives): the 32 neighbouring vectors that a warp takes together, 512 bytes, numbered
   // 1 + 8·turn + warp in the row's order.  Lane t keeps the largest of its warp's groups of turns t, t + 32, ...
   constexpr bool GROUPS = TOP && !WARP;
+  // A warp's rows: each lane keeps two, of its even and of its odd vectors (the k-th largest of 64 bounds better than that
+  // of 32: 50000 x 4000 with 32 alternatives 792 us with one).
+  constexpr bool PAIRS = TOP && WARP;
   uint32_t best_key = 0, best_group = 0, turn = 0;
-  auto take = [&](const uint4& q, int64_t j, bool in) {
+  float pair_top[2] = {-INFINITY, -INFINITY};
+  uint32_t pair_at[2] = {uint32_t(lo + 1 + tid), uint32_t(lo + 1 + tid + NT)};
+  bool pair_any[2] = {lo + tid < hi, lo + tid + NT < hi};
+  auto take = [&](const uint4& q, int64_t j, bool in, int odd) {
     const float top = Chunk<T>::top(q);
     if constexpr (GROUPS) {
       const uint32_t key = __reduce_max_sync(0xffffffffu, in ? order_key(top) : 0u);
@@ -374,9 +372,14 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
       ++turn;
     }
     if (!in) return;
+    if constexpr (PAIRS) {
+      const bool more = top > pair_top[odd];
+      pair_top[odd] = more ? top : pair_top[odd];
+      pair_at[odd] = more ? uint32_t(j) : pair_at[odd];
+    }
     float v[W];
     Chunk<T>::values(q, v);
-    consume<TOP && WARP>(m, v, top, uint32_t(j), a.c);
+    consume<W>(m, v, top, a.c);
   };
   const T* p = row.vector(lo + 1 + tid);
   int64_t j = lo + 1 + tid;
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) q[u] = load_stream(p + u * NT * W);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) take(q[u], j + u * NT, true);
+    for (int u = 0; u < kUnroll; ++u) take(q[u], j + u * NT, true, u & 1);
   }
   {  // what is left, all of it in flight at once
     uint4 q[kUnroll];
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (j - lane + u * NT > hi) break;
-      take(q[u], j + u * NT, j + u * NT <= hi);
+      take(q[u], j + u * NT, j + u * NT <= hi, u & 1);
     }
   }
   // the elements beside the whole vectors: the head with thread 0 of the first CTA, the tail with the last thread of
@@ -420,12 +423,16 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
         best_key = key;
         best_group = group;
       }
-    } else if (!any || (has_head && top >= m.top)) {
-      m.top = -INFINITY;
-      m.at = uint32_t(k);
+    } else if constexpr (PAIRS) {
+      // the head comes before the lane's even vectors, the tail after its odd ones
+      const int h = has_head ? 0 : 1;
+      if (!pair_any[h] || top > pair_top[h] || (has_head && top == pair_top[h])) {
+        pair_top[h] = top;
+        pair_at[h] = uint32_t(k);
+      }
+      pair_any[h] = true;
     }
-    any = true;
-    consume<TOP && WARP>(m, v, top, uint32_t(k), a.c);
+    consume<W>(m, v, top, a.c);
   }
 
   float b = m.b, s0, s1, w0, w1;
@@ -441,7 +448,9 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
     if (lane == 0) write_row(a, r, valid, given, M, log2s, mean);
     if constexpr (TOP) {
-      const uint64_t bound = __shfl_sync(0xffffffffu, sort_warp(any ? order(m.top, m.at) : 0ull, lane), a.top - 1);
+      const uint64_t even = sort_warp(pair_any[0] ? order(pair_top[0], pair_at[0]) : 0ull, lane);
+      const uint64_t odd = sort_warp(pair_any[1] ? order(pair_top[1], pair_at[1]) : 0ull, lane);
+      const uint64_t bound = __shfl_sync(0xffffffffu, merge_warp(even, odd, lane), a.top - 1);
       // vectors are few here: all of them are looked through
       for (int64_t j0 = 0; j0 <= tail; j0 += 32) {
         const int64_t jj = j0 + lane;
@@ -692,8 +701,12 @@ int xt_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens,
   cudaStream_t s = as_stream(stream);
   const int64_t bytes = V * int64_t(dtype_size(dt));
   // Short rows go to a warp each; longer ones to a CTA, and where the rows are too few to fill the GPU to a cluster of
-  // CTAs, as long as each of them keeps 8 KB of the row.
-  const bool warp = bytes <= 4096;
+  // CTAs, as long as each of them keeps 8 KB of the row.  With alternatives a CTA pays some five barriers a row, and a row
+  // of fewer groups of 512 bytes than alternatives would put all its elements in order: up to 16 KB a warp takes the row
+  // where there are eight for every SM (25000 x 8000 with 20: 237 us, 359 by CTAs), up to 8 KB where the groups are too
+  // few (100 x 4000 with 20: 25 us, 58); 3 x 8000 with 5 take 10 us by CTAs and 21 by warps.
+  const bool warp = bytes <= 4096 || (top && bytes <= 16384 && rows >= int64_t(num_sms()) * 8) ||
+                    (top && bytes <= 8192 && bytes < int64_t(top + 1) * 512);
   int cl = 1;
   while (!warp && cl < 8 && rows * cl * 2 <= int64_t(num_sms()) * 4 && bytes >= int64_t(cl) * 2 * 8192) cl *= 2;
   const int64_t grid = warp ? ceil_div(rows, kWarps) : rows * cl;
