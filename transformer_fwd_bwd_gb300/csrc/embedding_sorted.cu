@@ -3,8 +3,8 @@
 //
 // xt_embedding_plan sorts the tokens by id, those of one id by t: up to kRankTokens of them by counting (below), more by
 // a stable radix sort, least significant digit first,
-// by one cluster of CTAs (hardware barriers, no waiting on memory; 16 CTAs for many tokens: 131072 in 35 us where 8 take 56), every digit of up to 9 bits two sweeps over the
-// cluster's tokens: counts of each warp, their prefix over warps, CTAs and digits, then the moves.  One launch; 16 bits
+// by one cluster of CTAs (hardware barriers, no waiting on memory; 16 CTAs for many tokens: 131072 in 35 us where 8 take
+// 56), every digit of up to 9 bits two sweeps over the cluster's tokens: counts of each warp, their prefix over warps, CTAs and digits, then the moves.  One launch; 16 bits
 // of id take two digits.
 //
 // The gradient cuts the sorted tokens into chunks of 8 to 32.  A warp takes a chunk and 256 columns, keeps the running
