@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const int3
   uint32_t rank, cl;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
+  // the other CTAs are running before anything is stored into them (waited for at the first digit's totals)
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   pdl_begin();
   if (rank == 0 && threadIdx.x == 0) *static_cast<PlanHeader*>(plan) = PlanHeader{T, V};
   uint64_t* sorted = plan_entries(plan);
@@ -138,6 +140,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const int3
     }
     __syncthreads();
     // counts → prefix over the CTA's warps; the CTA's totals go to every CTA of the cluster
+    if (p == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     if (threadIdx.x < kDigits) {
       uint32_t sum = 0;
 #pragma unroll 8
