@@ -16,6 +16,7 @@
 
 #include <cuda.h>
 
+#include "cluster_drain.cuh"
 #include "common.cuh"
 
 namespace xt {
@@ -88,6 +89,10 @@ __device__ __forceinline__ void fence_barrier_init() {
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Counts bytes on a barrier as landed that no copy brings.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -308,6 +313,48 @@ __device__ __forceinline__ void tma_load_4d_mc(uint32_t dst, const CUtensorMap* 
       "[%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(mask)
       : "memory");
+}
+// Stores `value` at this CTA's shared address `slot`, and arrives on its barrier `counted`, in the CTAs [first, first + n) of
+// the cluster.
+__device__ __forceinline__ void cluster_tell(uint32_t slot, uint32_t counted, int value, int first, int n) {
+  for (int c = first; c < first + n; ++c) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(slot, uint32_t(c))), "r"(value) : "memory");
+    mbar_arrive_cluster(mapa_shared(counted, uint32_t(c)));
+  }
+}
+// Limit of the wait for the others' counts: their producers end at most a wait after the last MMA, which ends at most a wait
+// after this CTA's.
+__device__ __forceinline__ uint64_t counted_limit(uint64_t wait_ns) {
+  return kTimeoutNs + 2 * (wait_ns < (1ull << 62) ? wait_ns : 1ull << 62);
+}
+// Waits (bounded) until every copy that the cluster's CTAs asked for into this CTA's stages, or with a completion on its full
+// barriers, has landed: see cluster_drain.cuh.  counts[c]: fills asked for by CTA c, as it told this one (barrier `counted`);
+// bytes[c]: what a fill of CTA c brings to a barrier here; relayed: arrivals that another thread passed on to these barriers,
+// one for each fill (null: none expected).  False when a wait ran out.
+template <int CL, int STAGES>
+__device__ __forceinline__ bool cluster_drain(uint64_t* full, uint64_t* counted, const volatile int* counts, int self,
+                                              int issued, const uint32_t (&bytes)[CL], const volatile int* relayed,
+                                              uint64_t wait_ns, volatile int* abort_flag) {
+  const bool known = mbar_wait_spin_cl(smem_u32(counted), 0, counted_limit(wait_ns));
+  int n[CL], most = issued, least = issued;
+#pragma unroll
+  for (int c = 0; c < CL; ++c) {
+    n[c] = known ? counts[c] : issued;
+    most = n[c] > most ? n[c] : most;
+    least = n[c] < least ? n[c] : least;
+  }
+  const int passed = relayed && known ? *relayed : most;
+  if (most != least) *abort_flag = 1;  // no product is taken of a stage that is made up for below
+  for (int f = most - 1; f >= 0 && f >= most - STAGES; --f) {
+    const DrainStep d = drain_step<CL>(f, n, self, bytes);
+    if (!d.wait) continue;
+    const uint32_t bar = smem_u32(&full[f % STAGES]);
+    if (d.complete) mbar_complete_tx(bar, d.complete);
+    if (d.expect) mbar_expect_tx(bar, d.expect);
+    if (passed <= f) mbar_arrive(bar);
+    if (!mbar_wait(bar, uint32_t(f / STAGES) & 1)) return false;
+  }
+  return known;
 }
 template <int CG>
 __device__ __forceinline__ void tmem_alloc_cg(uint32_t dst_smem, uint32_t ncols) {
@@ -643,6 +690,10 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
   uint64_t* mma_done = bars + 2 * STAGES + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // fills asked for by every CTA of the cluster, and those that the odd CTA's relay passed on, as they report them at the end
+  uint64_t* counted = bars + 2 * STAGES + 6;
+  int* counts = reinterpret_cast<int*>(bars + 2 * STAGES + 7);
+  static_assert((2 * STAGES + 7) * 8 + (CL + 1) * 4 <= C_::BAR_BYTES, "room for the barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -655,6 +706,7 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
       mbar_init(smem_u32(&tempty[b]), epilogue_warps(ACT) * CG);
     }
     mbar_init(smem_u32(mma_done), 1);
+    if constexpr (CG == 2) mbar_init(smem_u32(counted), CL + (MC == 2 ? 1 : 0));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -774,14 +826,29 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
       }
-      // Wait (bounded) for the copies that may still be in flight: the last min(STAGES, issued)
-      // fills, so no TMA write lands in shared memory after the CTA exits.  A pair's full
-      // barriers live in the even CTA and count both CTAs' bytes: the even CTA waits for both,
-      // and the cluster barrier before exit keeps the odd CTA resident until then.
-      const int pending = rank != 0 ? 0 : issued < STAGES ? issued : STAGES;
-      for (int i = 0; i < pending; ++i) {
-        if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
-        if (!mbar_wait(smem_u32(&full[stage]), phase)) { give_up(); break; }
+      // Wait (bounded) for the copies that may still be in flight: the last STAGES fills, so no TMA
+      // write lands in shared memory after a CTA exits.  A pair's full barriers live in the even CTA
+      // and count both CTAs' bytes: the even CTA waits for both, and the cluster barrier before exit
+      // keeps the odd CTA resident until then.  Multicast stages of B complete in every CTA.
+      if constexpr (CG == 1) {
+        const int pending = issued < STAGES ? issued : STAGES;
+        for (int i = 0; i < pending; ++i) {
+          if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
+          if (!mbar_wait(smem_u32(&full[stage]), phase)) { give_up(); break; }
+        }
+      } else {
+        cluster_tell(smem_u32(&counts[crank]), smem_u32(counted), issued, 0, MC == 2 ? CL : 1);
+        if (MC == 2 || rank == 0) {
+          uint32_t bytes[CL];
+#pragma unroll
+          for (int c = 0; c < CL; ++c)
+            bytes[c] = MC == 1 ? uint32_t(C_::STAGE_BYTES)
+                               : (rank == 0 && (c >> 1) == pidx ? uint32_t(C_::A_BYTES) : 0u) +
+                                     ((c & 1) == rank ? uint32_t(C_::B_BYTES / 2) : 0u);
+          if (!cluster_drain<CL, STAGES>(full, counted, counts, crank, issued, bytes,
+                                         MC == 2 && rank == 0 ? &counts[CL] : nullptr, p.wait_ns, abort_flag))
+            give_up();
+        }
       }
     }
   } else if (warp == 1) {
@@ -854,6 +921,7 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
       int stage = 0;
       uint32_t phase = 0;
       const uint32_t full_at = mapa_shared(smem_u32(&full[0]), leader);
+      int relayed = 0;
       Cursor cur = cursor_begin(p, unit, units);
       int t, kb0, kb1;
       bool ok = true;
@@ -863,10 +931,12 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
         for (int kb = ti.kb_begin; kb < ti.kb_end; ++kb) {
           if (*abort_flag || !mbar_wait_spin(smem_u32(&full[stage]), phase, p.wait_ns)) { ok = false; break; }
           mbar_arrive_cluster(full_at + uint32_t(stage * 8));
+          ++relayed;
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
       }
       if (!ok) give_up();
+      cluster_tell(smem_u32(&counts[CL]), smem_u32(counted), relayed, leader, 2);
     }
   } else {
     // -------------------------------------------------------------------- epilogue
