@@ -85,3 +85,17 @@ def test_gated_block(short_waits):
         return gu, h, dgu, dw
     assert kinds(run)[:2] == [1256, 1256]
     runs_out_and_recovers(run)
+
+
+def test_muon(short_waits):
+    """Enough matrices for the tiles that pairs share."""
+    shapes = [(300, 700)] * 14 + [(769, 264)] * 8 + [(256, 256)] * 5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    grads = [torch.randn(*s, generator=g, device="cuda") for s in shapes]
+
+    def run():
+        p, m = ([torch.zeros(*s, device="cuda") for s in shapes] for _ in range(2))
+        xt.xt_muon_step(xt.muon_config(0.02), p, grads, m)
+        torch.cuda.synchronize()
+        return (*p, *m)
+    runs_out_and_recovers(run)

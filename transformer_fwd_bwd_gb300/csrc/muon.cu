@@ -113,6 +113,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
   uint64_t* mma_done = tfull + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* counted = tfull + 6;  // the pair's stages asked for, as its producers report them at the end
+  int* counts = reinterpret_cast<int*>(tfull + 7);
+  static_assert((2 * kStages + 7) * 8 + kCg * 4 <= 256, "room for the barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -124,6 +127,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
       mbar_init(smem_u32(&tempty[b]), kEpilogueWarps * kCg);
     }
     mbar_init(smem_u32(mma_done), 1);
+    if constexpr (kCg == 2) mbar_init(smem_u32(counted), 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -184,11 +188,17 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
       }
-      // copies that may still be in flight (both CTAs' bytes are counted in the even one) land before the CTA exits
-      const int pending = rank != 0 ? 0 : issued < kStages ? issued : kStages;
-      for (int i = 0; i < pending; ++i) {
-        if (--stage < 0) { stage = kStages - 1; phase ^= 1; }
-        if (!mbar_wait(smem_u32(&full[stage]), phase)) { give_up(); break; }
+      // copies that may still be in flight land before a CTA exits (both CTAs' bytes are counted in the even one)
+      if constexpr (kCg == 1) {
+        for (int i = 0; i < kStages && i < issued; ++i) {
+          if (--stage < 0) { stage = kStages - 1; phase ^= 1; }
+          if (!mbar_wait(smem_u32(&full[stage]), phase)) { give_up(); break; }
+        }
+      } else {
+        cluster_tell(smem_u32(&counts[rank]), smem_u32(counted), issued, 0, 1);
+        const uint32_t bytes[2] = {kStageBytes, kStageBytes};
+        if (rank == 0 && !cluster_drain<2, kStages>(full, counted, counts, rank, issued, bytes, nullptr, a.wait_ns, abort_flag))
+          give_up();
       }
     }
   } else if (warp == 1) {
