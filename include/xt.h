@@ -693,8 +693,9 @@ int xt_adamw8_decode(int n, const int8_t* const* m_code, const uint8_t* const* r
  *   W ← W (1 − lr·λ) − lr·rms·√max(rows, cols)·X      (rms: the update's root mean square is about rms·lr).
  * s = grad_scale, μ = momentum, λ = weight_decay.  momentum buffers M (float32) start at 0 and are updated in place with
  * W; grad is read only; shadow as for xt_adamw_step.  Products are taken on f16 tensor cores from operands in two terms
- * (22 bits), so X is as accurate as with float32 products.  A gradient of 0 with a momentum of 0 leaves X = 0; one that is
- * not finite makes its own matrix NaN.  param, grad, momentum, shadow, rows and cols are HOST arrays; buffers are
+ * (22 bits), so X is as accurate as with float32 products.  Gradients may be of any
+ * finite size (as long as M and U are finite too).  A gradient of 0 with a momentum of 0 leaves X = 0; one that is not
+ * finite makes its own matrix NaN.  param, grad, momentum, shadow, rows and cols are HOST arrays; buffers are
  * contiguous, of any alignment of float32 (multiples of 8 columns in 16-byte aligned buffers run on 16-byte accesses), and must
  * not overlap.  At most 64 different shapes; matrices of one shape run as a batch.  Workspace: xt_muon_workspace_size
  * bytes, 16-byte aligned, contents on entry do not matter; about 8 bytes per weight and 8·min(rows, cols)² per matrix.

@@ -23,6 +23,7 @@
 
 #include <cmath>
 #include <atomic>
+#include <cfloat>
 #include <cstring>
 
 #include "gemm.cuh"
@@ -408,6 +409,18 @@ __device__ __forceinline__ int matrix_of(const Table& a, int t) {
   return lo;
 }
 
+// The block's sum, in every thread.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < kElemThreads / 32; ++i) v += red[i];
+  return v;
+}
+
 // M ← μ M + s·G and each piece's Σ U².
 __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __grid_constant__ Table a) {
   pdl_begin();
@@ -440,7 +453,19 @@ __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __gri
     for (int64_t i = threadIdx.x; i < len; i += kElemThreads) one(g[i], m[i]);
   }
   sum = group_reduce<false>(sum, kElemThreads, red);
-  if (threadIdx.x == 0) a.part[blockIdx.x] = double(sum);
+  double total = double(sum);
+  // squares beyond float32's range, or so small that they lost bits there: over again in doubles, from the new momentum (the
+  // block's stores lie before the barriers above)
+  if (!(sum >= 1e-20f && sum <= FLT_MAX)) {
+    __shared__ double red64[kElemThreads / 32];
+    total = 0;
+    for (int64_t i = threadIdx.x; i < len; i += kElemThreads) {
+      const double u = double(a.nesterov ? fmaf(a.momentum, m[i], g[i] * a.scale) : m[i]);
+      total = fma(u, u, total);
+    }
+    total = block_sum(total, red64);
+  }
+  if (threadIdx.x == 0) a.part[blockIdx.x] = total;
 }
 
 // 8 elements of a row of a matrix whose rows are whole 16 bytes, or one.
@@ -488,7 +513,7 @@ __device__ __forceinline__ bool whole_rows(const Matrix& k, const void* a, const
 
 // X₀ from the new momentum, in two terms.
 template <int W>
-__device__ __forceinline__ void begin_piece(const Table& a, const Matrix& k, int64_t base, int64_t len, float f) {
+__device__ __forceinline__ void begin_piece(const Table& a, const Matrix& k, int64_t base, int64_t len, float f1, float f2) {
   for (int64_t i = threadIdx.x * W; i < len; i += kElemThreads * W) {
     float g[W], m[W];
     if constexpr (W == 8) {
@@ -499,7 +524,7 @@ __device__ __forceinline__ void begin_piece(const Table& a, const Matrix& k, int
       m[0] = k.m[base + i];
     }
 #pragma unroll
-    for (int e = 0; e < W; ++e) m[e] = (a.nesterov ? fmaf(a.momentum, m[e], g[e] * a.scale) : m[e]) * f;
+    for (int e = 0; e < W; ++e) m[e] = (a.nesterov ? fmaf(a.momentum, m[e], g[e] * a.scale) : m[e]) * f1 * f2;
     const int64_t r = (base + i) / k.cols, at = r * k.ld + (base + i - r * k.cols);
     Terms<W>::store(k.x + at, k.x + k.x_term + at, m);
   }
@@ -511,18 +536,16 @@ __global__ void __launch_bounds__(kElemThreads) muon_begin_kernel(const __grid_c
   const int pieces = int((k.n + kElemTile - 1) / kElemTile);
   double sum = 0;
   for (int i = threadIdx.x; i < pieces; i += kElemThreads) sum += __ldcg(a.part + k.tile0 + i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = 0;
-#pragma unroll
-  for (int i = 0; i < kElemThreads / 32; ++i) sum += red[i];
-  const float f = float(double(kScale) / (sqrt(sum) + double(a.eps)));
+  const double f = double(kScale) / (sqrt(block_sum(sum, red)) + double(a.eps));
+  // as two factors, the first a power of two: f itself may lie outside float32's range (0 or not a number: the gradient
+  // is not finite)
+  const int e = ((__double2hiint(f) >> 20) & 0x7ff) - 1023, half = e > -250 && e < 250 ? e / 2 : 0;
+  const float f1 = __int_as_float((127 + half) << 23);
+  const float f2 = float(f * __hiloint2double((1023 - half) << 20, 0));
   const int64_t base = int64_t(int(blockIdx.x) - k.tile0) * kElemTile;
   const int64_t len = k.n - base < kElemTile ? k.n - base : kElemTile;
-  if (whole_rows(k, k.g, k.m)) begin_piece<8>(a, k, base, len, f);
-  else begin_piece<1>(a, k, base, len, f);
+  if (whole_rows(k, k.g, k.m)) begin_piece<8>(a, k, base, len, f1, f2);
+  else begin_piece<1>(a, k, base, len, f1, f2);
 }
 
 // W ← W (1 − lr·λ) − step·X, and the working copy.
