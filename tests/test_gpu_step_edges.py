@@ -1,5 +1,7 @@
 """What a training step's operators (sorted embeddings, the gated block, Muon) have to hold beside their ordinary calls: plans
-made while other kernels hold the SMs."""
+made while other kernels hold the SMs, the override that keeps paired kernels out."""
+import re
+
 import pytest
 import torch
 
@@ -40,3 +42,38 @@ def test_plans_beside_kernels_that_hold_the_gpu():
             got, at = entries(plan, ids.numel())
             assert torch.equal(got, want.values) and torch.equal(at, want.indices)
     assert xt.device_errors() == 0
+
+
+def captured(fn, path):
+    """A graph of what fn launches, as the driver prints it (kernels by name)."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    graph.enable_debug_mode()
+    with torch.cuda.graph(graph):
+        fn()
+    graph.debug_dump(str(path))
+    return path.read_text()
+
+
+def test_muon_without_pairs(tmp_path):
+    """xt_gemm_set_pairing(1), never a paired kernel, holds for Muon's products too, and X is as accurate."""
+    shapes = [(300, 700)] * 14 + [(769, 264)] * 8 + [(256, 256)] * 5   # tiles for pairs
+    g = torch.Generator(device="cuda").manual_seed(4)
+    grads = [torch.randn(*s, generator=g, device="cuda") for s in shapes]
+
+    def run():
+        p, m = ([torch.zeros(*s, device="cuda") for s in shapes] for _ in range(2))
+        xt.xt_muon_step(xt.muon_config(0.02), p, grads, m)
+        return p
+    with_pairs = run()
+    pair, one = (re.compile(rf"muon_product_kernel(?:<{k}>|ILi{k}E)") for k in (2, 1))
+    assert pair.search(captured(run, tmp_path / "pairs.dot"))
+    try:
+        xt.gemm_set_pairing(1)
+        single = run()
+        text = captured(run, tmp_path / "single.dot")
+    finally:
+        xt.gemm_set_pairing(0)
+    assert one.search(text) and not pair.search(text)
+    # both are within 9e-4 of the formula's X (tests/test_gpu_muon.py), whose norm is at least 0.68 of its root rank
+    for a, b in zip(with_pairs, single):
+        assert float((a - b).norm()) <= 2 * 9e-4 * float(a.norm())

@@ -98,6 +98,7 @@ static int g_schedule = 0;
 // Paired-kernel override (xt_gemm_set_pairing): 0 the model's choice, 1 never, 2 wherever allowed,
 // 3 the multicast form of the paired kernel wherever allowed (else as 2).
 static int g_pairing = 0;
+int pairing() { return g_pairing; }
 // Tile-width override (xt_gemm_set_tile): 0 the model's choice, else that BN wherever it is a
 // candidate.
 static int g_tile = 0;

@@ -111,6 +111,8 @@ int launch_bf16_pair(int bn, int mc, bool a_mn, bool b_mn, const CUtensorMap& ta
                      const CUtensorMap& tc, const CUtensorMap& tc2, const Params& p, int grid, cudaStream_t s);
 // CTA pairs of the paired kernel that can be resident at once on the current device (0 if none).
 int pair_capacity();
+// The pairing override (xt_gemm_set_pairing): 1 never the paired kernels.
+int pairing();
 // Clusters of two pairs (the multicast form) that can be resident at once (0 if none).
 int mc_capacity();
 

@@ -656,16 +656,15 @@ int make_map(CUtensorMap* tm, __half* base, int64_t rows, int64_t cols, int64_t 
 int products(const Layout& l, int first, int count, int which, int flip, __half* ws, cudaStream_t s) {
   Products a{};
   a.groups = count;
-  const int pairs = pair_capacity();
-  if (pairs < 1) return fail(XT_ERR_CUDA, "xt_muon_step: no CTA pair can be resident");
-  // 256 × 256 tiles where they fill half of the pairs
+  // 256 × 256 tiles where they fill half of the pairs (and pairs may be used at all)
+  const int pairs = pairing() == 1 ? 0 : pair_capacity();
   int64_t big = 0;
   for (int i = 0; i < count; ++i) {
     const Shape& sh = l.shape[first + i];
     const int64_t nk = ceil_div(sh.k, 2 * BM);
     big += sh.count * (which < 2 ? nk * (nk + 1) / 2 : ceil_div(sh.rows, 2 * BM) * ceil_div(sh.cols, 2 * BM));
   }
-  const int cg = 2 * big >= pairs ? 2 : 1, tile = BM * cg;
+  const int cg = pairs > 0 && 2 * big >= pairs ? 2 : 1, tile = BM * cg;
   for (int i = 0; i < count; ++i) {
     const Shape& sh = l.shape[first + i];
     Group& g = a.g[i];
