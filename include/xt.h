@@ -483,9 +483,9 @@ int xt_embedding_bwd(const int32_t* ids, const void* dh, void* dE, void* dP, int
  * are zeroed.  An id outside [0, V) sets XT_DEVERR_INDEX, its row of h is NaN and its row of dh is left out.  A plan
  * made for another T or V sets XT_DEVERR_PLAN and the backward writes nothing.  The workspace
  * (xt_embedding_sorted_bwd_workspace_size, 16-byte aligned) holds the shares of ids whose tokens are summed in several
- * pieces; its contents on entry do not matter.  dh, dE, the plan and the workspace must not overlap.  E and h, and dh
- * and dE, may have different dtypes; rows are contiguous, any d (multiples of 8 in 16-byte aligned buffers run on
- * 16-byte accesses). */
+ * pieces; its contents on entry do not matter, and one made for a larger T serves any smaller one.  dh, dE, the plan and
+ * the workspace must not overlap.  E and h, and dh and dE, may have different dtypes; rows are contiguous, any d
+ * (multiples of 8 in 16-byte aligned buffers run on 16-byte accesses). */
 int xt_embedding_lookup_fwd(const int32_t* ids, const void* E, void* h, int64_t T, int64_t d, int64_t V, float scale,
                             int dt_e, int dt_h, void* stream);
 int xt_embedding_plan_size(int64_t T, size_t* bytes);

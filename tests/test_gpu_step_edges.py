@@ -1,5 +1,6 @@
 """What a training step's operators (sorted embeddings, the gated block, Muon) have to hold beside their ordinary calls: plans
-made while other kernels hold the SMs, the override that keeps paired kernels out."""
+made while other kernels hold the SMs, the override that keeps paired kernels
+out, workspaces made for larger batches."""
 import re
 
 import pytest
@@ -77,3 +78,24 @@ def test_muon_without_pairs(tmp_path):
     # both are within 9e-4 of the formula's X (tests/test_gpu_muon.py), whose norm is at least 0.68 of its root rank
     for a, b in zip(with_pairs, single):
         assert float((a - b).norm()) <= 2 * 9e-4 * float(a.norm())
+
+
+def test_embedding_workspace_of_a_larger_batch():
+    """A batch just short of the length at which its pieces grow longer needs more room than the longer ones."""
+    V, d = 1000, 768
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ws = xt.embedding_sorted_workspace(52000, d)
+    for T in (51800, 25900, 3):
+        ids = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+        dh = torch.randn(T, d, generator=g, device="cuda")
+        plan = xt.embedding_plan_buffer(T)
+        xt.xt_embedding_plan(ids, V, plan)
+        dE, own = torch.empty(V, d, device="cuda"), torch.empty(V, d, device="cuda")
+        xt.xt_embedding_sorted_bwd(plan, dh, dE, ws=ws)
+        xt.xt_embedding_sorted_bwd(plan, dh, own)
+        assert torch.equal(dE, own)
+        want = torch.zeros(V, d, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dh.double())
+        mag = torch.zeros_like(want).index_add_(0, ids.long(), dh.double().abs())
+        # at most 32 additions in a piece, then the pieces of an id
+        count = int(torch.bincount(ids).max())
+        assert ((dE.double() - want).abs() <= (count + 2) * 2.0 ** -24 * mag).all()

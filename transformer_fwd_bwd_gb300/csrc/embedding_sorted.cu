@@ -270,11 +270,20 @@ constexpr int kCols = 256;  // columns of a warp: 8 to a lane
 constexpr int kWarps = 8;
 
 // Sorted tokens per chunk: 32, or fewer where that leaves too few warps to keep HBM busy.
+constexpr int64_t kManyWarps = 4864;  // 32 on each of 152 SMs
 __host__ inline int chunk_tokens(int64_t T, int64_t d) {
   const int64_t tiles = ceil_div(d, kCols);
   int c = 32;
-  while (c > 8 && ceil_div(T, c) * tiles < 4864) c /= 2;  // 32 warps on each of 152 SMs
+  while (c > 8 && ceil_div(T, c) * tiles < kManyWarps) c /= 2;
   return c;
+}
+__host__ inline size_t part_bytes_for(int64_t chunks, int64_t d) { return size_t(chunks) * 2 * size_t(d) * 4; }
+// The most chunks that a batch of up to T tokens is cut into.  Where chunks grow from c to 2c tokens their number falls: the
+// last T of chunks of c has fewer than kManyWarps warps' worth of chunks of 2c, that is twice as many of c.
+__host__ inline int64_t most_chunks(int64_t T, int64_t d) {
+  const int c = chunk_tokens(T, d);
+  const int64_t chunks = ceil_div(T, c), shorter = 2 * ((kManyWarps - 1) / ceil_div(d, kCols));
+  return c > 8 && shorter > chunks ? shorter : chunks;
 }
 
 struct Grad {
@@ -628,7 +637,7 @@ int xt_embedding_plan(const int32_t* ids, int64_t T, int64_t V, void* plan, size
 int xt_embedding_sorted_bwd_workspace_size(int64_t T, int64_t d, size_t* bytes) {
   XT_REQUIRE(bytes != nullptr, "xt_embedding_sorted_bwd_workspace_size: NULL pointer");
   XT_TRY(sizes_ok("xt_embedding_sorted_bwd_workspace_size", T, d, 1));
-  *bytes = size_t(ceil_div(T, chunk_tokens(T, d))) * 2 * size_t(d) * 4;
+  *bytes = part_bytes_for(most_chunks(T, d), d);
   return XT_OK;
 }
 
@@ -643,8 +652,7 @@ int xt_embedding_sorted_bwd(const void* plan, size_t plan_bytes, const void* dh,
              plan ? plan_bytes : size_t(0), plan_bytes_for(T));
   if (!aligned16(plan)) return fail(XT_ERR_ALIGNMENT, "%s: the plan must be 16-byte aligned", fn);
   XT_REQUIRE(dE && (T == 0 || dh), "%s: NULL pointer", fn);
-  size_t need = 0;
-  XT_TRY(xt_embedding_sorted_bwd_workspace_size(T, d, &need));
+  const size_t need = part_bytes_for(ceil_div(T, chunk_tokens(T, d)), d);
   XT_REQUIRE(need == 0 || (ws && ws_bytes >= need), "%s: the workspace holds %zu bytes, %zu are needed", fn,
              ws ? ws_bytes : size_t(0), need);
   if (ws && !aligned16(ws)) return fail(XT_ERR_ALIGNMENT, "%s: the workspace must be 16-byte aligned", fn);
