@@ -403,9 +403,9 @@ int xt_cross_entropy_bwd(const void* logits, const int32_t* targets, const float
  *   dx_v (+)= scale·(d_logp·([v = token] − p_v) − d_entropy·p_v·(log p_v + entropy)).
  * A row whose d_logp and d_entropy are both 0 gets zeros whatever it holds (padding).
  * entropy and stats may be NULL in the forward; the backward needs stats, and entropy where d_entropy is given.
- * Logits of −∞ (banned tokens) have p = 0 and gradient 0; a row that holds a NaN or +∞, or nothing but −∞, has no
- * distribution: NaN in all its values, −1 as its ids.  Any finite logits are allowed, those of the type's lowest
- * value among them.  A token outside [0, V) sets XT_DEVERR_INDEX and makes logp and the gradient of its row NaN.
+ * Logits of −∞ (banned tokens) have p = 0 and gradient 0, but scale·d_logp where the row's token is one; a row that
+ * holds a NaN or +∞, or nothing but −∞, has no distribution: NaN in all its values, −1 as its ids.  Any finite logits
+ * are allowed, those of the type's lowest value among them.  A token outside [0, V) sets XT_DEVERR_INDEX and makes logp and the gradient of its row NaN.
  * Layout: row r of logits at logits + r·ld (ld ≥ V), dlogits likewise with ld_d; dlogits may be logits (one dtype
  * and stride, acc = 0).  Any alignment of the element type; rows of aligned 16 bytes need no more than that.
  * scale in [1e-6, 1e6].  Entropies are accurate to about 1e-6 absolute.  Deterministic.
@@ -694,11 +694,13 @@ int xt_adamw8_decode(int n, const int8_t* const* m_code, const uint8_t* const* r
  *   W ← W (1 − lr·λ) − lr·rms·√max(rows, cols)·X      (rms: the update's root mean square is about rms·lr).
  * s = grad_scale, μ = momentum, λ = weight_decay.  momentum buffers M (float32) start at 0 and are updated in place with
  * W; grad is read only; shadow as for xt_adamw_step.  Products are taken on f16 tensor cores from operands in two terms
- * (22 bits), so X is as accurate as with float32 products.  Gradients may be of any
- * finite size (as long as M and U are finite too).  A gradient of 0 with a momentum of 0 leaves X = 0; one that is not
- * finite makes its own matrix NaN.  param, grad, momentum, shadow, rows and cols are HOST arrays; buffers are
- * contiguous, of any alignment of float32 (multiples of 8 columns in 16-byte aligned buffers run on 16-byte accesses), and must
- * not overlap.  At most 64 different shapes; matrices of one shape run as a batch.  Workspace: xt_muon_workspace_size
+ * (22 bits) with float32 sums that they cut off instead of rounding: X is good to a few 1e-6 in norm, two to five times
+ * the error of float32 products, growing with the sides.  A matrix is orthogonalised as it is given: projections that are
+ * stored side by side in one ([Wq | Wk | Wv]) are taken as one matrix, in the polynomial and in √max(rows, cols).
+ * Gradients may be of any finite size (as long as M and U are finite too).  A gradient of 0 with a momentum of 0 leaves
+ * X = 0; one that is not finite makes its own matrix NaN.  param, grad, momentum, shadow, rows and cols are HOST arrays;
+ * buffers are contiguous, of any alignment of float32 (multiples of 8 columns in 16-byte aligned buffers run on 16-byte
+ * accesses), and must not overlap.  At most 64 different shapes; matrices of one shape run as a batch.  Workspace: xt_muon_workspace_size
  * bytes, 16-byte aligned, contents on entry do not matter; about 8 bytes per weight and 8·min(rows, cols)² per matrix.
  * Deterministic.  Device-side waits are bounded (XT_DEVERR_TIMEOUT). */
 typedef struct xt_muon_config {

@@ -55,6 +55,7 @@ def captured(fn, path):
     return path.read_text()
 
 
+@pytest.mark.filterwarnings("ignore:DEBUG")
 def test_muon_without_pairs(tmp_path):
     """xt_gemm_set_pairing(1), never a paired kernel, holds for Muon's products too, and X is as accurate."""
     shapes = [(300, 700)] * 14 + [(769, 264)] * 8 + [(256, 256)] * 5   # tiles for pairs

@@ -180,7 +180,9 @@ class NativeBlock:
         matrices="muon": the layers' weight matrices (Wqkv, Wo, Wup, Wdown) take xt_muon_step with muon_lr,
         muon_momentum, muon_rms and weight_decay instead, and keep one float32 momentum each; embeddings, positions and
         norms stay with AdamW, whose gradient norm and clipping then cover those alone (Muon's update has a norm of its
-        own, whatever the gradient's)."""
+        own, whatever the gradient's).  The matrices are taken as the stack stores them: Wqkv, and Wup of a SwiGLU stack, hold
+        projections side by side and are orthogonalised, and their step sized, as one matrix each, which is not the same as
+        Muon on every projection by itself."""
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         if matrices not in ("adamw", "muon"):

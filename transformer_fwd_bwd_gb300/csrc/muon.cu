@@ -5,11 +5,13 @@
 //
 // Precision.  The polynomial's slope at 0 is a = 3.44, so what is rounded off X₀ grows by up to a⁵ = 485 in the
 // directions of small singular values: with every operand rounded to bf16 X comes out with a relative error of a few
-// 10⁻², to f16 of a few 10⁻³.  Here X, A and B = b A + c A² are held as two f16 terms each (value and remainder,
-// 22 bits, scaled by 2¹⁰ so that remainders stay normal numbers; singular values stay below 1.21, entries of B below
-// 16), and a product is three: hi·lo + lo·hi + hi·hi, float32 sums in tensor memory.  The sums there are cut off, not
-// rounded, after every 16 elements of K: the small products come first, while the sum is small.  X is then good to a few 10⁻⁶,
-// as with float32 products, at three times the operations of a single f16 product.
+// 10⁻², to f16 of a few 10⁻³.  Here X, A and B = b A + c A² are held as two f16 terms each (value and remainder, scaled by
+// 2¹⁰: 22 bits of what is at least 2⁻³ as held, 1.2·10⁻⁴ of X; the remainders of smaller entries are subnormal, and what is held
+// is good to 2⁻²⁵, 3·10⁻¹¹ of X; singular values stay below 1.21, entries of B below 16), and a product is three:
+// hi·lo + lo·hi + hi·hi, float32 sums in tensor memory.  The sums there are cut off, not rounded, after every 16 elements of K:
+// the small products come first, while the sum is small.  X is then good to a few 10⁻⁶ at three times the operations of a
+// single f16 product: two to five times what float32 products leave, more with a longer K (the weights of 12 layers of width 768
+// after a step 2.3·10⁻⁶ against 4.9·10⁻⁷ in norm).
 //
 // Work.  A and A² are symmetric: only the tiles on and above the diagonal are computed, the others written from them.
 // Matrices of one shape form a batch, up to kMaxGroups shapes run in one launch, so that the tiles of all of a model's

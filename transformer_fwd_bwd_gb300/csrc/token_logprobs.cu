@@ -19,9 +19,10 @@
 // depends on timing.
 //
 // Bound by HBM: a logit is read once (backward: read and written).  On one GB300: 8192 x 50304 bf16 forward 142 us (5.8 TB/s),
-// backward 258 us (6.4 TB/s); 4096 x 128256 with 20 alternatives 215 us (4.9 TB/s: a quarter more instructions and five block
-// barriers at a row's end, during which its block loads nothing); 3 x 50257 with 5 alternatives 10 us.  Six blocks per SM of 40
-// registers with four vectors in flight: fewer blocks or more vectors were 2 to 10 % slower.
+// backward 258 us (6.4 TB/s); 4096 x 128256 with 20 alternatives 213 us (4.9 TB/s; 163 without: a quarter more instructions and 14
+// block barriers at a row's end, six for either merge of the warps' lists, during which its block loads nothing); 3 x 50257 with
+// 5 alternatives 7.5 us.  Six blocks per SM of 40 registers with four vectors in flight: fewer blocks or more vectors were 2 to 10 %
+// slower.
 #include <cfloat>
 #include <cstring>
 
@@ -701,10 +702,12 @@ int xt_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens,
   cudaStream_t s = as_stream(stream);
   const int64_t bytes = V * int64_t(dtype_size(dt));
   // Short rows go to a warp each; longer ones to a CTA, and where the rows are too few to fill the GPU to a cluster of
-  // CTAs, as long as each of them keeps 8 KB of the row.  With alternatives a CTA pays some five barriers a row, and a row
-  // of fewer groups of 512 bytes than alternatives would put all its elements in order: up to 16 KB a warp takes the row
-  // where there are eight for every SM (25000 x 8000 with 20: 237 us, 359 by CTAs), up to 8 KB where the groups are too
-  // few (100 x 4000 with 20: 25 us, 58); 3 x 8000 with 5 take 10 us by CTAs and 21 by warps.
+  // CTAs, as long as each of them keeps 8 KB of the row.  With alternatives a CTA pays 14 barriers a row, and one whose part
+  // of the row has fewer groups of 512 bytes than there are alternatives puts all of its elements in order: up to 16 KB a warp
+  // takes the row where there are eight for every SM (25000 x 8000 with 20: 237 us, 359 by CTAs), up to 8 KB where the groups
+  // are too few (100 x 4000 with 20: 25 us, 58); 3 x 8000 with 5 take 10 us by CTAs and 21 by warps.  Longer rows do not
+  // look at the number of alternatives, so with 17 to 32 of them a CTA's 8 to 16 KB can have too few groups: 3 x 50257 take
+  // 7.5 us with 5, 11 with 20 and 108 with 32 (eight CTAs of 24 groups), 16 x 36000 8, 88 and 89, 1000 x 5000 14, 29 and 206.
   const bool warp = bytes <= 4096 || (top && bytes <= 16384 && rows >= int64_t(num_sms()) * 8) ||
                     (top && bytes <= 8192 && bytes < int64_t(top + 1) * 512);
   int cl = 1;
