@@ -8,7 +8,7 @@ import pytest
 
 CSRC = pathlib.Path(__file__).resolve().parents[1] / "transformer_fwd_bwd_gb300" / "csrc"
 # stores, arrivals and addresses in another CTA; copies that complete on another CTA's barrier
-REMOTE = re.compile(r"st\.shared::cluster|mapa\.shared::cluster|mapa_shared\(|mbar_arrive_cluster\(|tma_load_4d_pair\(|tma_load_4d_mc\(")
+REMOTE = re.compile(r"st\.shared::cluster|mapa\.shared::cluster|mapa_shared\(|mbar_arrive_cluster\(|cluster_store\(|tma_load_4d_pair\(|tma_load_4d_mc\(")
 WAIT = re.compile(r"barrier\.cluster\.wait|cluster_sync_all\(\)|cluster_barrier\(\)")
 
 

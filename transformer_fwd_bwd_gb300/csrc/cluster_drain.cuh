@@ -1,8 +1,8 @@
-// The end of a cluster's copy producers.  A stage's full barrier may count bytes that several CTAs ask for, while only its
-// own CTA announces them (one arrival that expects all the bytes of a fill).  When a wait has run out, the CTAs may have asked
-// for different numbers of fills: an announced fill lacks the bytes of a CTA that stopped earlier, and a CTA that went
+// The end of a cluster after a wait that ran out (without one the MMA issuers have waited for every copy).  A stage's full barrier may count bytes that several CTAs ask for, while only its
+// own CTA announces them (one arrival that expects all the bytes of a fill).  The CTAs may have asked for different numbers
+// of fills: an announced fill lacks the bytes of a CTA that stopped earlier, and a CTA that went
 // further has copies under way that nobody announced.  Before a CTA exits, every copy into shared memory of the cluster has
-// to have landed, so the producers tell each other how many fills they asked for, and what each barrier's count lacks is
+// to have landed, so the CTAs tell each other how many fills they asked for, and what each barrier's count lacks is
 // made up for, after which its phase ends with the last copy that is under way.  A fill is asked for only when the same
 // stage's last one has been consumed everywhere, so only the last STAGES fills are in question, and counts differ by no more.
 #pragma once

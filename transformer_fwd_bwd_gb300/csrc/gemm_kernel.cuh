@@ -314,47 +314,65 @@ __device__ __forceinline__ void tma_load_4d_mc(uint32_t dst, const CUtensorMap* 
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(mask)
       : "memory");
 }
-// Stores `value` at this CTA's shared address `slot`, and arrives on its barrier `counted`, in the CTAs [first, first + n) of
-// the cluster.
-__device__ __forceinline__ void cluster_tell(uint32_t slot, uint32_t counted, int value, int first, int n) {
-  for (int c = first; c < first + n; ++c) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(slot, uint32_t(c))), "r"(value) : "memory");
-    mbar_arrive_cluster(mapa_shared(counted, uint32_t(c)));
+// Stores `value` at this CTA's shared address `at` in the CTAs [first, first + n) of the cluster.
+__device__ __forceinline__ void cluster_store(uint32_t at, int value, int first, int n) {
+#pragma unroll 1
+  for (int c = first; c < first + n; ++c)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(at, uint32_t(c))), "r"(value) : "memory");
+}
+// A give-up in a cluster: every CTA's flag at the shared address `abort_flag` is set.  (Out of line, as the next: code that
+// never runs otherwise costs a fetch on the way of the code around it, 0.3 % of the 12-layer step.)
+template <int CL>
+__device__ __noinline__ void cluster_give_up(uint32_t abort_flag, uint32_t* flag) {
+  cluster_store(abort_flag, 1, 0, CL);
+  flag_error(flag, XT_DEVERR_TIMEOUT);
+}
+// The end of a cluster in which a wait ran out, by all its threads, every role having ended and every CTA being here: waits
+// (bounded) until every copy that any CTA asked for has landed (see cluster_drain.cuh).  full: the shared address of the full
+// barriers; counts: of CL counts of fills asked for, this CTA's own set, and with MC = 2 of the number that the odd CTA's relay
+// passed on, set there.  A pair's full barriers are in the even CTA and count both CTAs' bytes; multicast stages of B complete
+// in every CTA, half of the rows from either pair.
+template <int STAGES, int MC>
+__device__ __noinline__ void cluster_finish(uint32_t full, uint32_t counts, uint32_t a_bytes, uint32_t b_bytes, uint32_t* flag) {
+  constexpr int CL = 2 * MC;
+  const int me = int(cluster_ctarank()), rank = me & 1;
+  auto count = [&](int i) {
+    int v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(counts + uint32_t(i) * 4) : "memory");
+    return v;
+  };
+  if (threadIdx.x == 0) {
+    cluster_store(counts + uint32_t(me) * 4, count(me), 0, CL);
+    if (MC == 2 && rank == 1) cluster_store(counts + CL * 4, count(CL), me - 1, 1);
   }
-}
-// Limit of the wait for the others' counts: their producers end at most a wait after the last MMA, which ends at most a wait
-// after this CTA's.
-__device__ __forceinline__ uint64_t counted_limit(uint64_t wait_ns) {
-  return kTimeoutNs + 2 * (wait_ns < (1ull << 62) ? wait_ns : 1ull << 62);
-}
-// Waits (bounded) until every copy that the cluster's CTAs asked for into this CTA's stages, or with a completion on its full
-// barriers, has landed: see cluster_drain.cuh.  counts[c]: fills asked for by CTA c, as it told this one (barrier `counted`);
-// bytes[c]: what a fill of CTA c brings to a barrier here; relayed: arrivals that another thread passed on to these barriers,
-// one for each fill (null: none expected).  False when a wait ran out.
-template <int CL, int STAGES>
-__device__ __forceinline__ bool cluster_drain(uint64_t* full, uint64_t* counted, const volatile int* counts, int self,
-                                              int issued, const uint32_t (&bytes)[CL], const volatile int* relayed,
-                                              uint64_t wait_ns, volatile int* abort_flag) {
-  const bool known = mbar_wait_spin_cl(smem_u32(counted), 0, counted_limit(wait_ns));
-  int n[CL], most = issued, least = issued;
+  __syncwarp();
+  cluster_sync_all();
+  if (threadIdx.x == 0 && (MC == 2 || rank == 0)) {
+    uint32_t bytes[CL];
+    int n[CL], most = 0;
 #pragma unroll
-  for (int c = 0; c < CL; ++c) {
-    n[c] = known ? counts[c] : issued;
-    most = n[c] > most ? n[c] : most;
-    least = n[c] < least ? n[c] : least;
+    for (int c = 0; c < CL; ++c) {
+      bytes[c] = MC == 1 ? a_bytes + b_bytes
+                         : (rank == 0 && (c >> 1) == (me >> 1) ? a_bytes : 0u) + ((c & 1) == rank ? b_bytes / 2 : 0u);
+      n[c] = count(c);
+      most = n[c] > most ? n[c] : most;
+    }
+    const int relayed = MC == 2 && rank == 0 ? count(CL) : most;
+    for (int f = most - 1; f >= 0 && f >= most - STAGES; --f) {
+      const DrainStep d = drain_step<CL>(f, n, me, bytes);
+      if (!d.wait) continue;
+      const uint32_t bar = full + uint32_t(f % STAGES) * 8;
+      if (d.complete) mbar_complete_tx(bar, d.complete);
+      if (d.expect) mbar_expect_tx(bar, d.expect);
+      if (relayed <= f) mbar_arrive(bar);  // the relay's arrival
+      if (!mbar_wait(bar, uint32_t(f / STAGES) & 1)) {
+        flag_error(flag, XT_DEVERR_TIMEOUT);
+        break;
+      }
+    }
   }
-  const int passed = relayed && known ? *relayed : most;
-  if (most != least) *abort_flag = 1;  // no product is taken of a stage that is made up for below
-  for (int f = most - 1; f >= 0 && f >= most - STAGES; --f) {
-    const DrainStep d = drain_step<CL>(f, n, self, bytes);
-    if (!d.wait) continue;
-    const uint32_t bar = smem_u32(&full[f % STAGES]);
-    if (d.complete) mbar_complete_tx(bar, d.complete);
-    if (d.expect) mbar_expect_tx(bar, d.expect);
-    if (passed <= f) mbar_arrive(bar);
-    if (!mbar_wait(bar, uint32_t(f / STAGES) & 1)) return false;
-  }
-  return known;
+  __syncwarp();
+  cluster_sync_all();
 }
 template <int CG>
 __device__ __forceinline__ void tmem_alloc_cg(uint32_t dst_smem, uint32_t ncols) {
@@ -690,10 +708,9 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
   uint64_t* mma_done = bars + 2 * STAGES + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // fills asked for by every CTA of the cluster, and those that the odd CTA's relay passed on, as they report them at the end
-  uint64_t* counted = bars + 2 * STAGES + 6;
-  int* counts = reinterpret_cast<int*>(bars + 2 * STAGES + 7);
-  static_assert((2 * STAGES + 7) * 8 + (CL + 1) * 4 <= C_::BAR_BYTES, "room for the barriers");
+  // fills asked for by every CTA of the cluster, and those that the odd CTA's relay passed on (see the end)
+  volatile int* counts = reinterpret_cast<volatile int*>(bars + 2 * STAGES + 6);
+  static_assert((2 * STAGES + 6) * 8 + (CL + 1) * 4 <= C_::BAR_BYTES, "room for the barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -706,7 +723,6 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
       mbar_init(smem_u32(&tempty[b]), epilogue_warps(ACT) * CG);
     }
     mbar_init(smem_u32(mma_done), 1);
-    if constexpr (CG == 2) mbar_init(smem_u32(counted), CL + (MC == 2 ? 1 : 0));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -753,9 +769,13 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
     return ti;
   };
 
-  auto give_up = [&]() {
-    *abort_flag = 1;
-    flag_error(p.flag, XT_DEVERR_TIMEOUT);
+  auto give_up = [&]() {  // every CTA of the cluster stops
+    if constexpr (CG == 2) {
+      cluster_give_up<CL>(smem_u32(const_cast<int*>(abort_flag)), p.flag);
+    } else {
+      *abort_flag = 1;
+      flag_error(p.flag, XT_DEVERR_TIMEOUT);
+    }
   };
 
   if (warp == 0) {
@@ -826,10 +846,9 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
       }
-      // Wait (bounded) for the copies that may still be in flight: the last STAGES fills, so no TMA
-      // write lands in shared memory after a CTA exits.  A pair's full barriers live in the even CTA
-      // and count both CTAs' bytes: the even CTA waits for both, and the cluster barrier before exit
-      // keeps the odd CTA resident until then.  Multicast stages of B complete in every CTA.
+      // Wait (bounded) for the copies that may still be in flight: the last min(STAGES, issued)
+      // fills, so no TMA write lands in shared memory after the CTA exits.  In a cluster the MMA
+      // issuers (and relays) have waited for every fill unless a wait ran out: see the end.
       if constexpr (CG == 1) {
         const int pending = issued < STAGES ? issued : STAGES;
         for (int i = 0; i < pending; ++i) {
@@ -837,18 +856,7 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
           if (!mbar_wait(smem_u32(&full[stage]), phase)) { give_up(); break; }
         }
       } else {
-        cluster_tell(smem_u32(&counts[crank]), smem_u32(counted), issued, 0, MC == 2 ? CL : 1);
-        if (MC == 2 || rank == 0) {
-          uint32_t bytes[CL];
-#pragma unroll
-          for (int c = 0; c < CL; ++c)
-            bytes[c] = MC == 1 ? uint32_t(C_::STAGE_BYTES)
-                               : (rank == 0 && (c >> 1) == pidx ? uint32_t(C_::A_BYTES) : 0u) +
-                                     ((c & 1) == rank ? uint32_t(C_::B_BYTES / 2) : 0u);
-          if (!cluster_drain<CL, STAGES>(full, counted, counts, crank, issued, bytes,
-                                         MC == 2 && rank == 0 ? &counts[CL] : nullptr, p.wait_ns, abort_flag))
-            give_up();
-        }
+        counts[crank] = issued;
       }
     }
   } else if (warp == 1) {
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
         }
       }
       if (!ok) give_up();
-      cluster_tell(smem_u32(&counts[CL]), smem_u32(counted), relayed, leader, 2);
+      counts[CL] = relayed;
     }
   } else {
     // -------------------------------------------------------------------- epilogue
@@ -1378,7 +1386,11 @@ __global__ void __launch_bounds__(threads_of(ACT), 1)
   __syncthreads();
   // a pair: neither CTA releases TMEM or exits while the other may still signal its barriers
   // or (the even CTA's MMAs) read its shared memory and write its TMEM
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (CG == 2) {
+    cluster_sync_all();
+    if (*abort_flag)  // in every CTA of the cluster alike: a give-up sets it in all of them before they come here
+      cluster_finish<STAGES, MC>(smem_u32(full), smem_u32(const_cast<int*>(counts)), C_::A_BYTES, C_::B_BYTES, p.flag);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<CG>(tbase, TCOLS);

@@ -116,9 +116,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
   uint64_t* mma_done = tfull + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* counted = tfull + 6;  // the pair's stages asked for, as its producers report them at the end
-  int* counts = reinterpret_cast<int*>(tfull + 7);
-  static_assert((2 * kStages + 7) * 8 + kCg * 4 <= 256, "room for the barriers");
+  volatile int* counts = reinterpret_cast<volatile int*>(tfull + 6);  // fills asked for by either CTA (see the end)
+  static_assert((2 * kStages + 6) * 8 + kCg * 4 <= 256, "room for the barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -130,7 +129,6 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
       mbar_init(smem_u32(&tempty[b]), kEpilogueWarps * kCg);
     }
     mbar_init(smem_u32(mma_done), 1);
-    if constexpr (kCg == 2) mbar_init(smem_u32(counted), 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -151,9 +149,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
   pdl_wait();
   pdl_trigger();
 
-  auto give_up = [&]() {
-    *abort_flag = 1;
-    flag_error(a.flag, XT_DEVERR_TIMEOUT);
+  auto give_up = [&]() {  // both CTAs of a pair stop
+    if constexpr (kCg == 2) {
+      cluster_give_up<2>(smem_u32(const_cast<int*>(abort_flag)), a.flag);
+    } else {
+      *abort_flag = 1;
+      flag_error(a.flag, XT_DEVERR_TIMEOUT);
+    }
   };
 
   if (warp == 0) {
@@ -191,17 +193,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
       }
-      // copies that may still be in flight land before a CTA exits (both CTAs' bytes are counted in the even one)
+      // copies that may still be in flight land before the CTA exits (in a pair the MMA issuer has waited for every fill
+      // unless a wait ran out: see the end)
       if constexpr (kCg == 1) {
         for (int i = 0; i < kStages && i < issued; ++i) {
           if (--stage < 0) { stage = kStages - 1; phase ^= 1; }
           if (!mbar_wait(smem_u32(&full[stage]), phase)) { give_up(); break; }
         }
       } else {
-        cluster_tell(smem_u32(&counts[rank]), smem_u32(counted), issued, 0, 1);
-        const uint32_t bytes[2] = {kStageBytes, kStageBytes};
-        if (rank == 0 && !cluster_drain<2, kStages>(full, counted, counts, rank, issued, bytes, nullptr, a.wait_ns, abort_flag))
-          give_up();
+        counts[rank] = issued;
       }
     }
   } else if (warp == 1) {
@@ -371,7 +371,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) muon_product_kernel(const 
   }
   __syncthreads();
   // neither CTA releases tensor memory or exits while the other may still signal its barriers or read its operands
-  if constexpr (kCg == 2) cluster_sync_all();
+  if constexpr (kCg == 2) {
+    cluster_sync_all();
+    if (*abort_flag)  // in both alike; as in the GEMM, every copy that either CTA asked for lands before one of them exits
+      cluster_finish<kStages, 1>(smem_u32(full), smem_u32(const_cast<int*>(counts)), kOperandBytes, kOperandBytes, a.flag);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<kCg>(tbase, 2 * kTile);
