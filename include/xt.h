@@ -408,7 +408,7 @@ int xt_cross_entropy_bwd(const void* logits, const int32_t* targets, const float
  * are allowed, those of the type's lowest value among them.  A token outside [0, V) sets XT_DEVERR_INDEX and makes logp and the gradient of its row NaN.
  * Layout: row r of logits at logits + r·ld (ld ≥ V), dlogits likewise with ld_d; dlogits may be logits (one dtype
  * and stride, acc = 0).  Any alignment of the element type; rows of aligned 16 bytes need no more than that.
- * scale in [1e-6, 1e6].  Entropies are accurate to about 1e-6 absolute.  Deterministic.
+ * scale in [1e-6, 1e6].  No log probability is above 0.  Entropies are accurate to about 1e-6 absolute.  Deterministic.
  * ------------------------------------------------------------------------------- */
 int xt_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens, float scale, int top, float* logp,
                           float* entropy, float* stats, float* top_logp, int32_t* top_ids, int64_t rows, int64_t V,

@@ -313,6 +313,13 @@ __device__ __forceinline__ void warp_join(float& b, float& s, float& w) {
   b = B;
 }
 
+// log2 Σ 2^(c(x − M)) of sums to the base b.  The largest element's own term is 1, so it is nought at least: what the
+// exponential rounded off would leave probabilities above 1.  (NaN stays.)
+__device__ __forceinline__ double log2_sum(float b, float s, float M, float c) {
+  const double l = double(log2f(s)) + (double(b) - double(M) * double(c));
+  return l < 0 ? 0 : l;
+}
+
 // WARP: a warp to a row (short rows); else a CTA, or with gridDim.x a multiple of the cluster size a cluster of CTAs
 // that share the row's vectors out in ranges and join in the first one's shared memory.
 template <typename T, bool TOP, bool WARP>
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
   uint64_t list = 0;
 
   if constexpr (WARP) {
-    double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
+    double log2s = log2_sum(b, s, M, a.c);
     double mean = double(w / s) + (double(b) - double(M) * double(a.c));
     if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
     if (lane == 0) write_row(a, r, valid, given, M, log2s, mean);
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
   }
   M = warp_max(M);
   warp_join(b, s, w);
-  double log2s = double(log2f(s)) + (double(b) - double(M) * double(a.c));
+  double log2s = log2_sum(b, s, M, a.c);
   double mean = double(w / s) + (double(b) - double(M) * double(a.c));
   if (!(s > 0.f && s < FLT_MAX) || !isfinite(M) || !isfinite(w)) row_safe(x, a.V, a.scale, lane, M, log2s, mean);
   if (lane == 0) write_row(a, r, valid, given, M, log2s, mean);
