@@ -39,6 +39,23 @@ def runs_out_and_recovers(run, repeats=3):
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def runs_out_somewhere(run, limits=(200, 500, 1000, 2000, 4000, 8000)):
+    """Limits within which some waits end and others do not: the CTAs stop at fills of their own in the middle of the work."""
+    want = run()
+    for limit in limits:
+        xt.set_wait_limit_ns(limit)
+        t0 = time.perf_counter()
+        got = run()
+        assert time.perf_counter() - t0 < 1.0
+        if xt.device_errors() == 0:
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+        xt.set_wait_limit_ns(0)
+        xt.clear_device_errors()
+        got = run()
+        assert xt.device_errors() == 0
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def kinds(fn):
     """Tile-width code of every product that fn launches: 1000 and more are pairs'."""
     xt.profile_gemm(16)
@@ -67,6 +84,7 @@ def test_gemm(pairing, short_waits):
     codes = kinds(run)
     assert len(codes) == 1 and codes[0] >= 1000
     runs_out_and_recovers(run)
+    runs_out_somewhere(run)
 
 
 def test_gated_block(short_waits):
@@ -85,6 +103,7 @@ def test_gated_block(short_waits):
         return gu, h, dgu, dw
     assert kinds(run)[:2] == [1256, 1256]
     runs_out_and_recovers(run)
+    runs_out_somewhere(run)
 
 
 def test_muon(short_waits):
@@ -99,3 +118,4 @@ def test_muon(short_waits):
         torch.cuda.synchronize()
         return (*p, *m)
     runs_out_and_recovers(run)
+    runs_out_somewhere(run)
